@@ -69,6 +69,9 @@ typedef struct CUstream_st* spec_stream_t;
 #define SPEC_DEVERR_TIMEOUT 32     /* an asynchronous copy did not arrive        */
 #define SPEC_DEVERR_MODE 64        /* mode not 0/1                               */
 #define SPEC_DEVERR_POOL_ROW 128   /* state-pool row index outside the pool      */
+#define SPEC_DEVERR_TREE 256       /* parents do not describe a tree             */
+#define SPEC_DEVERR_NO_PAGE 512    /* no free page left for a row                */
+#define SPEC_DEVERR_SRC_ROW 1024   /* source row outside [-1, B)                 */
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* spec_status_string(int status);
@@ -405,6 +408,201 @@ int spec_gdn_verify_pooled(const float* q, const float* k, const float* v, const
                            int32_t batch, int32_t num_tokens, int32_t num_heads, int32_t dk,
                            int32_t dv, int32_t num_slots, int32_t alignment, int32_t* dev_err,
                            spec_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 5. Tree speculation: verify attention over a tree of drafts                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A tree step drafts several candidates per position. Its num_nodes = N nodes
+ * of a sequence are described by `parents` [B, N] int32:
+ *
+ *   parents[b, i] = j, 0 <= j < i   node i is a child of node j
+ *   parents[b, i] = SPEC_TREE_ROOT  node i has no parent (node 0 always)
+ *   parents[b, i] = SPEC_TREE_UNUSED  no node: the slot is padding
+ *
+ * Node 0 is the last committed token, as row 0 of a chain step is; the chain is
+ * the tree parents[b, i] = i - 1. A child of an unused node, a parent outside
+ * [-2, i) or a node 0 with a parent is no tree (SPEC_DEVERR_TREE). A sequence
+ * whose node 0 is unused is an empty row of a padded batch: its other inputs
+ * are not looked at, and no error is set for it.
+ */
+#define SPEC_TREE_ROOT (-1)
+#define SPEC_TREE_UNUSED (-2)
+
+#define SPEC_DTYPE_BF16 0
+#define SPEC_DTYPE_FP16 1
+#define SPEC_DTYPE_FP32 2
+
+/*
+ * out[b, i, h, :] = softmax_t( q[b,i,h,:] . K[b,t,g,:] / sqrt(D) ) . V[b,t,g,:]
+ * for node i of sequence b and query head h, g = h / G, over the committed
+ * tokens t < base = ctx_lens[b] - N and over t = base + j for node i itself and
+ * its ancestors j. Rows of unused nodes are zeros.
+ *
+ *  q           [B, N, Hq, D] of type `dtype` (SPEC_DTYPE_BF16 or _FP16)
+ *  k_cache     [num_blocks, bs, Hkv, D] of type `dtype`; node j's K and V are in
+ *  v_cache     the cache at token base + j. Slots of unused nodes and slots at
+ *              or past ctx_lens[b] may hold anything, NaN included; a NaN or
+ *              infinity in the V of any other slot may reach every row of the
+ *              sequence.
+ *  block_table [B, max_blocks_per_seq] int32
+ *  ctx_lens    [B] int32, tokens in the cache, the N tree slots included; must
+ *              lie in [N, max_blocks_per_seq * bs]
+ *  parents     [B, N] int32
+ *  out         [B, N, Hq, D] of type `out_dtype`: fp32, or `dtype`
+ *  workspace   >= spec_tree_attention_workspace(d, N) bytes, 256-byte aligned,
+ *              ZERO-FILLED before its first use; reusable by later calls on the
+ *              same stream (two calls in flight at once, or two captured graphs
+ *              that may run at once, need two workspaces).
+ *
+ * Device errors: a sequence with an out-of-range ctx_len (SPEC_DEVERR_CTX_LEN),
+ * block id (SPEC_DEVERR_BLOCK_ID) or tree (SPEC_DEVERR_TREE) gets out rows of
+ * zeros. Device pointers 16-byte aligned.
+ * Supported: D in {64,128,256}; bs in {16,32,64,128}; N <= 64; G <= 128;
+ * B <= 4096.
+ */
+size_t spec_tree_attention_workspace(const spec_attn_desc* d, int32_t num_nodes);
+
+int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_table, const int32_t* ctx_lens,
+                        const int32_t* parents, int32_t num_nodes, void* out, int32_t dtype,
+                        int32_t out_dtype, const spec_attn_desc* d, void* workspace,
+                        size_t workspace_bytes, int32_t* dev_err, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 6. Tree speculation: acceptance                                            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Walks the tree of each sequence from node 0. At node n:
+ *
+ *  Greedy rows (mode[b] == SPEC_MODE_GREEDY): a = argmax_v target_logits[b,n,v]
+ *  (lowest index on ties). The first child (lowest node index) whose token is a
+ *  is accepted and the walk goes on there; without one, a is emitted last.
+ *
+ *  Sampling rows (mode[b] == SPEC_MODE_SAMPLE), T = temperature[b] > 0:
+ *  p = softmax(target_logits[b,n,:] / T). The children c of n are tried in
+ *  increasing node index against the residual r, at first r = p:
+ *    with draft_probs: q = draft_probs[b,n,:], the distribution every child of n
+ *      was drawn from independently. c is accepted iff u_c q(x_c) < r(x_c);
+ *      else r <- max(0, r - q) / sum.
+ *    without (NULL): the children are deterministic. c is accepted iff
+ *      u_c < r(x_c); else r <- r with x_c removed, normalised.
+ *    A residual that would be all zero stays as it was.
+ *  If no child is accepted, the last token is drawn from r by the exponential
+ *  race of spec_accept.
+ *
+ *  Random numbers as in spec_accept with the node index in place of the
+ *  position: u_c uses word 0 of counter (0, c - 1, b, 0), the race at node n
+ *  counter (x / 4, n, b, 1). On a chain the call computes what spec_accept does.
+ *
+ *  target_logits [B, N, V] fp32, row n the target's logits after node n
+ *  tokens        [B, N] int32; the token of node n (node 0's is not looked at)
+ *  parents       [B, N] int32; nodes other than 0 without a parent are never
+ *                reached
+ *  draft_probs   [B, N, V] fp32 or NULL; rows of nodes without children are not
+ *                read
+ *  mode          [B] int32; temperature [B] fp32 (ignored for greedy rows)
+ *  out_tokens    [B, N] int32: the accepted nodes' tokens, the last token, -1s
+ *  path          [B, N] int32: 0, the accepted nodes in order, -1s
+ *  accept_len    [B] int32: accepted nodes, node 0 not counted
+ *
+ * Rows are read only along the accepted path.
+ * Device errors: a row with a used node's token outside [0, V)
+ * (SPEC_DEVERR_TOKEN), a bad tree (SPEC_DEVERR_TREE), mode (SPEC_DEVERR_MODE) or
+ * temperature (SPEC_DEVERR_TEMPERATURE), and an empty row of a padded batch (no
+ * error), get out_tokens and path all -1 and accept_len -1.
+ * Supported: N <= 64; vocab <= 2^30.
+ */
+int spec_tree_accept(const float* target_logits, const int32_t* tokens, const int32_t* parents,
+                     const float* draft_probs, uint64_t philox_seed, const int32_t* mode,
+                     const float* temperature, int32_t* out_tokens, int32_t* path,
+                     int32_t* accept_len, int32_t batch, int32_t num_nodes, int32_t vocab,
+                     int32_t* dev_err, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 7. The paged cache between two steps                                       */
+/* ------------------------------------------------------------------------ */
+
+/* A cache of num_layers layers, [num_layers, num_blocks, block_size, token_bytes]
+ * each for K and V, whose pages the rows of one block table name. */
+typedef struct spec_cache_desc {
+  int32_t batch;              /* B: rows of the block table                      */
+  int32_t num_layers;         /* L                                               */
+  int32_t block_size;         /* tokens per page, 1 to 65536                     */
+  int32_t max_blocks_per_seq; /* row stride of block_table                       */
+  int64_t num_blocks;         /* pages                                           */
+  int64_t token_bytes;        /* bytes of one token's K (or V) in one layer      */
+} spec_cache_desc;
+
+/*
+ * Keeps the accepted path of a tree step: in every layer, K and V of token
+ * base + path[b, j] move to token base + j, j = 1 .. accept_len[b], in place,
+ * base = ctx_lens[b] - N; the rest of the cache is left as it is.
+ * new_lens[b] = base + accept_len[b] + 1, the row's committed tokens.
+ *
+ *  block_table [B, max_blocks_per_seq] int32; ctx_lens [B] int32
+ *  path [B, N] int32 and accept_len [B] int32 as written by spec_tree_accept
+ *  new_lens [B] int32, not overlapping ctx_lens
+ *
+ * A row with accept_len -1 moves nothing and gets new_lens = max(0, base).
+ * Device errors, with the same treatment: accept_len outside [-1, N - 1] or a
+ * path that does not increase from 0 within [0, N) (SPEC_DEVERR_ACCEPT_LEN), a
+ * ctx_len outside [N, max_blocks_per_seq * block_size] (SPEC_DEVERR_CTX_LEN), a
+ * page outside [0, num_blocks) (SPEC_DEVERR_BLOCK_ID). Rows must not share the
+ * pages of their tree slots. Supported: N <= 64; L * B <= 2^31 - 1.
+ */
+int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_t* block_table,
+                           const int32_t* ctx_lens, const int32_t* path,
+                           const int32_t* accept_len, int32_t* new_lens, int32_t num_nodes,
+                           const spec_cache_desc* d, int32_t* dev_err, spec_stream_t stream);
+
+/*
+ * Gives every row of the block table the pages for new_lens[b] tokens, on the
+ * device: trims, reserves, frees, forks and reorders rows in one call.
+ *
+ *  block_table [B, max_blocks_per_seq] int32, in place; -1 means no page
+ *  page_refs   [num_blocks] int32, in place: how many table entries (and other
+ *              holders) name the page; a page with 0 is free
+ *  cur_lens    [B] int32: tokens the rows hold; new_lens [B] int32: tokens they
+ *              shall have room for
+ *  src_rows    [B] int32 or NULL: the row b continues from: b itself (NULL: all
+ *              rows do), another row (a fork, or a beam's reordering), or -1 to
+ *              free the row
+ *
+ * With s = src_rows[b], row b keeps the first keep = min(cur_lens[s], new_lens[b])
+ * tokens of row s. Entry i of the new row, for i < ceil(new_lens[b] / bs):
+ *   - a page wholly inside the kept tokens is shared;
+ *   - any other page of row s stays with the row that continues s (s itself if
+ *     src_rows[s] == s, else the lowest b with that source), if no other holder
+ *     has it (page_refs is 1 at entry);
+ *   - else a free page is taken, and the kept tokens that the old page holds
+ *     are copied into it, K and V of every layer.
+ * Entries behind are -1. References are counted again, and pages that reach 0
+ * are free at once (one that is copied from, after the call). Free pages are
+ * handed out lowest index first, in the order of rows and entries, so the result
+ * does not depend on timing.
+ *
+ *  k_cache, v_cache: both, or both NULL (then num_layers and token_bytes are not
+ *              looked at and nothing is copied: for callers whose rows never
+ *              share partly filled pages)
+ *  workspace   >= spec_cache_update_workspace(d) bytes, 256-byte aligned, no
+ *              initial contents needed; one call at a time
+ *
+ * Device errors: a row with a source outside [-1, B) (SPEC_DEVERR_SRC_ROW), a
+ * length outside [0, max_blocks_per_seq * bs] (SPEC_DEVERR_CTX_LEN), or a kept
+ * token in an entry outside [0, num_blocks) (SPEC_DEVERR_BLOCK_ID) keeps its
+ * entries as they are. Entries that find no free page are -1
+ * (SPEC_DEVERR_NO_PAGE). Supported: B * max_blocks_per_seq <= 2^30;
+ * num_blocks <= 2^30.
+ */
+size_t spec_cache_update_workspace(const spec_cache_desc* d);
+
+int spec_cache_update(int32_t* block_table, int32_t* page_refs, const int32_t* cur_lens,
+                      const int32_t* new_lens, const int32_t* src_rows, void* k_cache,
+                      void* v_cache, const spec_cache_desc* d, void* workspace,
+                      size_t workspace_bytes, int32_t* dev_err, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,14 @@ library is missing, calls raise.
     spec_accept(target_logits, draft_tokens, draft_probs, philox_seed, mode,
                 temperature, out_tokens, accept_len)
     spec_commit_state(snapshots, accept_len, live_state)
+
+and, for a tree of drafts instead of a chain:
+
+    spec_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, parents, out)
+    spec_tree_accept(target_logits, tokens, parents, draft_probs, philox_seed, mode,
+                     temperature, out_tokens, path, accept_len)
+    spec_cache_commit_path(k_cache, v_cache, block_table, ctx_lens, path, accept_len, new_lens)
+    spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size)
 """
 
 from __future__ import annotations
@@ -29,14 +37,16 @@ __all__ = [
     "spec_verify_attention_plan",
     "spec_accept", "spec_commit_state", "spec_commit_state_aligned", "spec_commit_select", "spec_gdn_verify",
     "spec_gdn_verify_pooled", "status_string",
-    "DEVERR", "MODE_GREEDY", "MODE_SAMPLE", "ALIGN_TOKEN", "ALIGN_LAST",
+    "spec_tree_attention", "spec_tree_attention_workspace", "spec_tree_accept", "spec_cache_commit_path",
+    "spec_cache_update", "spec_cache_update_workspace",
+    "DEVERR", "MODE_GREEDY", "MODE_SAMPLE", "ALIGN_TOKEN", "ALIGN_LAST", "TREE_ROOT", "TREE_UNUSED",
 ]
 
 MODE_GREEDY = 0
 MODE_SAMPLE = 1
 DEVERR = {
     "block_id": 1, "token": 2, "accept_len": 4, "ctx_len": 8, "temperature": 16,
-    "timeout": 32, "mode": 64, "pool_row": 128,
+    "timeout": 32, "mode": 64, "pool_row": 128, "tree": 256, "no_page": 512, "src_row": 1024,
 }
 
 _lock = threading.Lock()
@@ -66,6 +76,17 @@ class _AttnDesc(ctypes.Structure):
         ("block_size", ctypes.c_int32),
         ("max_blocks_per_seq", ctypes.c_int32),
         ("num_blocks", ctypes.c_int64),
+    ]
+
+
+class _CacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_layers", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int64),
+        ("token_bytes", ctypes.c_int64),
     ]
 
 
@@ -116,6 +137,18 @@ def load_library():
         lib.spec_gdn_verify_pooled.argtypes = [P, P, P, P, P, ctypes.c_float, P, i64, P, P, P, i32, i32, i32, i32,
                                                 i32, i32, i32, P, P]
         lib.spec_gdn_verify_pooled.restype = ctypes.c_int
+        lib.spec_tree_attention_workspace.argtypes = [ctypes.POINTER(_AttnDesc), i32]
+        lib.spec_tree_attention_workspace.restype = sz
+        lib.spec_tree_attention.argtypes = [P, P, P, P, P, P, i32, P, i32, i32, ctypes.POINTER(_AttnDesc), P, sz, P, P]
+        lib.spec_tree_attention.restype = ctypes.c_int
+        lib.spec_tree_accept.argtypes = [P, P, P, P, u64, P, P, P, P, P, i32, i32, i32, P, P]
+        lib.spec_tree_accept.restype = ctypes.c_int
+        lib.spec_cache_commit_path.argtypes = [P, P, P, P, P, P, P, i32, ctypes.POINTER(_CacheDesc), P, P]
+        lib.spec_cache_commit_path.restype = ctypes.c_int
+        lib.spec_cache_update_workspace.argtypes = [ctypes.POINTER(_CacheDesc)]
+        lib.spec_cache_update_workspace.restype = sz
+        lib.spec_cache_update.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(_CacheDesc), P, sz, P, P]
+        lib.spec_cache_update.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -389,3 +422,168 @@ def spec_gdn_verify_pooled(q, k, v, g, beta, pool, live_row, ckpt_rows, out, sca
                                     int(alignment), _err_ptr(dev_err), _stream_handle(stream))
     _check("spec_gdn_verify_pooled", rc)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Tree speculation
+# ---------------------------------------------------------------------------
+TREE_ROOT, TREE_UNUSED = -1, -2
+
+_DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _is(t, dtype, shape, dev: int) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev \
+        and t.shape == shape and t.is_contiguous()
+
+
+def _need_shape(t, name: str, dtype, shape, dev: int):
+    """A contiguous CUDA tensor of this type and shape on the current device `dev`."""
+    if not _is(t, dtype, shape, dev):
+        _need(t, name, dtype, len(shape))
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def spec_tree_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor) -> int:
+    """Workspace bytes spec_tree_attention needs for these shapes (zero-filled before its first use:
+    new_attention_workspace)."""
+    d = _attn_desc(q, k_cache, block_table)
+    return int(load_library().spec_tree_attention_workspace(ctypes.byref(d), int(q.shape[1])))
+
+
+def spec_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, parents, out,
+                        workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of the N tree nodes of every sequence over a paged cache into `out` [B, N, Hq, D] (see
+    spec_verify.h). q and the caches are bf16 or fp16; out is fp32 or of their type."""
+    lib = load_library()
+    dev = torch.cuda.current_device()
+    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be a bfloat16 or float16 tensor")
+    _need(q, "q", q.dtype, 4)
+    _need(k_cache, "k_cache", q.dtype, 4)
+    _need_shape(v_cache, "v_cache", q.dtype, k_cache.shape, dev)
+    B, N, _, _ = q.shape
+    _need(block_table, "block_table", torch.int32, 2)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    _need_shape(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    _need_shape(parents, "parents", torch.int32, (B, N), dev)
+    if not isinstance(out, torch.Tensor) or out.dtype not in (q.dtype, torch.float32):
+        raise ValueError(f"out must be a float32 or {q.dtype} tensor")
+    _need_shape(out, "out", out.dtype, q.shape, dev)
+    d = _attn_desc(q, k_cache, block_table)
+    if workspace is None:
+        workspace = new_attention_workspace(int(lib.spec_tree_attention_workspace(ctypes.byref(d), N)), q.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    rc = lib.spec_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                 ctx_lens.data_ptr(), parents.data_ptr(), N, out.data_ptr(), _DTYPE_CODES[q.dtype],
+                                 _DTYPE_CODES[out.dtype], ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
+                                 _err_ptr(dev_err), _stream_handle(stream))
+    _check("spec_tree_attention", rc)
+    return out
+
+
+def spec_tree_accept(target_logits, tokens, parents, draft_probs, philox_seed: int, mode, temperature, out_tokens, path,
+                     accept_len, dev_err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Walk of every row's tree, greedy or by speculative sampling (see spec_verify.h)."""
+    lib = load_library()
+    dev = torch.cuda.current_device()
+    _need(target_logits, "target_logits", torch.float32, 3)
+    B, N, V = target_logits.shape
+    _need_shape(tokens, "tokens", torch.int32, (B, N), dev)
+    _need_shape(parents, "parents", torch.int32, (B, N), dev)
+    if draft_probs is not None:
+        _need_shape(draft_probs, "draft_probs", torch.float32, (B, N, V), dev)
+    _need_shape(mode, "mode", torch.int32, (B,), dev)
+    _need_shape(temperature, "temperature", torch.float32, (B,), dev)
+    _need_shape(out_tokens, "out_tokens", torch.int32, (B, N), dev)
+    _need_shape(path, "path", torch.int32, (B, N), dev)
+    _need_shape(accept_len, "accept_len", torch.int32, (B,), dev)
+    rc = lib.spec_tree_accept(target_logits.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
+                              None if draft_probs is None else draft_probs.data_ptr(),
+                              int(philox_seed) & 0xFFFFFFFFFFFFFFFF, mode.data_ptr(), temperature.data_ptr(),
+                              out_tokens.data_ptr(), path.data_ptr(), accept_len.data_ptr(), B, N, V,
+                              _err_ptr(dev_err), _stream_handle(stream))
+    _check("spec_tree_accept", rc)
+    return out_tokens, path, accept_len
+
+
+def _need_caches(k_cache, v_cache, dev: int):
+    """K and V caches [num_layers, num_blocks, bs, Hkv, D], or one layer's without the first dimension, of any type:
+    (layers, pages, page size, bytes of a token)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() not in (4, 5):
+        raise ValueError("k_cache must be a tensor [num_layers, num_blocks, block_size, heads, head_dim] "
+                         "or [num_blocks, block_size, heads, head_dim]")
+    _need(k_cache, "k_cache", k_cache.dtype, k_cache.dim())
+    _need_shape(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    pages, page, heads, dim = k_cache.shape[-4:]
+    return layers, pages, page, heads * dim * k_cache.element_size()
+
+
+def spec_cache_commit_path(k_cache, v_cache, block_table, ctx_lens, path, accept_len, new_lens,
+                           dev_err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Move the accepted path's K and V to consecutive tokens, in place and in every layer, and write the rows' new
+    lengths (see spec_verify.h)."""
+    lib = load_library()
+    dev = torch.cuda.current_device()
+    layers, pages, page, token_bytes = _need_caches(k_cache, v_cache, dev)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(path, "path", torch.int32, 2)
+    B, N = path.shape
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    _need_shape(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    _need_shape(accept_len, "accept_len", torch.int32, (B,), dev)
+    _need_shape(new_lens, "new_lens", torch.int32, (B,), dev)
+    d = _CacheDesc(B, layers, page, block_table.shape[1], pages, token_bytes)
+    rc = lib.spec_cache_commit_path(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(),
+                                    path.data_ptr(), accept_len.data_ptr(), new_lens.data_ptr(), N, ctypes.byref(d),
+                                    _err_ptr(dev_err), _stream_handle(stream))
+    _check("spec_cache_commit_path", rc)
+    return new_lens
+
+
+def spec_cache_update_workspace(block_table: torch.Tensor, page_refs: torch.Tensor) -> int:
+    """Workspace bytes spec_cache_update needs for a table and a cache of these sizes."""
+    d = _CacheDesc(block_table.shape[0], 0, 1, block_table.shape[1], page_refs.shape[0], 1)
+    return int(load_library().spec_cache_update_workspace(ctypes.byref(d)))
+
+
+def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: int,
+                      src_rows: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                      v_cache: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      dev_err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Trim, reserve, free, fork and reorder rows of the page table on the device (see spec_verify.h):
+    block_table [B, W] and page_refs [num_blocks] are updated in place, partly filled pages are copied in the
+    caches, if given."""
+    lib = load_library()
+    dev = torch.cuda.current_device()
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(page_refs, "page_refs", torch.int32, 1)
+    B, W = block_table.shape
+    _need_shape(cur_lens, "cur_lens", torch.int32, (B,), dev)
+    _need_shape(new_lens, "new_lens", torch.int32, (B,), dev)
+    if src_rows is not None:
+        _need_shape(src_rows, "src_rows", torch.int32, (B,), dev)
+    d = _CacheDesc(B, 0, int(block_size), W, page_refs.shape[0], 1)
+    if (k_cache is None) != (v_cache is None):
+        raise ValueError("k_cache and v_cache go together")
+    if k_cache is not None:
+        layers, pages, page, token_bytes = _need_caches(k_cache, v_cache, dev)
+        if pages != page_refs.shape[0] or page != block_size:
+            raise ValueError(f"caches of {pages} pages of {page} tokens do not fit {page_refs.shape[0]} page_refs "
+                             f"and block_size {block_size}")
+        d.num_layers, d.token_bytes = layers, token_bytes
+    if workspace is None:
+        workspace = torch.empty(int(lib.spec_cache_update_workspace(ctypes.byref(d))), dtype=torch.uint8,
+                                device=block_table.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    rc = lib.spec_cache_update(block_table.data_ptr(), page_refs.data_ptr(), cur_lens.data_ptr(), new_lens.data_ptr(),
+                               None if src_rows is None else src_rows.data_ptr(),
+                               None if k_cache is None else k_cache.data_ptr(),
+                               None if v_cache is None else v_cache.data_ptr(), ctypes.byref(d), workspace.data_ptr(),
+                               workspace.numel(), _err_ptr(dev_err), _stream_handle(stream))
+    _check("spec_cache_update", rc)
+    return block_table, page_refs
