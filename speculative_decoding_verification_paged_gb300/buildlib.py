@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
-SOURCES = ["attention.cu", "accept.cu", "commit.cu", "gdn.cu", "tree_attention.cu", "tree_accept.cu", "cache_pages.cu"]
+SOURCES = ["attention.cu", "accept.cu", "commit.cu", "gdn.cu", "tree_attention.cu", "tree_attention_d64.cu",
+           "tree_attention_d128.cu", "tree_attention_d256.cu", "tree_accept.cu", "cache_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

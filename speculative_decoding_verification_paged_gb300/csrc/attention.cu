@@ -55,6 +55,7 @@
 #include "attention_mma.cuh"
 #include "attention_tc.cuh"
 #include "launch_memo.h"
+#include "tensor_map.h"
 
 namespace specv {
 namespace attn {
@@ -95,25 +96,6 @@ static Layout layout_for(const spec_attn_desc* d, int k_draft) {
   L.opart_off = L.lse_off + align256((size_t)(slots * n_rows * 4));
   L.total = L.opart_off + align256((size_t)(slots * n_rows * d->head_dim * 4));
   return L;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Resolved once per process (a function-local static is initialised exactly
-// once even when several host threads arrive together).
-static EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(ptr);
-  }();
-  return fn;
 }
 
 // A bf16 3-D view {x: 64-wide slice of D, y: head, z: token row} with 128-byte swizzle.

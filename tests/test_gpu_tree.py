@@ -236,6 +236,36 @@ def test_attention_reuses_its_workspace(sv):
     check_attention(a, first[0])
 
 
+@pytest.mark.parametrize("case", [(12, 3000, 16, 32, 8, 128, "same"), (30, 1024, 16, 32, 8, 128, "same"),
+                                  (8, 2048, 64, 32, 8, 128, "same"), (16, 2000, 40, 32, 8, 64, "f32"),
+                                  (16, 2000, 16, 32, 8, 128, "f32"), (16, 1500, 16, 24, 4, 256, "f32")])
+def test_attention_repeats_bit_for_bit_from_cold_memory(sv, case):
+    """Every other call starts with the caches out of L2, so tiles land late and out of order; the calls before the
+    check run back to back or one at a time."""
+    B, longest, N, H, K, D, out = case
+    g = torch.Generator(device=DEV).manual_seed(B)
+    ctx = torch.randint(N, longest + 1, (B,), generator=g, device=DEV).int()
+    W = -(-longest // 64)
+    table = torch.randperm(B * W, generator=g, device=DEV).int().view(B, W)
+    k, v = (torch.randn((B * W, 64, K, D), generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn((B, N, H, D), generator=g, device=DEV, dtype=torch.bfloat16)
+    par = cuda(random_trees(np.random.default_rng(B), B, N))
+    outs = [torch.empty((B, N, H, D), device=DEV, dtype=torch.float32 if out == "f32" else q.dtype) for _ in range(2)]
+    ws = sv.new_attention_workspace(sv.spec_tree_attention_workspace(q, k, table), DEV)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device=DEV)
+    sv.spec_tree_attention(q, k, v, table, ctx, par, outs[0], workspace=ws)
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(300):
+        outs[1].fill_(float("nan"))
+        if i % 2:
+            flush.fill_(i % 251)
+        if i % 4 > 1:
+            torch.cuda.synchronize()
+        sv.spec_tree_attention(q, k, v, table, ctx, par, outs[1], workspace=ws)
+        differ += (outs[0] != outs[1]).sum()
+    assert int(differ) == 0
+
+
 def test_attention_on_other_streams_and_in_graphs(sv):
     """Two captured graphs with a workspace each, replayed at once on two streams with new inputs."""
     rng = np.random.default_rng(7)
