@@ -37,11 +37,18 @@ static bool shape_supported(const spec_attn_desc* d, int nodes) {
 struct Rows {
   int mt, groups, npt;
 };
-static Rows rows_for(const spec_attn_desc* d, int nodes) {
+static int streams_for(int D, int terms) {  // accumulators of the instance
+  switch (D) {
+    case 64: return terms == 3 ? Cfg<64, 1, 3, false>::STREAMS : Cfg<64, 1, 1, false>::STREAMS;
+    case 128: return terms == 3 ? Cfg<128, 1, 3, false>::STREAMS : Cfg<128, 1, 1, false>::STREAMS;
+    default: return terms == 3 ? Cfg<256, 1, 3, false>::STREAMS : Cfg<256, 1, 1, false>::STREAMS;
+  }
+}
+static Rows rows_for(const spec_attn_desc* d, int nodes, int terms) {
   const int most = kRows / (d->num_q_heads / d->num_kv_heads);
   const int tiles = (nodes + most - 1) / most;
   Rows r;
-  r.mt = (tiles > 1 && d->head_dim <= 128) ? 2 : 1;
+  r.mt = tiles > 1 ? streams_for(d->head_dim, terms) : 1;
   r.groups = (tiles + r.mt - 1) / r.mt;
   r.npt = (nodes + r.mt * r.groups - 1) / (r.mt * r.groups);
   return r;
@@ -50,9 +57,9 @@ static Rows rows_for(const spec_attn_desc* d, int nodes) {
 struct Layout {
   size_t lse, opart, total;
 };
-static Layout layout_for(const spec_attn_desc* d, int mt) {
+static Layout layout_for(const spec_attn_desc* d, int nodes) {
   Layout L;
-  const size_t slots = 2 * (size_t)kMaxGrid * mt;
+  const size_t slots = 2 * (size_t)kMaxGrid * rows_for(d, nodes, 1).mt;  // the most of any output type
   L.lse = attn::align256(kMaxGrid * sizeof(Split));
   L.opart = L.lse + attn::align256(slots * kRows * 4);
   L.total = L.opart + slots * kRows * d->head_dim * 4;
@@ -66,7 +73,7 @@ using namespace specv;
 
 extern "C" size_t spec_tree_attention_workspace(const spec_attn_desc* d, int32_t num_nodes) {
   if (!tattn::desc_ok(d, num_nodes) || !tattn::shape_supported(d, num_nodes)) return 0;
-  return tattn::layout_for(d, tattn::rows_for(d, num_nodes).mt).total;
+  return tattn::layout_for(d, num_nodes).total;
 }
 
 extern "C" int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -82,8 +89,7 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
        reinterpret_cast<uintptr_t>(out)) & 15)
     return SPEC_ERR_INVALID_ARG;
-  const tattn::Rows rows = tattn::rows_for(d, num_nodes);
-  const tattn::Layout L = tattn::layout_for(d, rows.mt);
+  const tattn::Layout L = tattn::layout_for(d, num_nodes);
   if (workspace == nullptr || workspace_bytes < L.total) return SPEC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return SPEC_ERR_INVALID_ARG;
 
@@ -91,6 +97,7 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   // bits of it (two fp16 parts, three bf16 ones).
   const bool fp16 = dtype == SPEC_DTYPE_FP16;
   const int D = d->head_dim, terms = out_dtype == SPEC_DTYPE_FP32 ? (fp16 ? 2 : 3) : 1;
+  const tattn::Rows rows = tattn::rows_for(d, num_nodes, terms);
   tattn::Launch l;
   int rc;
   switch (D) {
@@ -142,11 +149,15 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)p.heads, (cuuint64_t)num_nodes, (cuuint64_t)d->batch};
   const cuuint64_t qs[3] = {qd[0] * 2, qd[0] * qd[1] * 2, qd[0] * qd[1] * qd[2] * 2};
   const cuuint32_t qbox[4] = {64, (cuuint32_t)p.gqa, (cuuint32_t)p.npt, 1};
-  const int tk = tattn::tile_keys(D, terms);
-  const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)p.kv_heads, (cuuint64_t)d->num_blocks * d->block_size};
-  const cuuint64_t ks[2] = {kd[0] * 2, kd[0] * kd[1] * 2};
-  const cuuint32_t kbox[3] = {64, 1, (cuuint32_t)(d->block_size < tk ? d->block_size : tk)};
-  if (!map(&c.tq, q, 4, qd, qs, qbox) || !map(&c.tk, k_cache, 3, kd, ks, kbox) || !map(&c.tv, v_cache, 3, kd, ks, kbox))
+  // K and V [token rows][Hkv][D]: a box holds one head's rows of a page (or of a tile), 64 elements wide; where that is
+  // a whole tile, all of its slices, slice by slice
+  const int tk = D <= 128 ? 128 : 64;
+  const bool whole = d->block_size >= tk;
+  const cuuint64_t row_bytes = (cuuint64_t)p.kv_heads * D * 2;
+  const cuuint64_t kd[4] = {64, (cuuint64_t)d->num_blocks * d->block_size, (cuuint64_t)D / 64, (cuuint64_t)p.kv_heads};
+  const cuuint64_t ks[3] = {row_bytes, 128, (cuuint64_t)D * 2};
+  const cuuint32_t kbox[4] = {64, (cuuint32_t)(whole ? tk : d->block_size), whole ? (cuuint32_t)D / 64 : 1, 1};
+  if (!map(&c.tq, q, 4, qd, qs, qbox) || !map(&c.tk, k_cache, 4, kd, ks, kbox) || !map(&c.tv, v_cache, 4, kd, ks, kbox))
     return SPEC_ERR_LAUNCH;
   switch (D) {
     case 64: return tattn::launch<64>(rows.mt, terms, fp16, l, c);

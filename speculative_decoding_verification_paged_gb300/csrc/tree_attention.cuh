@@ -19,14 +19,13 @@ using attn::piece_slot;
 
 constexpr int kMaxGrid = 160;  // one CTA per SM, at most
 constexpr int kMaxSlots = 10;  // K and V tiles in shared memory
-constexpr int kMinSlots = 4;   // two of each
 constexpr int kTmemCols = 512;
-constexpr int kLaunchRegs = 168; // registers a thread that a kernel of 384 threads is launched with
-constexpr int kTables = 1024;  // bytes of shared memory for barriers and small tables
+constexpr int kLaunchRegs = 96;  // registers a thread that a kernel of 640 threads is launched with
+constexpr int kTables = 576;   // bytes of shared memory for barriers and small tables
 constexpr int kRows = 128;     // packed query rows of a row tile (MMA M)
-constexpr int kBarGroup = 1;   // named barriers: one per softmax warpgroup (1, 2),
+constexpr int kBarStream = 1;  // named barriers: the softmax threads of a stream (1, 2),
 constexpr int kBarSoftmax = 3; // all softmax threads,
-constexpr int kBarTail = 4;    // softmax threads and the issuing warps
+constexpr int kBarTail = 4;    // softmax threads and the issuing warp
 
 // What the merge needs of a unit cut over several CTAs; written by the CTA that holds its first piece.
 struct Split {
@@ -58,29 +57,37 @@ template <int D_, int MT_, int TERMS_, bool FP16_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_, TERMS = TERMS_;
   static constexpr bool FP16 = FP16_;
-  static constexpr bool DUAL = D <= 128;  // two accumulators and two softmax warpgroups
-  static constexpr int NWG = DUAL ? 2 : 1;
-  static constexpr int ISSUERS = NWG;  // threads that issue MMAs
-  static constexpr int TK = (D == 256 || TERMS == 3) ? 64 : 128;  // keys per tile
-  static constexpr int PW = TK / 2;                               // tensor-memory columns of one part of P
-  static constexpr int SW = TERMS * PW > TK ? TERMS * PW : TK;    // columns of an S / P buffer
-  static constexpr int QB = (DUAL && MT == 1) ? 2 : 1;            // query buffers
+  // Keys per tile. 128 keep the scores' MMAs at N = 128 (66 cycles each for 16 head dims; N = 64 takes 96); at D = 256
+  // two tiles of 128 keys would leave no room for a ring.
+  static constexpr int TK = D <= 128 ? 128 : 64;
+  static constexpr int PW = TK / 2;                             // tensor-memory columns of one part of P
+  static constexpr int SW = TERMS * PW > TK ? TERMS * PW : TK;  // columns of an S / P buffer
+  // Streams: accumulators, each with an S / P buffer and two softmax warpgroups, which work in turns with the tensor
+  // core. One accumulator with two buffers where two do not fit tensor memory.
+  static constexpr int STREAMS = 2 * (SW + D) <= kTmemCols ? 2 : 1;
+  static constexpr int NB = STREAMS == 2 ? 1 : 2;  // S / P buffers a stream
+  static constexpr int BUFS = 2;
+  static constexpr int AHEAD = BUFS / MT;  // tiles whose scores are issued before a tile's product
+  static constexpr bool JOIN = STREAMS == 2 && MT == 1;  // two accumulators hold the same rows
+  static constexpr int CW = TK / 2;                      // keys of a softmax thread
   static constexpr int SUBS = D / 64;
   static constexpr int Q_TILE = kRows * D * 2;
   static constexpr int Q_BYTES = MT * Q_TILE;
   static constexpr int SLOT = TK * D * 2;
-  static constexpr int kThreads = 128 + 128 * NWG;
-  static constexpr int COL_O = 2 * SW;
-  static constexpr int ML_BYTES = (DUAL && MT == 1) ? 2 * kRows * 8 : 0;  // (max, sum) of both warpgroups' rows
-  static_assert(MT == 1 || DUAL, "two row tiles need two accumulators");
-  static_assert(COL_O + NWG * D <= kTmemCols, "S / P buffers and accumulators fit tensor memory");
-  static_assert(TERMS >= 1 && TERMS <= 3, "");
+  static constexpr int kSoftmaxThreads = 256 * STREAMS;
+  static constexpr int kThreads = 128 + kSoftmaxThreads;
+  static constexpr int COL_O = BUFS * SW;
+  static constexpr int X_BYTES = 2 * STREAMS * kRows * 4 * (JOIN ? 2 : 1);  // row statistics exchanged by warpgroups
+  static constexpr int kMinV = 2;                                           // V slots at least, see wait_v
+  static_assert(MT <= STREAMS, "two row tiles need two accumulators");
+  static_assert(COL_O + STREAMS * D <= kTmemCols, "S / P buffers and accumulators fit tensor memory");
+  static_assert(TERMS >= 1 && TERMS <= 3 && kMinV >= AHEAD, "");
 };
 
 // Shared memory besides the ring: alignment, query buffers, barriers and tables, the plan.
 template <class C>
 size_t smem_fixed(int batch) {
-  return 1024 + (size_t)C::QB * C::Q_BYTES + kTables + C::ML_BYTES + attn::align256((size_t)(batch + 2) * 4);
+  return 1024 + (size_t)C::Q_BYTES + kTables + C::X_BYTES + (((size_t)(batch + 2) * 4 + 63) & ~size_t(63));
 }
 
 template <class C>
@@ -88,16 +95,19 @@ __device__ __forceinline__ uint32_t idesc(int n, int b_mn) {
   return (1u << 4) | (C::FP16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kRows >> 4) << 24);
 }
+// The tensor-core instructions below are executed by a whole warp with the same operands; one elected lane issues them.
+// (Operands are then known to be uniform; in a branch of one lane each would be moved to a uniform register first.)
 // D[tmem] (+)= A * B^T, 16-bit inputs, fp32 accumulate; the descriptors of A and B share their high word.
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id, uint32_t accumulate) {
   asm volatile(
       "{\n"
-      ".reg .pred p;\n"
+      ".reg .pred p, q;\n"
       ".reg .b64 a, b;\n"
+      "elect.sync _|q, 0xffffffff;\n"
       "setp.ne.b32 p, %5, 0;\n"
       "mov.b64 a, {%1, %3};\n"
       "mov.b64 b, {%2, %3};\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
       "}\n" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id), "r"(accumulate)
       : "memory");
@@ -106,13 +116,23 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t id, uint32_t accumulate) {
   asm volatile(
       "{\n"
-      ".reg .pred p;\n"
+      ".reg .pred p, q;\n"
       ".reg .b64 b;\n"
+      "elect.sync _|q, 0xffffffff;\n"
       "setp.ne.b32 p, %5, 0;\n"
       "mov.b64 b, {%2, %3};\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
       "}\n" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(hi), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -129,6 +149,40 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
       "[%6];\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+// K or V rows of one kv head: box {64 elements, rows, slices of 64, 1 head} at {0, row, slice, head}.
+__device__ __forceinline__ void tma_kv_elect(uint32_t dst, const void* map, int row, int slice, int head, uint64_t* bar,
+                                             uint64_t policy, bool once) {
+  if (once)
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "elect.sync _|q, 0xffffffff;\n"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3, %7, %4}], [%5], %6;\n"
+        "}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(smem_u32(bar)), "l"(policy), "r"(slice)
+        : "memory");
+  else
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "elect.sync _|q, 0xffffffff;\n"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %6, %4}], [%5];\n"
+        "}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(smem_u32(bar)), "r"(slice)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect_elect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+      "}\n" ::"r"(smem_u32(bar)),
+      "r"(bytes)
       : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -151,6 +205,35 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n"
+      ".reg .b64 a, b, c, d;\n"
+      "mov.b64 a, {%2, %3};\n"
+      "mov.b64 b, {%4, %5};\n"
+      "mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\n"
+      "mov.b64 {%0, %1}, d;\n"
+      "}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n"
+      ".reg .b64 a, b, d;\n"
+      "mov.b64 a, {%2, %3};\n"
+      "mov.b64 b, {%4, %5};\n"
+      "add.rn.f32x2 d, a, b;\n"
+      "mov.b64 {%0, %1}, d;\n"
+      "}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // Bits k = 0 .. 63: bit (o + k) of m, where bits before the first are 1 (committed tokens) and behind the last 0.
 __device__ __forceinline__ uint64_t window(uint64_t m, int o) {
   if (o <= -64) return ~0ull;
@@ -158,17 +241,17 @@ __device__ __forceinline__ uint64_t window(uint64_t m, int o) {
   return o < 64 ? m >> o : 0ull;
 }
 
-// Write 32 consecutive columns of one output row (element offset `at`).
+// Write 16 consecutive columns of one output row (element offset `at`).
 template <bool FP16>
-__device__ __forceinline__ void store_row32(const Params& p, int64_t at, const float (&v)[32]) {
+__device__ __forceinline__ void store_row(const Params& p, int64_t at, const float* v) {
   if (p.out_f32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   } else {
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
       o[i] = make_uint4(pack2<FP16>(v[8 * i], v[8 * i + 1]), pack2<FP16>(v[8 * i + 2], v[8 * i + 3]),
                         pack2<FP16>(v[8 * i + 4], v[8 * i + 5]), pack2<FP16>(v[8 * i + 6], v[8 * i + 7]));
   }
@@ -187,31 +270,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
                                                                         const __grid_constant__ CUtensorMap tm_q,
                                                                         const __grid_constant__ CUtensorMap tm_k,
                                                                         const __grid_constant__ CUtensorMap tm_v) {
-  constexpr int D = C::D, MT = C::MT, TK = C::TK, SW = C::SW, PW = C::PW, TERMS = C::TERMS, NWG = C::NWG;
-  constexpr int kThreads = C::kThreads, kSoftmaxThreads = 128 * NWG;
+  constexpr int D = C::D, MT = C::MT, TK = C::TK, SW = C::SW, PW = C::PW, TERMS = C::TERMS, NB = C::NB, BUFS = C::BUFS;
+  constexpr int kThreads = C::kThreads, kSoftmaxThreads = C::kSoftmaxThreads;
+  constexpr bool JOIN = C::JOIN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int RK = p.kslots, RV = p.vslots, S = RK + RV;
   uint8_t* qbuf = smem;
-  uint8_t* ring = qbuf + C::QB * C::Q_BYTES;
+  uint8_t* ring = qbuf + C::Q_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * C::SLOT);  // [RK of K, RV of V]: the slot's tile has landed
   uint64_t* empty = full + kMaxSlots;                                // [...]: its MMAs are done
-  uint64_t* s_full = empty + kMaxSlots;  // [2]: S buffer x holds the scores of its item
-  uint64_t* p_full = s_full + 2;         // [2]: its weights are written (one arrival per warp)
+  uint64_t* s_full = empty + kMaxSlots;  // [2]: S / P buffer x holds the scores of its item
+  uint64_t* p_full = s_full + 2;         // [2]: its weights are written (one arrival per warp of the stream)
   uint64_t* pv_done = p_full + 2;        // [2]: the product that read them is complete
-  uint64_t* q_full = pv_done + 2;        // [2]
-  uint64_t* q_empty = q_full + 2;        // [2]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_empty + 2);
-  int32_t* s_lock = reinterpret_cast<int32_t*>(s_tmem + 1);
+  uint64_t* q_full = pv_done + 2;
+  uint64_t* q_empty = q_full + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_empty + 1);
   int32_t* s_bad = reinterpret_cast<int32_t*>(s_tmem + 2);  // [8] per piece (seq & 7): a page id was bad
-  int32_t* s_misc = s_bad + 8;                              // [32]
-  uint64_t* s_used = reinterpret_cast<uint64_t*>(s_misc + 32);  // [2 warpgroups]
-  int32_t* s_par = reinterpret_cast<int32_t*>(s_used + 2);      // [2 warpgroups][64]
-  static_assert(8 * (2 * kMaxSlots + 10) + 8 + 32 + 128 + 16 + 2 * 64 * 4 <= kTables, "the tables fit their area");
-  float2* s_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(full) + kTables);  // [2 warpgroups][128]
-  int32_t* s_prefix = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(s_ml) + C::ML_BYTES);
+  int32_t* s_misc = s_bad + 8;                              // [24]: per warp, then the tile counts' range
+  uint64_t* s_used = reinterpret_cast<uint64_t*>(s_misc + 24);  // [2 streams]
+  int8_t* s_par = reinterpret_cast<int8_t*>(s_used + 2);        // [2 streams][64]
+  static_assert(8 * (2 * kMaxSlots + 8) + 8 + 32 + 96 + 16 + 2 * 64 <= kTables, "the tables fit their area");
+  float* s_x = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + kTables);  // [warpgroups][128] (joined: twice)
+  int32_t* s_prefix = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(s_x) + C::X_BYTES);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int B = p.batch, N = p.nodes, U = p.kv_heads * p.groups;
   const int64_t max_ctx = (int64_t)p.max_blocks << p.page_shift;
 
@@ -230,8 +313,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     const int b0 = tid * per;
     int mine = 0, lo = INT32_MAX, hi = 0;
     if (tid == 0) {
-      s_misc[30] = INT32_MAX;
-      s_misc[31] = 0;
+      s_misc[22] = INT32_MAX;
+      s_misc[23] = 0;
     }
     for (int b = b0; b < b0 + per && b < B; ++b) {
       int ctx;
@@ -252,8 +335,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     if (lane == 31) s_misc[warp] = incl;
     __syncthreads();
     if (hi > 0) {
-      atomicMin(&s_misc[30], lo);
-      atomicMax(&s_misc[31], hi);
+      atomicMin(&s_misc[22], lo);
+      atomicMax(&s_misc[23], hi);
     }
     int run = incl - mine;
     for (int w = 0; w < warp; ++w) run += s_misc[w];
@@ -266,17 +349,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     if (tid == 0) {
       for (int s = 0; s < S; ++s) {
         mbar_init(&full[s], 1);
-        mbar_init(&empty[s], MT);  // one arrival for each row tile that read it
+        mbar_init(&empty[s], 1);
       }
       for (int x = 0; x < 2; ++x) {
         mbar_init(&s_full[x], 1);
-        mbar_init(&p_full[x], 4);
+        mbar_init(&p_full[x], 8);
         mbar_init(&pv_done[x], 1);
-        mbar_init(&q_full[x], 1);
-        mbar_init(&q_empty[x], C::ISSUERS);
       }
+      mbar_init(q_full, 1);
+      mbar_init(q_empty, 1);
       fence_mbar_init();
-      *s_lock = 0;
       p.split[blockIdx.x].nseg = 0;
     }
     __syncthreads();
@@ -305,7 +387,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
   }
   // padding rows of the query tiles (the copies write npt * gqa rows each)
   const int packed = p.npt * p.gqa;
-  for (int i = tid; i < C::QB * MT * C::SUBS * (kRows - packed) * 8; i += kThreads) {
+  for (int i = tid; i < MT * C::SUBS * (kRows - packed) * 8; i += kThreads) {
     const int rest = i / 8, slice = rest / (kRows - packed), r = packed + rest % (kRows - packed);
     *reinterpret_cast<uint4*>(qbuf + slice * kRows * 128 + r * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
   }
@@ -325,339 +407,317 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     }
   };
 
-  // Registers: 384 threads are launched with kLaunchRegs each; the warps that only issue copies and MMAs give theirs to
-  // the softmax warps, which hold a row's scores (3 * 168 = 72 + 2 * 216). Each role's branch has its own
-  // instruction: where branches join, the compiler would hold all that follows to the smaller number.
+  // Registers: 640 threads are launched with kLaunchRegs each; the warps that only issue copies and MMAs give some of
+  // theirs to the softmax warps (5 * 96 = 64 + 4 * 104). Each role's branch has its own instruction: where branches
+  // join, the compiler would hold all that follows to the smaller number.
   if (warp == 0) {
     // =================== producer: TMA ===================
+    if constexpr (C::STREAMS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     // Tile j's K goes to slot j % RK of the K ring, its V to slot j % RV of the V ring, in the order in which they are
-    // taken: K0, K1 V0, K2 V1, ... with one row tile, K0 V0, K1 V1, ... with two. A barrier's parity names its phase only
-    // while the phase before is over, so every slot is used by both issuers, or by one alone (even depths, one row tile).
-    if constexpr (C::DUAL) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    // taken: the first AHEAD tiles' K, then V0 K(AHEAD), V1 K(AHEAD + 1), ...
     const int bs = 1 << p.page_shift;
-    const int BH = bs < TK ? bs : TK;
+    const int BH = bs < TK ? bs : TK;  // tokens of a copy: a page, or a tile of it
     const int pieces = TK / BH;
     const uint64_t pol = l2_evict_first_policy();  // K and V that no other unit reads again
-    // Lane i < pieces copies page piece i of a tile.
-    Cursor ld = cursor_at(f0, s_prefix, B, U);
-    int seq = 0, win_b = -1, win_base = 0, win_val = 0, ctx = p.ctx_lens[ld.b];
-    bool fresh = true;
-    int zk = 0, zv = 0, gv = 0;  // token rows of the lane's piece, kv head
-    auto load_tile = [&](const CUtensorMap* map, int g, int z, int first, int depth, int j) {  // ring `first`, tile j
-      const int s = first + j % depth;
-      if (lane == 0) {
-        if (j >= depth) wait(&empty[s], j / depth - 1);
-        if (!lost) mbar_arrive_expect_tx(&full[s], (uint32_t)C::SLOT);
+    // Two walks over the tiles, K's AHEAD tiles before V's. The lanes hold a window of 32 entries of the block table's row
+    // as token rows; entries past the context and bad ones lie far outside the cache and read zeros.
+    constexpr int kNowhere = -(1 << 20);
+    struct Walk {
+      Cursor c;
+      int left, ctx, win_b, win_base, win_row, slot, phase;
+      bool win_bad;
+    };
+    auto load_tile = [&](Walk& w, const CUtensorMap* map, int first, int depth) {  // into ring `first`
+      const int t0 = w.c.tile * TK, n0 = t0 >> p.page_shift;
+      if (w.c.b != w.win_b || n0 < w.win_base || n0 + pieces > w.win_base + 32) {
+        w.win_b = w.c.b;
+        w.win_base = n0;
+        const bool in = n0 + lane < ((w.ctx + bs - 1) >> p.page_shift);
+        const int page = in ? __ldg(p.block_table + (int64_t)w.c.b * p.max_blocks + n0 + lane) : 0;
+        const bool ok = page >= 0 && (int64_t)page < p.num_blocks;
+        w.win_row = in && ok ? page << p.page_shift : kNowhere;
+        w.win_bad = __any_sync(0xffffffffu, in && !ok);
       }
-      lost = __shfl_sync(0xffffffffu, (int)lost, 0) != 0;
-      if (lane < pieces && !lost) {
-        const uint32_t dst = ring_u32 + s * C::SLOT + lane * BH * 128;
+      if (w.win_bad && lane == 0) s_bad[w.c.seq & 7] = 1;  // somewhere in the sequence: all of its rows are zeros
+      if (w.phase > 0) wait(&empty[first + w.slot], w.phase - 1);
+      if (!lost) {
+        uint64_t* bar = &full[first + w.slot];
+        mbar_expect_elect(bar, (uint32_t)C::SLOT);
+        const uint32_t dst = ring_u32 + (first + w.slot) * C::SLOT;
+        const int g = p.groups == 1 ? w.c.g : w.c.g / p.groups, in_page = t0 & (bs - 1);
 #pragma unroll
-        for (int sub = 0; sub < C::SUBS; ++sub) {
-          if (p.groups == 1) tma_load_3d_hint(dst + sub * TK * 128, map, sub * 64, g, z, &full[s], pol);
-          else tma_load_3d(dst + sub * TK * 128, map, sub * 64, g, z, &full[s]);
-        }
+        for (int i = 0; i < TK / 16; ++i)
+          if (i < pieces) {
+            const int row = __shfl_sync(0xffffffffu, w.win_row, n0 - w.win_base + i) + in_page;
+            if (pieces == 1) {
+              tma_kv_elect(dst, map, row, 0, g, bar, pol, p.groups == 1);  // all slices
+            } else {
+#pragma unroll
+              for (int sub = 0; sub < C::SUBS; ++sub)
+                tma_kv_elect(dst + sub * TK * 128 + i * BH * 128, map, row, sub, g, bar, pol, p.groups == 1);
+            }
+          }
+      }
+      if (++w.slot == depth) w.slot = 0, ++w.phase;
+      if (--w.left == 0) {
+        w.c.tile = w.c.ntiles - 1;
+        cursor_advance(w.c, s_prefix, B, U);
+        w.left = w.c.ntiles;
+        if (w.c.b < B) w.ctx = p.ctx_lens[w.c.b];
+      } else {
+        ++w.c.tile;
       }
     };
+    Walk wk;
+    wk.c = cursor_at(f0, s_prefix, B, U);
+    wk.left = wk.c.ntiles - wk.c.tile;
+    wk.ctx = p.ctx_lens[wk.c.b];
+    wk.win_b = -1;
+    wk.win_base = wk.win_row = wk.slot = wk.phase = 0;
+    wk.win_bad = false;
+    Walk wv = wk;
+    const int steps = __shfl_sync(0xffffffffu, n_tiles, 0);
+    int fresh = -1;  // the last piece whose queries were asked for
 #pragma unroll 1
-    for (int j = 0; j < n_tiles; ++j) {
-      const int g = ld.g / p.groups;
-      zv = zk;
-      {
-        // the tile's page ids, from a window of 32 of the block table's row held by the lanes
-        const int n_first = (ld.tile * TK) >> p.page_shift;
-        if (ld.b != win_b || n_first < win_base || n_first + pieces > win_base + 32) {
-          win_b = ld.b;
-          win_base = n_first;
-          win_val = (n_first + lane < ((ctx + bs - 1) >> p.page_shift))
-                        ? __ldg(p.block_table + (int64_t)ld.b * p.max_blocks + n_first + lane) : 0;
-        }
-        const int t = ld.tile * TK + lane * BH;
-        const int32_t page = __shfl_sync(0xffffffffu, win_val, ((t >> p.page_shift) - win_base) & 31);
-        const bool in = lane < pieces && t < ctx, ok = page >= 0 && (int64_t)page < p.num_blocks;
-        zk = in && ok ? (int)(((int64_t)page << p.page_shift) + (t & (bs - 1))) : -BH;  // -BH: reads zeros
-        const bool bad = __any_sync(0xffffffffu, in && !ok);
-        if (lane == 0) {
-          if (fresh) s_bad[seq & 7] = 0;
-          if (bad) s_bad[seq & 7] = 1;
-        }
-      }
-      load_tile(&tm_k, g, zk, 0, RK, j);
-      if (MT == 2) load_tile(&tm_v, g, zk, RK, RV, j);
-      else if (j > 0) load_tile(&tm_v, gv, zv, RK, RV, j - 1);
-      if (fresh && lane == 0) {
-        const int x = seq % C::QB;
-        if (seq >= C::QB) wait(&q_empty[x], seq / C::QB - 1);
-        const int n0 = (ld.g % p.groups) * MT * p.npt;
-        if (!lost) mbar_arrive_expect_tx(&q_full[x], (uint32_t)(MT * packed * D * 2));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int sub = 0; sub < C::SUBS && !lost; ++sub)
-            tma_load_4d(q_u32 + x * C::Q_BYTES + mt * C::Q_TILE + sub * kRows * 128, &tm_q, sub * 64, g * p.gqa,
-                        n0 + mt * p.npt, ld.b, &q_full[x]);
-      }
+    for (int j = 0; j < steps + C::AHEAD; ++j) {
+      if (j >= C::AHEAD) load_tile(wv, &tm_v, RK, RV);
+      if (j >= steps) continue;
+      const Cursor c = wk.c;
+      if (c.seq != fresh && lane == 0) s_bad[c.seq & 7] = 0;  // the piece eight before is long written
       __syncwarp();
-      gv = g;
-      const int before = ld.seq, b_before = ld.b;
-      cursor_advance(ld, s_prefix, B, U);
-      fresh = ld.seq != before;
-      if (fresh) ++seq;
-      if (ld.b != b_before && ld.b < B) ctx = p.ctx_lens[ld.b];
+      load_tile(wk, &tm_k, 0, RK);
+      if (c.seq != fresh) {
+        if (c.seq > 0) wait(q_empty, c.seq - 1);
+        if (!lost && lane == 0) {
+          const int n0 = (c.g % p.groups) * MT * p.npt;
+          mbar_arrive_expect_tx(q_full, (uint32_t)(MT * packed * D * 2));
+#pragma unroll 1
+          for (int i = 0; i < MT * C::SUBS; ++i) {
+            const int tile = i / C::SUBS, sub = i % C::SUBS;
+            tma_load_4d(q_u32 + tile * C::Q_TILE + sub * kRows * 128, &tm_q, sub * 64, (c.g / p.groups) * p.gqa,
+                        n0 + tile * p.npt, c.b, q_full);
+          }
+        }
+        __syncwarp();
+        fresh = c.seq;
+      }
     }
-    if (MT == 1) load_tile(&tm_v, gv, zk, RK, RV, n_tiles - 1);
     return;
   }
 
-  if (warp <= C::ISSUERS) {
-    // =================== MMA issuers (one thread of warp 1, and of warp 2 with two accumulators) ===================
-    // Item j is tile j (one row tile) or row tile j & 1 of tile j >> 1 (two); it uses S / P buffer j & 1. An issuer's
-    // MMAs run in the order of its instructions, so scores issued after a product may overwrite the weights it reads.
-    if constexpr (C::DUAL) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-    if (lane == 0) {
+  if (warp == 1) {
+    // =================== MMA issuer (one warp) ===================
+    // Item j is tile j (one row tile) or row tile j & 1 of tile j >> 1 (two). Its S / P buffer is j & 1, its accumulator
+    // the buffer's own, or the only one. The scores run two items ahead: those of item j + 2 follow the product of item
+    // j, whose weights they overwrite (MMAs run in the order of their instructions), and while the softmax works on one
+    // buffer, the tensor core works on the other.
+    if constexpr (C::STREAMS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    {
       const uint32_t id_qk = idesc<C>(TK, 0), id_pv = idesc<C>(D, 1);
       // Descriptors differ in their low words only (start address / 16 in the low 14 bits).
       const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);       // Q, K: rows of 64 elements, K-major
       const uint64_t vmn = smem_desc_sw128(0, TK * 128, 1024);  // V: MN-major, slices of 64 dims
       const uint32_t k_hi = (uint32_t)(kmaj >> 32), v_hi = (uint32_t)(vmn >> 32);
       const uint32_t q_lo = (uint32_t)kmaj + (q_u32 >> 4), k_lo = (uint32_t)kmaj + (ring_u32 >> 4);
-      const uint32_t v_lo = (uint32_t)vmn + (ring_u32 >> 4);
-      auto qk = [&](uint32_t s, uint32_t qb, int slot) {  // scores into buffer address s
-        tc_fence_after();
-        const uint32_t kb = k_lo + slot * (C::SLOT >> 4);
+      const uint32_t v_lo = (uint32_t)vmn + ((ring_u32 + RK * C::SLOT) >> 4);
+      const int n_items = __shfl_sync(0xffffffffu, n_tiles, 0) * MT;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // scores: the next item, its tile's slot and phase, the tiles left in its unit
+      Cursor cq = cursor_at(f0, s_prefix, B, U);
+      int jq = 0, sk = 0, pk = 0, left_q = __shfl_sync(0xffffffffu, min(cq.ntiles - cq.tile, n_tiles), 0);
+      bool q_fresh = true;
+      int q_seq = 0;
+      // products: the same, and the items of the unit so far
+      Cursor cv = cq;
+      int sv = 0, pv = 0, left_v = left_q, in_unit = 0;
+      auto scores = [&]() {
+        const int x = jq & 1, mt = MT == 2 ? x : 0;
+        if (mt == 0) {
+          if (q_fresh) wait(q_full, q_seq);
+          wait(&full[sk], pk);
+          tc_fence_after();
+        }
+        const uint32_t qb = q_lo + ((mt * C::Q_TILE) >> 4), kb = k_lo + sk * (C::SLOT >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t qo = ((ks >> 2) * kRows * 128 + (ks & 3) * 32) >> 4;
           const uint32_t ko = ((ks >> 2) * TK * 128 + (ks & 3) * 32) >> 4;
-          umma_ss(s, qb + qo, kb + ko, k_hi, id_qk, ks > 0 ? 1u : 0u);
+          umma_ss(tm + (uint32_t)(x * SW), qb + qo, kb + ko, k_hi, id_qk, ks > 0 ? 1u : 0u);
         }
+        umma_commit_elect(&s_full[x]);
+        if (mt == MT - 1) {
+          umma_commit_elect(&empty[sk]);
+          if (++sk == RK) sk = 0, ++pk;
+          q_fresh = --left_q == 0;
+          if (q_fresh) {
+            umma_commit_elect(q_empty);
+            cq.tile = cq.ntiles - 1;
+            cursor_advance(cq, s_prefix, B, U);
+            ++q_seq;
+            left_q = __shfl_sync(0xffffffffu, cq.ntiles, 0);
+          }
+        }
+        ++jq;
       };
-      auto pv = [&](uint32_t d, uint32_t s, int slot, bool first) {  // first: nothing is in the accumulator yet
+#pragma unroll 1
+      for (int i = 0; i < BUFS && jq < n_items; ++i) scores();
+#pragma unroll 1
+      for (int j = 0; j < n_items; ++j) {
+        const int x = j & 1, mt = MT == 2 ? x : 0;
+        if (mt == 0) wait(&full[RK + sv], pv);
+        wait(&p_full[x], j >> 1);
         tc_fence_after();
-        const uint32_t vb = v_lo + slot * (C::SLOT >> 4);
+        const uint32_t vb = v_lo + sv * (C::SLOT >> 4), d = tm + (uint32_t)(C::COL_O + (C::STREAMS == 2 ? x * D : 0));
+        const bool first = in_unit < C::STREAMS;  // nothing of the unit is in the accumulator
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
           for (int kk = 0; kk < TK / 16; ++kk)
-            umma_ts(d, s + term * PW + kk * 8, vb + ((kk * 2048) >> 4), v_hi, id_pv,
+            umma_ts(d, tm + (uint32_t)(x * SW + term * PW + kk * 8), vb + ((kk * 2048) >> 4), v_hi, id_pv,
                     (first && term == 0 && kk == 0) ? 0u : 1u);
-      };
-      if constexpr (C::DUAL) {
-        // Issuer h owns buffer and accumulator h: scores, wait for the weights, product, next scores. The two issuers'
-        // MMAs interleave, so one item's softmax runs under the other's MMAs.
-        const int h = warp - 1;
-        const uint32_t s = tmem + (uint32_t)(h * SW), d = tmem + (uint32_t)(C::COL_O + h * D);
-        constexpr int step = MT == 1 ? 2 : 1;  // tiles from one item of an issuer to its next
-        Cursor cu = cursor_at(f0, s_prefix, B, U);
-        int done = 0, item = 0, sk = MT == 1 ? h : 0, sv = sk, pk = 0, pv_ = 0;  // slots and phases of the item's K and V
-        // A product and the next scores are issued as one burst under a lock: if the two issuers' MMAs alternated one by
-        // one, both items' results would come at the end of both, and both softmaxes would run at once, then both
-        // MMA phases (measured: 5000 cycles a tile against 3000).
-        bool held = false;
-        auto lock = [&]() {
-          const long long start = clock64();  // order is all it gives: after the limit the issue goes on without it
-          while (!held && atomicCAS(s_lock, 0, 1) != 0 && clock64() - start < 100000) {
-          }
-          held = true;
-        };
-        auto unlock = [&]() {
-          if (held) atomicExch(s_lock, 0);
-          held = false;
-        };
-        for (int seq = 0; done < n_tiles; ++seq) {
-          const int n = min(cu.ntiles - cu.tile, n_tiles - done), x = seq % C::QB;
-          const int t_first = MT == 1 ? ((done & 1) == h ? 0 : 1) : 0;
-          const uint32_t qb = q_lo + ((x * C::Q_BYTES + (MT == 2 ? h : 0) * C::Q_TILE) >> 4);
-          if (held && !mbar_try_wait(&q_full[x], (uint32_t)((seq / C::QB) & 1))) unlock();
-          wait(&q_full[x], seq / C::QB);  // without an item too: the buffer's last use must be over before the arrival
-          if (t_first >= n) mbar_arrive(&q_empty[x]);
-          for (int tt = t_first; tt < n; tt += step, ++item) {
-            if (!mbar_try_wait(&full[sk], (uint32_t)(pk & 1))) {
-              unlock();  // not while waiting
-              wait(&full[sk], pk);
-            }
-            lock();
-            qk(s, qb, sk);
-            umma_commit(&s_full[h]);
-            unlock();
-            umma_commit(&empty[sk]);
-            if (tt + step >= n) umma_commit(&q_empty[x]);
-            if ((sk += step) >= RK) sk -= RK, ++pk;
-            wait(&full[RK + sv], pv_);
-            wait(&p_full[h], item);
-            lock();
-            pv(d, s, RK + sv, tt == t_first);
-            umma_commit(&pv_done[h]);
-            umma_commit(&empty[RK + sv]);
-            if ((sv += step) >= RV) sv -= RV, ++pv_;
-          }
-          done += n;
-          cu.tile += n - 1;
-          cursor_advance(cu, s_prefix, B, U);
-        }
-        unlock();
-      } else {
-        // One accumulator: the scores of item j + 1 are issued before the product of item j, so they run while the
-        // softmax works on item j.
-        const uint32_t d = tmem + (uint32_t)C::COL_O;
-        Cursor cq = cursor_at(f0, s_prefix, B, U), cv = cq;
-        int left_q = min(cq.ntiles - cq.tile, n_tiles), left_v = left_q, sk = 0, pk = 0, sv = 0, pv_ = 0;
-        bool q_fresh = true, v_fresh = true;
-        auto issue_qk = [&](int j) {
-          if (q_fresh) wait(&q_full[0], cq.seq);
-          wait(&full[sk], pk);
-          qk(tmem + (uint32_t)((j & 1) * SW), q_lo, sk);
-          umma_commit(&s_full[j & 1]);
-          umma_commit(&empty[sk]);
-          if (++sk == RK) sk = 0, ++pk;
-          q_fresh = --left_q == 0;
-          if (q_fresh) {
-            umma_commit(&q_empty[0]);
-            cq.tile = cq.ntiles - 1;
-            cursor_advance(cq, s_prefix, B, U);
-            left_q = cq.ntiles;
-          }
-        };
-        issue_qk(0);
-        for (int j = 0; j < n_tiles; ++j) {
-          if (j + 1 < n_tiles) issue_qk(j + 1);
-          wait(&full[RK + sv], pv_);
-          wait(&p_full[j & 1], j >> 1);
-          pv(d, tmem + (uint32_t)((j & 1) * SW), RK + sv, v_fresh);
-          umma_commit(&pv_done[j & 1]);
-          umma_commit(&empty[RK + sv]);
-          if (++sv == RV) sv = 0, ++pv_;
-          v_fresh = --left_v == 0;
-          if (v_fresh) {
+        umma_commit_elect(&pv_done[x]);  // before the buffer's next scores, see wait_pv
+        if (mt == MT - 1) umma_commit_elect(&empty[RK + sv]);
+        if (jq < n_items) scores();
+        ++in_unit;
+        if (mt == MT - 1) {
+          if (++sv == RV) sv = 0, ++pv;
+          if (--left_v == 0) {
             cv.tile = cv.ntiles - 1;
             cursor_advance(cv, s_prefix, B, U);
-            left_v = cv.ntiles;
+            left_v = __shfl_sync(0xffffffffu, cv.ntiles, 0);
+            in_unit = 0;
           }
         }
       }
     }
     __syncwarp();
-    named_sync(kBarTail, 32 * C::ISSUERS + kSoftmaxThreads);  // the softmax warps are done with tensor memory
-    if (warp == 1) {
-      tc_fence_after();
-      tmem_dealloc(tmem, kTmemCols);
-    }
+    named_sync(kBarTail, 32 + kSoftmaxThreads);  // the softmax warps are done with tensor memory
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
     return;
   }
   if (warp < 4) {
-    if constexpr (C::DUAL) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if constexpr (C::STREAMS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     return;
   }
 
   // =================== softmax / epilogue: one thread per row ===================
-  if constexpr (C::DUAL) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
-  const int h = (warp - 4) >> 2;      // warpgroup
-  const int r = tid - 128 - h * 128;  // row of the row tile = tensor-memory lane
+  if constexpr (C::STREAMS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+  const int wg = (warp - 4) >> 2, h = wg >> 1, half = wg & 1;  // warpgroup; its stream and half of a tile's keys
+  const int r = tid & 127;                                     // row of the row tile = tensor-memory lane
+  const int st = tid & 255;                                    // with half * 128 + r the stream's threads, in some order
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-  const int bar = kBarGroup + h;
+  const int bar = kBarStream + h;
   const int mt = MT == 2 ? h : 0;
-  const uint32_t t_o = tmem + (uint32_t)(C::COL_O + h * D) + lanes;  // this warpgroup's accumulator
-  auto wait_pv = [&](int j) {
-    wait(&pv_done[j & 1], j >> 1);
-    tc_fence_after();
-  };
-  // The slot of item j's V tile, which has landed. The slot's tile before it was multiplied before the scores of item j
-  // were issued (RV >= 2), so the parity is unambiguous.
-  auto wait_v = [&](int j) -> int {
-    const int tile = MT == 2 ? j >> 1 : j, s = RK + tile % RV;
+  constexpr int CW = C::CW;
+  const uint32_t t_o = tmem + (uint32_t)(C::COL_O + h * D) + lanes;  // the stream's accumulator
+  // The slot of tile `tile`'s V, which has landed. The slot's tile before it was multiplied before the scores of this one
+  // were issued (RV >= AHEAD), so the parity is unambiguous.
+  auto wait_v = [&](int tile) -> int {
+    const int s = RK + tile % RV;
     wait(&full[s], tile / RV);
     return s;
+  };
+  // The product of the stream's item i is complete. Its buffer's product before it was issued before the scores of
+  // item i, and the next one needs weights of this stream: the parity is unambiguous.
+  auto wait_pv = [&](int i) {
+    wait(&pv_done[C::STREAMS == 2 ? h : i & 1], i / NB);
+    tc_fence_after();
   };
 
   Cursor cu = cursor_at(f0, s_prefix, B, U);
   int done = 0;  // tiles of this CTA before the unit
+  int item = 0;  // items of this stream before the current one
   for (int seq = 0; done < n_tiles; ++seq) {
-    const int b = cu.b, u = cu.g, n = min(cu.ntiles - cu.tile, n_tiles - done);
-    const int ctx = p.ctx_lens[b], base = ctx - N;
-    const int n0 = ((u % p.groups) * MT + mt) * p.npt;  // first node of the row tile
-    float m = -INFINITY, l = 0.f;  // running maximum (scaled; it may lag by up to 8) and sum of the row
+    const int n = min(cu.ntiles - cu.tile, n_tiles - done);
+    const int base = p.ctx_lens[cu.b] - N;
+    float m = -INFINITY, l = 0.f;  // running maximum (scaled; it may lag by up to 8), the thread's share of the row's sum
     bool tree_bad = false, dead = false, have_tree = false;
-    uint64_t sees = 0, used = 0;
-    int mine = 0;  // items of this warpgroup in the unit so far
-    int last_j = -1;
-    // the first tile of this warpgroup: every tile, or every other one of the CTA's
-    const int t_first = (C::DUAL && MT == 1) ? ((done & 1) == h ? 0 : 1) : 0;
-    for (int tt = t_first; tt < n; tt += (C::DUAL && MT == 1) ? 2 : 1) {
-      const int j = MT == 2 ? 2 * (done + tt) + h : done + tt;
-      const int x = j & 1;
+    uint64_t sees = 0;
+    int mine = 0;  // items of this stream in the unit so far
+    // the stream's first tile: every tile, or every other one of the CTA's
+#pragma unroll 1
+    for (int tt = JOIN ? ((done & 1) == h ? 0 : 1) : 0; tt < n; tt += JOIN ? 2 : 1, ++item, ++mine) {
+      const int x = C::STREAMS == 2 ? h : item & 1;
       const uint32_t t_s = tmem + (uint32_t)(x * SW) + lanes;
-      const int t0 = (cu.tile + tt) * TK;
-      const bool edge = t0 + TK > base;  // the tile holds keys that not every row sees
+      const int off = (cu.tile + tt) * TK - base;  // the tile's first key among the tree's
+      const bool edge = off + TK > 0;              // the tile holds keys that not every row sees
       if (edge && !have_tree) {
         have_tree = true;
-        if (r < N) s_par[h * 64 + r] = __ldg(p.parents + (int64_t)b * N + r);
-        named_sync(bar, 128);
-        const bool bad = r < N && !tree::parent_ok(s_par + h * 64, r);
-        const uint32_t word = __ballot_sync(0xffffffffu, r < N && s_par[h * 64 + (r & 63)] != SPEC_TREE_UNUSED);
-        if (r == 0) reinterpret_cast<uint32_t*>(s_used + h)[0] = word;
-        if (r == 32) reinterpret_cast<uint32_t*>(s_used + h)[1] = word;
-        tree_bad = named_sync_or(bar, 128, bad);
-        used = s_used[h];
-        const int node = n0 + r / p.gqa;
+        int par = SPEC_TREE_ROOT;
+        if (st < N) {
+          par = __ldg(p.parents + (int64_t)cu.b * N + st);
+          s_par[h * 64 + st] = (int8_t)max(-3, min(64, par));  // what is out of range stays a bad parent
+        }
+        named_sync(bar, 256);
+        const bool bad = st < N && !tree::parent_ok(s_par + h * 64, st);
+        const uint32_t word = __ballot_sync(0xffffffffu, st < N && par != SPEC_TREE_UNUSED);
+        if (st == 0) reinterpret_cast<uint32_t*>(s_used + h)[0] = word;
+        if (st == 32) reinterpret_cast<uint32_t*>(s_used + h)[1] = word;
+        tree_bad = named_sync_or(bar, 256, bad);
+        const int node = ((cu.g % p.groups) * MT + mt) * p.npt + r / p.gqa;
         if (r < packed && node < N) {
           sees = tree::ancestors(s_par + h * 64, node);
           dead = sees == 0;
         }
       }
-      wait(&s_full[x], j >> 1);
+      wait(&s_full[x], item / NB);
       tc_fence_after();
-      float v[TK];
+      float v[CW];
 #pragma unroll
-      for (int c = 0; c < TK / 16; ++c) tmem_ld16(t_s + c * 16, *reinterpret_cast<float(*)[16]>(&v[c * 16]));
-      tmem_wait_ld_regs<TK>(v);
+      for (int c = 0; c < CW / 16; ++c) tmem_ld16(t_s + half * CW + c * 16, *reinterpret_cast<float(*)[16]>(&v[c * 16]));
+      tmem_wait_ld_regs<CW>(v);
       if (edge) {
-        const int off = t0 - base;
         // V of slots that no row sees may hold anything: zeros, so that 0 weights give 0. With two row tiles both
-        // warpgroups write them, each before its own product.
-        {
-          const uint64_t dead0 = ~window(used, off), dead1 = TK > 64 ? ~window(used, off + 64) : 0;
-          if (dead0 | dead1) {
-            uint8_t* vt = ring + wait_v(j) * C::SLOT;
-            for (int i = r; i < TK * (D / 8); i += 128) {
-              const int key = i / (D / 8), ch = i % (D / 8);
-              if (((key < 64 ? dead0 : dead1) >> (key & 63)) & 1)
-                *reinterpret_cast<uint4*>(vt + (ch >> 3) * TK * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4)) =
-                    make_uint4(0, 0, 0, 0);
-            }
+        // streams write them, each before its own product.
+        const uint64_t dead0 = ~window(s_used[h], off), dead1 = TK > 64 ? ~window(s_used[h], off + 64) : 0;
+        if (dead0 | dead1) {
+          uint8_t* vt = ring + wait_v(done + tt) * C::SLOT;
+          for (int i = st; i < TK * (D / 8); i += 256) {
+            const int key = i / (D / 8), ch = i % (D / 8);
+            if (((key < 64 ? dead0 : dead1) >> (key & 63)) & 1)
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * TK * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4)) =
+                  make_uint4(0, 0, 0, 0);
           }
         }
+        const uint64_t w = window(sees, off + half * CW);
+        const uint32_t w0 = (uint32_t)w, w1 = (uint32_t)(w >> 32);
 #pragma unroll
-        for (int half = 0; half < TK / 64; ++half) {
-          const uint64_t w = window(sees, off + 64 * half);
-          const uint32_t w0 = (uint32_t)w, w1 = (uint32_t)(w >> 32);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (!((w0 >> k) & 1)) v[64 * half + k] = -INFINITY;
-            if (!((w1 >> k) & 1)) v[64 * half + 32 + k] = -INFINITY;
-          }
+        for (int k = 0; k < 32; ++k) {
+          if (!((w0 >> k) & 1)) v[k] = -INFINITY;
+          if (CW > 32 && !((w1 >> k) & 1)) v[CW > 32 ? 32 + k : k] = -INFINITY;
         }
       }
       float mx;
       {
         float a[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = v[i];
+        for (int i = 0; i < 8; ++i) a[i] = max3(v[i], v[8 + i], v[16 + i]);
 #pragma unroll
-        for (int k = 8; k < TK; k += 16)
+        for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], v[24 + i]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = k + 8 + i < TK ? max3(a[i], v[k + i], v[k + 8 + i]) : fmaxf(a[i], v[k + i]);
+        for (int k = 32; k < CW; k += 16)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = max3(a[i], v[k + i], v[k + 8 + i]);
         mx = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7])) * p.scale_log2;
       }
-      const bool grow = mx > m + 8.f;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? mx : m;
-        const float a = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
-        m = mn;
+      // Both halves of a row use one maximum. The barrier also tells that both have read their scores, which the weights
+      // overwrite.
+      tc_fence_before();
+      const bool any = named_sync_or(bar, 256, mx > m + 8.f);
+      tc_fence_after();
+      if (any) {
+        s_x[wg * kRows + r] = mx;
+        named_sync(bar, 256);
+        mx = fmaxf(mx, s_x[(wg ^ 1) * kRows + r]);
+        const bool grow = mx > m + 8.f;
+        const float a = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mx)) : 1.f;
+        m = grow ? mx : m;
         l *= a;
-        if (mine > 0) {  // the accumulator holds earlier tiles
-          wait_pv(last_j);
+        if (mine > 0) {  // the accumulator holds earlier tiles; each half of the stream rescales half of its columns
+          wait_pv(item - 1);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
             float o[16];
             tmem_ld16(t_o + c, o);
             tmem_wait_ld_regs<16>(o);
@@ -668,19 +728,19 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
         }
       }
       const float ms = m == -INFINITY ? 0.f : m;
-      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+      const float2 sc = make_float2(p.scale_log2, p.scale_log2), mm = make_float2(-ms, -ms);
+      float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
-      for (int c = 0; c < TK; c += 32) {
+      for (int c = 0; c < CW; c += 32) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          v[c + i] = fast_exp2(fmaf(v[c + i], p.scale_log2, -ms));
-          v[c + i + 1] = fast_exp2(fmaf(v[c + i + 1], p.scale_log2, -ms));
-          v[c + i + 2] = fast_exp2(fmaf(v[c + i + 2], p.scale_log2, -ms));
-          v[c + i + 3] = fast_exp2(fmaf(v[c + i + 3], p.scale_log2, -ms));
-          l0 += v[c + i];
-          l1 += v[c + i + 1];
-          l2 += v[c + i + 2];
-          l3 += v[c + i + 3];
+        for (int i = c; i < c + 32; i += 4) {
+          const float2 e0 = fma2(make_float2(v[i], v[i + 1]), sc, mm), e1 = fma2(make_float2(v[i + 2], v[i + 3]), sc, mm);
+          v[i] = fast_exp2(e0.x);
+          v[i + 1] = fast_exp2(e0.y);
+          v[i + 2] = fast_exp2(e1.x);
+          v[i + 3] = fast_exp2(e1.y);
+          l0 = add2(l0, make_float2(v[i], v[i + 1]));
+          l1 = add2(l1, make_float2(v[i + 2], v[i + 3]));
         }
         uint32_t w[16];
 #pragma unroll
@@ -696,47 +756,47 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
               e1 -= f.y;
             }
           }
-          tmem_st16u(t_s + term * PW + c / 2, w);
+          tmem_st16u(t_s + term * PW + (half * CW + c) / 2, w);
         }
       }
-      l += (l0 + l1) + (l2 + l3);
+      l0 = add2(l0, l1);
+      l += l0.x + l0.y;
       tmem_wait_st();
       if (edge) fence_proxy_async_smem();  // zeroed rows of V
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[x]);
-      last_j = j;
-      ++mine;
     }
 
     // ---- the unit's rows: output, or a normalised partial and its log-sum-exp
     const bool whole = cu.tile == 0 && n == cu.ntiles;
-    const int64_t u0 = (int64_t)s_prefix[b] * U + (int64_t)u * cu.ntiles;
+    const int64_t u0 = (int64_t)s_prefix[cu.b] * U + (int64_t)cu.g * cu.ntiles;
     const int c0 = (int)(u0 / W);
     const int slot = piece_slot((int)blockIdx.x, c0, u0, W);
     if (!whole && cu.tile == 0 && tid == 128)
-      p.split[blockIdx.x] = Split{(int)((u0 + cu.ntiles - 1) / W) - c0 + 1, b, u, slot};
-    if (mine > 0) wait_pv(last_j);
-    if (tree_bad && r == 0) raise_error(p.dev_err, SPEC_DEVERR_TREE);
+      p.split[blockIdx.x] = Split{(int)((u0 + cu.ntiles - 1) / W) - c0 + 1, cu.b, cu.g, slot};
+    if (mine > 0) wait_pv(item - 1);
+    if (tree_bad && st == 0) raise_error(p.dev_err, SPEC_DEVERR_TREE);
     if (tree_bad || dead) l = __int_as_float(0x7fc00000);  // no result: the row is zeros
-    float L = l, M = m, f[2] = {0.f, 0.f};  // factors of the accumulators
-    if constexpr (C::DUAL && MT == 1) {
-      // both warpgroups hold the same rows, over different keys: each writes half of the columns of their sum
-      s_ml[h * kRows + r] = make_float2(m, l);
-      tc_fence_before();
-      named_sync(kBarSoftmax, kSoftmaxThreads);
-      tc_fence_after();
-      const float2 a = s_ml[r], c = s_ml[kRows + r];
-      M = fmaxf(a.x, c.x);
-      const float w0 = a.x == -INFINITY ? 0.f : fast_exp2(a.x - M), w1 = c.x == -INFINITY ? 0.f : fast_exp2(c.x - M);
-      L = a.y * w0 + c.y * w1;
-      if (a.y != a.y || c.y != c.y) L = __int_as_float(0x7fc00000);
-      f[0] = w0;
-      f[1] = w1;
+    // Threads of a row: the two halves of its stream; with one row tile on two streams all four, which then write a
+    // quarter of the columns of both accumulators' sum each.
+    float L, M = m, f[2] = {1.f, 0.f};  // factors of the accumulators
+    s_x[wg * kRows + r] = l;
+    if (JOIN) s_x[(4 + wg) * kRows + r] = m;
+    tc_fence_before();
+    if (JOIN) named_sync(kBarSoftmax, kSoftmaxThreads);
+    else named_sync(bar, 256);
+    tc_fence_after();
+    if constexpr (JOIN) {
+      const float m0 = s_x[4 * kRows + r], m1 = s_x[6 * kRows + r];
+      M = fmaxf(m0, m1);
+      f[0] = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M);
+      f[1] = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
+      L = (s_x[r] + s_x[kRows + r]) * f[0] + (s_x[2 * kRows + r] + s_x[3 * kRows + r]) * f[1];
     } else {
-      f[0] = 1.f;
+      L = s_x[2 * h * kRows + r] + s_x[(2 * h + 1) * kRows + r];
     }
-    // read here: a warpgroup without a tile of the unit knows only now that the unit was loaded
+    // read here: a stream without a tile of the unit knows only now that the unit was loaded
     const bool bad = s_bad[seq & 7] != 0;
     if (bad && tid == 128) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
     if (bad) L = __int_as_float(0x7fc00000);
@@ -744,44 +804,40 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     const float inv = some ? 1.f / L : 0.f;
     f[0] *= inv;
     f[1] *= inv;
-    const int64_t row = row_offset(p, D, MT, b, u, mt, r);
-    if (!whole && (h == 0 || MT == 2))
+    const int64_t row = row_offset(p, D, MT, cu.b, cu.g, mt, r);
+    constexpr int COLS = JOIN ? D / 4 : D / 2;  // columns of a thread
+    const int part = JOIN ? wg : half;
+    if (!whole && part == 0)
       p.lse[((int64_t)slot * MT + mt) * kRows + r] = some ? M + __log2f(L) : (L == 0.f ? -INFINITY : L);
-    constexpr int COLS = (C::DUAL && MT == 1) ? D / 2 : D;
-    const int col0 = (C::DUAL && MT == 1) ? h * COLS : 0;
-    const uint32_t t_acc = (C::DUAL && MT == 1) ? tmem + (uint32_t)C::COL_O + lanes : t_o;
+    const uint32_t t_acc = JOIN ? tmem + (uint32_t)C::COL_O + lanes : t_o;
     // an accumulator that got no tile of the unit holds anything
-    const bool has0 = !(C::DUAL && MT == 1) || (done & 1) == 0 || n > 1, has1 = (C::DUAL && MT == 1) && ((done & 1) == 1 || n > 1);
+    const bool has0 = !JOIN || (done & 1) == 0 || n > 1, has1 = JOIN && ((done & 1) == 1 || n > 1);
 #pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-      float o[32], o1[32];
-      if (has0) {
-        tmem_ld16(t_acc + col0 + c, *reinterpret_cast<float(*)[16]>(&o[0]));
-        tmem_ld16(t_acc + col0 + c + 16, *reinterpret_cast<float(*)[16]>(&o[16]));
-      }
-      if (has1) {
-        tmem_ld16(t_acc + D + col0 + c, *reinterpret_cast<float(*)[16]>(&o1[0]));
-        tmem_ld16(t_acc + D + col0 + c + 16, *reinterpret_cast<float(*)[16]>(&o1[16]));
-      }
-      tmem_wait_ld_regs<32>(o);
-      if (has1) tmem_wait_ld_regs<32>(o1);
+    for (int c = part * COLS; c < (part + 1) * COLS; c += 16) {
+      float o[16], o1[16];
+      if (has0) tmem_ld16(t_acc + c, o);
+      if (has1) tmem_ld16(t_acc + D + c, o1);
+      tmem_wait_ld_regs<16>(o);
+      if (has1) tmem_wait_ld_regs<16>(o1);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 16; ++i) {
         float a = has0 ? o[i] * f[0] : 0.f;
         if (has1) a = fmaf(o1[i], f[1], a);
         o[i] = some ? a : 0.f;
       }
       if (whole) {
-        if (row >= 0) store_row32<C::FP16>(p, row + col0 + c, o);
+        if (row >= 0) store_row<C::FP16>(p, row + c, o);
       } else {
-        float4* dst = p.opart + (((int64_t)slot * MT + mt) * (D / 4) + (col0 + c) / 4) * kRows + r;
+        float4* dst = p.opart + (((int64_t)slot * MT + mt) * (D / 4) + c / 4) * kRows + r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) dst[i * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
     }
-    if constexpr (C::DUAL && MT == 1) {
+    // The next unit's first product waits for weights of every warp of its stream. With a join the other stream reads
+    // this one's accumulator and statistics too.
+    if constexpr (JOIN) {
       tc_fence_before();
-      named_sync(kBarSoftmax, kSoftmaxThreads);  // both accumulators are read, s_ml is free
+      named_sync(kBarSoftmax, kSoftmaxThreads);
       tc_fence_after();
     }
     done += n;
@@ -789,7 +845,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     cursor_advance(cu, s_prefix, B, U);
   }
   tc_fence_before();
-  named_sync(kBarTail, 32 * C::ISSUERS + kSoftmaxThreads);
+  named_sync(kBarTail, 32 + kSoftmaxThreads);
 }
 
 // Joins the pieces of the units that were cut: CTA (c, chunk) the 32 columns `chunk` of a row tile of the unit whose
@@ -837,7 +893,8 @@ __global__ void __launch_bounds__(kRows) tree_merge_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[i] *= inv;
   }
-  store_row32<C::FP16>(p, row + c4 * 4, acc);
+  store_row<C::FP16>(p, row + c4 * 4, acc);
+  store_row<C::FP16>(p, row + c4 * 4 + 16, acc + 16);
 }
 
 // Host side, one translation unit per head dim: the instance for a call. `settings` gets its grid and ring slots.
@@ -850,8 +907,11 @@ struct Call {
   CUtensorMap tq, tk, tv;
   cudaStream_t stream;
 };
-// tile(): keys per tile of the instance for head dim D, `terms` parts of P.
-inline int tile_keys(int D, int terms) { return (D == 256 || terms == 3) ? 64 : 128; }
+// Row tiles of a unit (1 or 2) where a call has several: two need two accumulators.
+template <int D, int TERMS>
+constexpr int max_row_tiles() {
+  return Cfg<D, 1, TERMS, false>::STREAMS;
+}
 template <int D>
 int settings(int mt, int terms, bool fp16, int batch, Launch* l);
 template <int D>

@@ -10,7 +10,6 @@ namespace tattn {
 template <class C>
 static int settings_of(int batch, Launch* l) {
   static LaunchMemo memo;
-  static bool regs_ok[kMaxDevices];
   const int dev = current_device();
   if (dev < 0) return SPEC_ERR_LAUNCH;
   auto kern = tree_attention_kernel<C>;
@@ -22,20 +21,18 @@ static int settings_of(int batch, Launch* l) {
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
         cudaFuncGetAttributes(&attr, kern) != cudaSuccess)
       return SPEC_ERR_LAUNCH;
-    // the register exchange inside the kernel must not ask for more than the launch brought
-    regs_ok[dev] = !C::DUAL || attr.numRegs >= kLaunchRegs;
+    // the register exchange inside the kernel must not ask for more than the launch brings
+    if (C::STREAMS == 2 && attr.numRegs < kLaunchRegs) return SPEC_ERR_LAUNCH;
     if (!grant_smem_locked(memo, (const void*)kern, dev, (size_t)optin)) return SPEC_ERR_LAUNCH;
     memo.grid[dev] = sms > kMaxGrid ? kMaxGrid : sms;
   }
-  if (!regs_ok[dev]) return SPEC_ERR_LAUNCH;
   const size_t fixed = smem_fixed<C>(batch), room = memo.granted[dev];
-  if (fixed + (size_t)kMinSlots * C::SLOT > room) return SPEC_ERR_UNSUPPORTED;
-  const size_t fit = (room - fixed) / C::SLOT;
+  const size_t fit = fixed < room ? (room - fixed) / C::SLOT : 0;
   const int slots = fit > kMaxSlots ? kMaxSlots : (int)fit;
-  // one row tile on two issuers: tiles alternate between them, so depths are even and a slot is one issuer's
-  l->vslots = (C::DUAL && C::MT == 1) ? slots / 4 * 2 : slots / 2;
-  l->kslots = (C::DUAL && C::MT == 1) ? l->vslots : slots - l->vslots;
-  l->smem = fixed + (size_t)(l->kslots + l->vslots) * C::SLOT;
+  l->vslots = slots / 2;
+  l->kslots = slots - l->vslots;
+  if (l->vslots < C::kMinV) return SPEC_ERR_UNSUPPORTED;
+  l->smem = fixed + (size_t)slots * C::SLOT;
   l->grid = memo.grid[dev];
   return SPEC_OK;
 }
@@ -61,7 +58,10 @@ static int launch_of(const Launch& l, const Call& c) {
 template <int D, int MT, class F>
 static int with_terms(int terms, bool fp16, F fn) {
   if (fp16) return terms == 1 ? fn(Cfg<D, MT, 1, true>{}) : fn(Cfg<D, MT, 2, true>{});
-  return terms == 1 ? fn(Cfg<D, MT, 1, false>{}) : fn(Cfg<D, MT, 3, false>{});
+  if constexpr (MT <= max_row_tiles<D, 3>()) {
+    if (terms == 3) return fn(Cfg<D, MT, 3, false>{});
+  }
+  return fn(Cfg<D, MT, 1, false>{});
 }
 template <int D, class F>
 static int with_instance(int mt, int terms, bool fp16, F fn) {

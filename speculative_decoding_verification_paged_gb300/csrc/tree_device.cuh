@@ -13,7 +13,8 @@ constexpr int kMaxNodes = 64;  // a node's ancestors fit one 64-bit word
 
 // Whether entry i of the parent table `par` (any readable pointer) is allowed: unused, without a
 // parent, or the child of an earlier used node; node 0 has no parent.
-__device__ __forceinline__ bool parent_ok(const int32_t* par, int i) {
+template <typename T>
+__device__ __forceinline__ bool parent_ok(const T* par, int i) {
   const int p = par[i];
   if (p == SPEC_TREE_UNUSED || p == SPEC_TREE_ROOT) return true;
   return p >= 0 && p < i && par[p] != SPEC_TREE_UNUSED;
@@ -21,7 +22,8 @@ __device__ __forceinline__ bool parent_ok(const int32_t* par, int i) {
 
 // Bit j set: node i sees node j, i itself and its ancestors; 0 for an unused node. The walk goes to
 // ever smaller indices, so it ends whatever the table holds.
-__device__ __forceinline__ uint64_t ancestors(const int32_t* par, int i) {
+template <typename T>
+__device__ __forceinline__ uint64_t ancestors(const T* par, int i) {
   int p = par[i];
   if (p == SPEC_TREE_UNUSED) return 0;
   uint64_t m = 1ull << i;
