@@ -432,6 +432,11 @@ TREE_ROOT, TREE_UNUSED = -1, -2
 _DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    """Handle of the stream to launch on; the current one without an argument."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+
+
 def _is(t, dtype, shape, dev: int) -> bool:
     return isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev \
         and t.shape == shape and t.is_contiguous()
@@ -479,7 +484,7 @@ def spec_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, parents, out
     rc = lib.spec_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  ctx_lens.data_ptr(), parents.data_ptr(), N, out.data_ptr(), _DTYPE_CODES[q.dtype],
                                  _DTYPE_CODES[out.dtype], ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
-                                 _err_ptr(dev_err), _stream_handle(stream))
+                                 _err_ptr(dev_err), _stream_of(stream, dev))
     _check("spec_tree_attention", rc)
     return out
 
@@ -504,7 +509,7 @@ def spec_tree_accept(target_logits, tokens, parents, draft_probs, philox_seed: i
                               None if draft_probs is None else draft_probs.data_ptr(),
                               int(philox_seed) & 0xFFFFFFFFFFFFFFFF, mode.data_ptr(), temperature.data_ptr(),
                               out_tokens.data_ptr(), path.data_ptr(), accept_len.data_ptr(), B, N, V,
-                              _err_ptr(dev_err), _stream_handle(stream))
+                              _err_ptr(dev_err), _stream_of(stream, dev))
     _check("spec_tree_accept", rc)
     return out_tokens, path, accept_len
 
@@ -540,7 +545,7 @@ def spec_cache_commit_path(k_cache, v_cache, block_table, ctx_lens, path, accept
     d = _CacheDesc(B, layers, page, block_table.shape[1], pages, token_bytes)
     rc = lib.spec_cache_commit_path(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(),
                                     path.data_ptr(), accept_len.data_ptr(), new_lens.data_ptr(), N, ctypes.byref(d),
-                                    _err_ptr(dev_err), _stream_handle(stream))
+                                    _err_ptr(dev_err), _stream_of(stream, dev))
     _check("spec_cache_commit_path", rc)
     return new_lens
 
@@ -584,6 +589,6 @@ def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: in
                                None if src_rows is None else src_rows.data_ptr(),
                                None if k_cache is None else k_cache.data_ptr(),
                                None if v_cache is None else v_cache.data_ptr(), ctypes.byref(d), workspace.data_ptr(),
-                               workspace.numel(), _err_ptr(dev_err), _stream_handle(stream))
+                               workspace.numel(), _err_ptr(dev_err), _stream_of(stream, dev))
     _check("spec_cache_update", rc)
     return block_table, page_refs

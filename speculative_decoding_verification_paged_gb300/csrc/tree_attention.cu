@@ -29,7 +29,10 @@ static bool shape_supported(const spec_attn_desc* d, int nodes) {
   if (bs != 16 && bs != 32 && bs != 64 && bs != 128) return false;
   if (nodes > tree::kMaxNodes || d->num_q_heads / d->num_kv_heads > kMaxGqa || d->batch > kMaxBatch) return false;
   const int64_t longest = (int64_t)d->max_blocks_per_seq * bs;
-  if (longest > INT32_MAX / 2 || (longest / 64 + 1) * d->batch > INT32_MAX) return false;  // tile counts are 32-bit
+  if (longest > INT32_MAX / 2) return false;
+  // tile counts of all units are 32-bit (units: at most N row tiles a kv head)
+  const int most = kRows / (d->num_q_heads / d->num_kv_heads), tiles = (nodes + most - 1) / most;
+  if ((longest / 64 + 1) * d->batch > INT32_MAX / ((int64_t)d->num_kv_heads * tiles)) return false;
   return (int64_t)d->num_blocks * bs <= INT32_MAX;  // TMA row coordinates are 32-bit
 }
 
@@ -41,7 +44,7 @@ static int streams_for(int D, int terms) {  // accumulators of the instance
   switch (D) {
     case 64: return terms == 3 ? Cfg<64, 1, 3, false>::STREAMS : Cfg<64, 1, 1, false>::STREAMS;
     case 128: return terms == 3 ? Cfg<128, 1, 3, false>::STREAMS : Cfg<128, 1, 1, false>::STREAMS;
-    default: return terms == 3 ? Cfg<256, 1, 3, false>::STREAMS : Cfg<256, 1, 1, false>::STREAMS;
+    default: return Cfg<256, 1, 3, false>::STREAMS;
   }
 }
 static Rows rows_for(const spec_attn_desc* d, int nodes, int terms) {
@@ -55,14 +58,15 @@ static Rows rows_for(const spec_attn_desc* d, int nodes, int terms) {
 }
 
 struct Layout {
-  size_t lse, opart, total;
+  size_t lse, opart, folds, total;
 };
-static Layout layout_for(const spec_attn_desc* d, int nodes) {
+static Layout layout_for(const spec_attn_desc* d, int nodes) {  // room for any output type
   Layout L;
-  const size_t slots = 2 * (size_t)kMaxGrid * rows_for(d, nodes, 1).mt;  // the most of any output type
-  L.lse = attn::align256(kMaxGrid * sizeof(Split));
+  const size_t slots = 2 * (size_t)kMaxGrid * rows_for(d, nodes, 1).mt, row_tile = (size_t)kRows * d->head_dim * 4;
+  L.lse = attn::align256(kMaxGrid * 4);
   L.opart = L.lse + attn::align256(slots * kRows * 4);
-  L.total = L.opart + slots * kRows * d->head_dim * 4;
+  L.folds = L.opart + slots * row_tile;
+  L.total = L.folds + (size_t)kMaxGrid * streams_for(d->head_dim, 1) * row_tile;
   return L;
 }
 
@@ -93,10 +97,10 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   if (workspace == nullptr || workspace_bytes < L.total) return SPEC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return SPEC_ERR_INVALID_ARG;
 
-  // Parts of P: one where the output is rounded to the input type anyway; for fp32 output as many as keep 22 to 24
-  // bits of it (two fp16 parts, three bf16 ones).
+  // Parts of P: one where the output is rounded to the input type anyway; for fp32 output as many as keep 22 to 24 bits
+  // of it (two fp16 parts, three bf16 ones; two bf16 parts alone would be 2.2e-6 off).
   const bool fp16 = dtype == SPEC_DTYPE_FP16;
-  const int D = d->head_dim, terms = out_dtype == SPEC_DTYPE_FP32 ? (fp16 ? 2 : 3) : 1;
+  const int D = d->head_dim, terms = out_dtype != SPEC_DTYPE_FP32 ? 1 : fp16 ? 2 : 3;
   const tattn::Rows rows = tattn::rows_for(d, num_nodes, terms);
   tattn::Launch l;
   int rc;
@@ -114,9 +118,10 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   p.ctx_lens = ctx_lens;
   p.parents = parents;
   p.out = out;
-  p.split = reinterpret_cast<tattn::Split*>(ws);
+  p.counters = reinterpret_cast<int32_t*>(ws);
   p.lse = reinterpret_cast<float*>(ws + L.lse);
   p.opart = reinterpret_cast<float4*>(ws + L.opart);
+  p.folds = reinterpret_cast<float4*>(ws + L.folds);
   p.dev_err = dev_err;
   p.num_blocks = d->num_blocks;
   p.batch = d->batch;
@@ -132,6 +137,7 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   p.kslots = l.kslots;
   p.vslots = l.vslots;
   p.out_f32 = out_dtype == SPEC_DTYPE_FP32;
+  p.out_wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   c.stream = reinterpret_cast<cudaStream_t>(stream_);
 

@@ -15,33 +15,31 @@ namespace tattn {
 using attn::Cursor;
 using attn::cursor_advance;
 using attn::cursor_at;
-using attn::piece_slot;
+
+// Partial slot of the piece of unit [u0, ...) held by CTA c: slot 0 for a CTA's first unit, slot 1 for its last one (the
+// units between are whole).
+__device__ __forceinline__ int piece_slot(int c, int c0, int u0, int W) { return 2 * c + ((c == c0 && u0 > c * W) ? 1 : 0); }
 
 constexpr int kMaxGrid = 160;  // one CTA per SM, at most
 constexpr int kMaxSlots = 10;  // K and V tiles in shared memory
 constexpr int kTmemCols = 512;
 constexpr int kLaunchRegs = 96;  // registers a thread that a kernel of 640 threads is launched with
+constexpr int kCutBytes = 8 * 32768;  // see tiles_per_cta
 constexpr int kTables = 576;   // bytes of shared memory for barriers and small tables
 constexpr int kRows = 128;     // packed query rows of a row tile (MMA M)
 constexpr int kBarStream = 1;  // named barriers: the softmax threads of a stream (1, 2),
 constexpr int kBarSoftmax = 3; // all softmax threads,
 constexpr int kBarTail = 4;    // softmax threads and the issuing warp
 
-// What the merge needs of a unit cut over several CTAs; written by the CTA that holds its first piece.
-struct Split {
-  int32_t nseg;  // pieces; 0: no unit starts here that is cut
-  int32_t b, u;  // sequence, unit of the sequence
-  int32_t slot;  // partial slot of the first piece; the others are slots 2 (c + 1), 2 (c + 2), ...
-};
-
 struct Params {
   const int32_t* block_table;
   const int32_t* ctx_lens;
   const int32_t* parents;
   void* out;
-  Split* split;  // [kMaxGrid]
-  float* lse;    // [2 * kMaxGrid][row tiles of a unit][128], log2 units; NaN: no result
-  float4* opart; // [2 * kMaxGrid][row tiles of a unit][D / 4][128], normalised
+  int32_t* counters;  // [kMaxGrid], zero between calls: pieces that met at the border before CTA c
+  float* lse;         // [2 * kMaxGrid][row tiles of a unit][128], log2 units; NaN: no result
+  float4* opart;      // [2 * kMaxGrid][row tiles of a unit][D / 4][128], normalised
+  float4* folds;      // [kMaxGrid][streams][D / 4][128], see fold
   int32_t* dev_err;
   int64_t num_blocks;
   int batch, nodes, heads, kv_heads, gqa;
@@ -49,7 +47,7 @@ struct Params {
   int groups;  // units per kv head
   int page_shift, max_blocks;
   int kslots, vslots;  // depths of the K and the V ring
-  int out_f32;
+  int out_f32, out_wide;  // fp32 output; output 32-byte aligned
   float scale_log2;
 };
 
@@ -79,6 +77,10 @@ struct Cfg {
   static constexpr int COL_O = BUFS * SW;
   static constexpr int X_BYTES = 2 * STREAMS * kRows * 4 * (JOIN ? 2 : 1);  // row statistics exchanged by warpgroups
   static constexpr int kMinV = 2;                                           // V slots at least, see wait_v
+  // Items after which an accumulator is folded into fp32 sums in memory, 0: never. The tensor core cuts each sum it adds
+  // to instead of rounding it, so an accumulator loses about 1.3e-8 of itself with every MMA; 512 keys keep that at the
+  // size of fp32's own errors. (Output of 16 bits does not show it: 1e-4 after 128K keys.)
+  static constexpr int FOLD = TERMS > 1 ? 512 / TK : 0;
   static_assert(MT <= STREAMS, "two row tiles need two accumulators");
   static_assert(COL_O + STREAMS * D <= kTmemCols, "S / P buffers and accumulators fit tensor memory");
   static_assert(TERMS >= 1 && TERMS <= 3 && kMinV >= AHEAD, "");
@@ -241,19 +243,39 @@ __device__ __forceinline__ uint64_t window(uint64_t m, int o) {
   return o < 64 ? m >> o : 0ull;
 }
 
+// 32 bytes at once.
+__device__ __forceinline__ void store32(void* at, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 // Write 16 consecutive columns of one output row (element offset `at`).
 template <bool FP16>
 __device__ __forceinline__ void store_row(const Params& p, int64_t at, const float* v) {
+  uint32_t w[8];
   if (p.out_f32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+    float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int c = 0; c < 16; c += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[c + i]);
+      if (p.out_wide) {
+        store32(o + c, w);
+      } else {
+        reinterpret_cast<uint4*>(o + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(o + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
   } else {
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      o[i] = make_uint4(pack2<FP16>(v[8 * i], v[8 * i + 1]), pack2<FP16>(v[8 * i + 2], v[8 * i + 3]),
-                        pack2<FP16>(v[8 * i + 4], v[8 * i + 5]), pack2<FP16>(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < 8; ++i) w[i] = pack2<FP16>(v[2 * i], v[2 * i + 1]);
+    if (p.out_wide) {
+      store32(o, w);
+    } else {
+      reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 
@@ -263,6 +285,19 @@ __device__ __forceinline__ int64_t row_offset(const Params& p, int D, int MT, in
   const int i = (rg * MT + mt) * p.npt + r / p.gqa, j = r % p.gqa;
   if (r >= p.npt * p.gqa || i >= p.nodes) return -1;
   return (((int64_t)b * p.nodes + i) * p.heads + g * p.gqa + j) * D;
+}
+
+// Tiles per CTA. An even split cuts a unit at every CTA's border; each cut costs the end of a unit (2 to 4 us) on two
+// CTAs, and the first one the merge (7 us). Where all units have the same length (unit_tiles > 0), whole units are taken
+// instead if the busiest CTA then has at most kCutBytes of K more than the even split gives it.
+template <class C>
+__device__ __forceinline__ int tiles_per_cta(int T, int unit_tiles, int grid) {
+  const int even = (T + grid - 1) / grid;
+  if (unit_tiles > 0) {
+    const int whole = (T / unit_tiles + grid - 1) / grid * unit_tiles;
+    if (whole <= even + kCutBytes / C::SLOT) return whole;
+  }
+  return even;
 }
 
 template <class C>
@@ -359,7 +394,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       mbar_init(q_full, 1);
       mbar_init(q_empty, 1);
       fence_mbar_init();
-      p.split[blockIdx.x].nseg = 0;
     }
     __syncthreads();
   }
@@ -373,13 +407,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + b * bytes);
     for (int64_t i = tid; i < bytes / 16; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
   }
-  const int64_t T = (int64_t)s_prefix[B] * U;
+  const int T = s_prefix[B] * U;  // the host made sure that it fits
   if (T == 0) return;
-  const int64_t W = (T + gridDim.x - 1) / gridDim.x;
-  const int64_t f0 = (int64_t)blockIdx.x * W;
-  const int64_t f1 = min(T, f0 + W);
+  const int W = tiles_per_cta<C>(T, s_misc[22] == s_misc[23] ? s_misc[23] : 0, (int)gridDim.x);
+  const int f0 = min(T, (int)blockIdx.x * W), f1 = min(T, f0 + W);
   if (f0 >= f1) return;
-  const int n_tiles = (int)(f1 - f0);
+  const int n_tiles = f1 - f0;
 
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), kTmemCols);
@@ -499,8 +532,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
           }
         }
         __syncwarp();
-        fresh = c.seq;
       }
+      fresh = c.seq;
     }
     return;
   }
@@ -568,7 +601,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
         wait(&p_full[x], j >> 1);
         tc_fence_after();
         const uint32_t vb = v_lo + sv * (C::SLOT >> 4), d = tm + (uint32_t)(C::COL_O + (C::STREAMS == 2 ? x * D : 0));
-        const bool first = in_unit < C::STREAMS;  // nothing of the unit is in the accumulator
+        const int nth = in_unit / C::STREAMS;  // item of its stream in the unit
+        const bool first = C::FOLD > 0 ? nth % (C::FOLD > 0 ? C::FOLD : 1) == 0 : nth == 0;  // the accumulator starts anew
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
@@ -625,16 +659,66 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     tc_fence_after();
   };
 
+  // Adds the stream's accumulator, which holds the products up to item `last`, to its sums in memory (`again`: they hold
+  // earlier folds, relative to the maximum m_fold), and leaves the result there, or in the accumulator (`back`). Each half
+  // of the stream does half of the columns. The loads go out before the product is waited for, 64 columns at a time.
+  auto fold = [&](float m_, float m_fold, bool again, bool back, int last) {
+    constexpr int CH = D / 2 < 64 ? D / 2 : 64;
+    float4* sums = p.folds + ((int64_t)blockIdx.x * C::STREAMS + h) * (D / 4) * kRows + r;
+    const float e = again && m_fold > -INFINITY ? fast_exp2(m_fold - m_) : 0.f;
+#pragma unroll 1
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += CH) {
+      float4 a[CH / 4];
+#pragma unroll
+      for (int i = 0; i < CH / 4; ++i)
+        a[i] = again && r < packed ? __ldcg(sums + (c / 4 + i) * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c == half * (D / 2)) wait_pv(last);
+#pragma unroll
+      for (int k = 0; k < CH; k += 16) {
+        float o[16];
+        tmem_ld16(t_o + c + k, o);
+        tmem_wait_ld_regs<16>(o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4& s = a[k / 4 + i];
+          s.x = o[4 * i] = fmaf(s.x, e, o[4 * i]);
+          s.y = o[4 * i + 1] = fmaf(s.y, e, o[4 * i + 1]);
+          s.z = o[4 * i + 2] = fmaf(s.z, e, o[4 * i + 2]);
+          s.w = o[4 * i + 3] = fmaf(s.w, e, o[4 * i + 3]);
+        }
+        if (back) tmem_st16(t_o + c + k, o);
+      }
+      if (!back && r < packed) {
+#pragma unroll
+        for (int i = 0; i < CH / 4; ++i) __stcg(sums + (c / 4 + i) * kRows, a[i]);
+      }
+    }
+    if (back) tmem_wait_st();
+  };
+
+  // Pieces of units that are cut, joined when the CTA is done: its first unit's and its last one's.
+  struct Piece {
+    int b, u, c0, nseg;
+  } cut[2];
+  int n_cut = 0;
+
   Cursor cu = cursor_at(f0, s_prefix, B, U);
   int done = 0;  // tiles of this CTA before the unit
   int item = 0;  // items of this stream before the current one
-  for (int seq = 0; done < n_tiles; ++seq) {
+  int base = p.ctx_lens[cu.b] - N, base_next = base;  // committed tokens of the unit's sequence and of the next unit's
+  for (int seq = 0; done < n_tiles; ++seq, base = base_next) {
     const int n = min(cu.ntiles - cu.tile, n_tiles - done);
-    const int base = p.ctx_lens[cu.b] - N;
+    if (cu.g == U - 1 && done + n < n_tiles) {  // asked for here: the unit's tiles hide the latency
+      Cursor nx = cu;
+      nx.tile = nx.ntiles - 1;
+      cursor_advance(nx, s_prefix, B, U);
+      base_next = p.ctx_lens[nx.b] - N;
+    }
     float m = -INFINITY, l = 0.f;  // running maximum (scaled; it may lag by up to 8), the thread's share of the row's sum
     bool tree_bad = false, dead = false, have_tree = false;
     uint64_t sees = 0;
     int mine = 0;  // items of this stream in the unit so far
+    [[maybe_unused]] float m_fold = -INFINITY;  // the maximum that the folded sums are relative to
     // the stream's first tile: every tile, or every other one of the CTA's
 #pragma unroll 1
     for (int tt = JOIN ? ((done & 1) == h ? 0 : 1) : 0; tt < n; tt += JOIN ? 2 : 1, ++item, ++mine) {
@@ -762,6 +846,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       l0 = add2(l0, l1);
       l += l0.x + l0.y;
       tmem_wait_st();
+      if constexpr (C::FOLD > 0) {
+        if (mine > 0 && mine % C::FOLD == 0) {  // this item's product starts the accumulator anew
+          fold(m, m_fold, mine > C::FOLD, false, item - 1);
+          m_fold = m;
+        }
+      }
       if (edge) fence_proxy_async_smem();  // zeroed rows of V
       tc_fence_before();
       __syncwarp();
@@ -770,12 +860,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
 
     // ---- the unit's rows: output, or a normalised partial and its log-sum-exp
     const bool whole = cu.tile == 0 && n == cu.ntiles;
-    const int64_t u0 = (int64_t)s_prefix[cu.b] * U + (int64_t)cu.g * cu.ntiles;
-    const int c0 = (int)(u0 / W);
-    const int slot = piece_slot((int)blockIdx.x, c0, u0, W);
-    if (!whole && cu.tile == 0 && tid == 128)
-      p.split[blockIdx.x] = Split{(int)((u0 + cu.ntiles - 1) / W) - c0 + 1, cu.b, cu.g, slot};
+    int slot = 0;
+    if (!whole) {
+      const int u0 = s_prefix[cu.b] * U + cu.g * cu.ntiles, c0 = u0 / W;
+      slot = piece_slot((int)blockIdx.x, c0, u0, W);
+      cut[n_cut++] = Piece{cu.b, cu.g, c0, (u0 + cu.ntiles - 1) / W - c0 + 1};
+    }
     if (mine > 0) wait_pv(item - 1);
+    if constexpr (C::FOLD > 0) {
+      if (mine > C::FOLD) fold(m, m_fold, true, true, item - 1);
+    }
     if (tree_bad && st == 0) raise_error(p.dev_err, SPEC_DEVERR_TREE);
     if (tree_bad || dead) l = __int_as_float(0x7fc00000);  // no result: the row is zeros
     // Threads of a row: the two halves of its stream; with one row tile on two streams all four, which then write a
@@ -812,7 +906,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     const uint32_t t_acc = JOIN ? tmem + (uint32_t)C::COL_O + lanes : t_o;
     // an accumulator that got no tile of the unit holds anything
     const bool has0 = !JOIN || (done & 1) == 0 || n > 1, has1 = JOIN && ((done & 1) == 1 || n > 1);
-#pragma unroll 1
+#pragma unroll
     for (int c = part * COLS; c < (part + 1) * COLS; c += 16) {
       float o[16], o1[16];
       if (has0) tmem_ld16(t_acc + c, o);
@@ -846,55 +940,74 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
   }
   tc_fence_before();
   named_sync(kBarTail, 32 + kSoftmaxThreads);
-}
 
-// Joins the pieces of the units that were cut: CTA (c, chunk) the 32 columns `chunk` of a row tile of the unit whose
-// first piece CTA c of the kernel above held; out = sum_k w_k part_k / sum_k w_k, w_k = 2^(lse_k - max lse).
-template <class C>
-__global__ void __launch_bounds__(kRows) tree_merge_kernel(const Params p) {
-  constexpr int D = C::D, MT = C::MT;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int4 sv = __ldcg(reinterpret_cast<const int4*>(p.split) + blockIdx.x);
-  const Split s{sv.x, sv.y, sv.z, sv.w};
-  if (s.nseg == 0) return;
-  const int r = threadIdx.x, mt = blockIdx.y / (D / 32), c4 = (blockIdx.y % (D / 32)) * 8;
-  const int64_t row = row_offset(p, D, MT, s.b, s.u, mt, r);
-  if (row < 0) return;
-  auto slot = [&](int k) -> int64_t { return ((k == 0 ? s.slot : 2 * ((int64_t)blockIdx.x + k)) * MT + mt); };
-  float M = -INFINITY;
-  bool nan = false;
-#pragma unroll 4
-  for (int k = 0; k < s.nseg; ++k) {
-    const float v = __ldcg(p.lse + slot(k) * kRows + r);
-    nan |= v != v;
-    M = fmaxf(M, v);
-  }
-  const bool some = !nan && M > -INFINITY;
-  float acc[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-  float Z = 0.f;
-  if (some) {
+  // ---- join the pieces of cut units, in pairs: of two neighbouring runs of pieces the CTA that comes second joins them
+  //   out = sum w_k part_k / sum w_k, w_k = 2^(lse_k - max lse),
+  // and goes on with the longer run; nobody waits. The counter of a pair is that of the border CTA between its runs.
+  constexpr int COLS = JOIN ? D / 4 : D / 2;
+  const int part = JOIN ? wg : half;
+  for (int k = 0; k < n_cut; ++k) {
+    const Piece c = cut[k];
+    const int u0 = s_prefix[c.b] * U + c.u * (s_prefix[c.b + 1] - s_prefix[c.b]);
+    int me = (int)blockIdx.x - c.c0;
+    bool going = true;
+    for (int run = 1; run < c.nseg && going; run *= 2) {
+      const int left = me / (2 * run) * (2 * run), right = left + run;
+      if (right >= c.nseg) continue;  // no neighbour on this level
+      named_sync(kBarSoftmax, kSoftmaxThreads);  // the run's stores are issued, s_misc is read
+      if (tid == 128) {
+        __threadfence();
+        const int before = atomicAdd(p.counters + c.c0 + right, 1);
+        if (before != 0) p.counters[c.c0 + right] = 0;
+        __threadfence();
+        s_misc[0] = before;
+      }
+      named_sync(kBarSoftmax, kSoftmaxThreads);
+      going = s_misc[0] != 0;
+      if (!going) break;
+      me = left;
+      const bool last = left == 0 && 2 * run >= c.nseg;
+      const int64_t sl = (int64_t)piece_slot(c.c0 + left, c.c0, u0, W) * MT + mt, sr = (int64_t)2 * (c.c0 + right) * MT + mt;
+      const float ll = __ldcg(p.lse + sl * kRows + r), lr = __ldcg(p.lse + sr * kRows + r);
+      const float M = fmaxf(ll, lr);
+      const bool some = ll == ll && lr == lr && M > -INFINITY;
+      const float wl = some ? fast_exp2(ll - M) : 0.f, wr = some ? fast_exp2(lr - M) : 0.f, inv = some ? 1.f / (wl + wr) : 0.f;
+      const float fl = wl * inv, fr = wr * inv;
+      const int64_t row = row_offset(p, D, MT, c.b, c.u, mt, r);
+      float4* a = p.opart + sl * (D / 4) * kRows + r;
+      const float4* o = p.opart + sr * (D / 4) * kRows + r;
 #pragma unroll 2
-    for (int k = 0; k < s.nseg; ++k) {
-      const float w = fast_exp2(__ldcg(p.lse + slot(k) * kRows + r) - M);
-      const float4* part = p.opart + (slot(k) * (D / 4) + c4) * kRows + r;
-      Z += w;
+      for (int q = part * COLS; q < (part + 1) * COLS; q += 16) {
+        float v[16];
+        float4 x[4], y[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = __ldcg(part + i * kRows);
-        acc[4 * i] = fmaf(w, v.x, acc[4 * i]);
-        acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
-        acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]);
-        acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          x[i] = __ldcg(a + (q / 4 + i) * kRows);
+          y[i] = __ldcg(o + (q / 4 + i) * kRows);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[4 * i] = x[i].x * fl + y[i].x * fr;
+          v[4 * i + 1] = x[i].y * fl + y[i].y * fr;
+          v[4 * i + 2] = x[i].z * fl + y[i].z * fr;
+          v[4 * i + 3] = x[i].w * fl + y[i].w * fr;
+        }
+        if (last) {
+          if (row >= 0) store_row<C::FP16>(p, row + q, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            __stcg(a + (q / 4 + i) * kRows, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        }
+      }
+      if (!last) {
+        named_sync(kBarSoftmax, kSoftmaxThreads);  // everyone has read the run's lse
+        if (part == 0)
+          __stcg(p.lse + sl * kRows + r,
+                 ll == ll && lr == lr ? (some ? M + __log2f(wl + wr) : -INFINITY) : __int_as_float(0x7fc00000));
       }
     }
-    const float inv = 1.f / Z;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) acc[i] *= inv;
   }
-  store_row<C::FP16>(p, row + c4 * 4, acc);
-  store_row<C::FP16>(p, row + c4 * 4 + 16, acc + 16);
 }
 
 // Host side, one translation unit per head dim: the instance for a call. `settings` gets its grid and ring slots.
@@ -907,11 +1020,6 @@ struct Call {
   CUtensorMap tq, tk, tv;
   cudaStream_t stream;
 };
-// Row tiles of a unit (1 or 2) where a call has several: two need two accumulators.
-template <int D, int TERMS>
-constexpr int max_row_tiles() {
-  return Cfg<D, 1, TERMS, false>::STREAMS;
-}
 template <int D>
 int settings(int mt, int terms, bool fp16, int batch, Launch* l);
 template <int D>

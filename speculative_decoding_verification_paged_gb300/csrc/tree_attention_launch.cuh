@@ -40,25 +40,14 @@ static int settings_of(int batch, Launch* l) {
 template <class C>
 static int launch_of(const Launch& l, const Call& c) {
   tree_attention_kernel<C><<<l.grid, C::kThreads, l.smem, c.stream>>>(c.p, c.tq, c.tk, c.tv);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_LAUNCH;
-  // the merge starts when the kernel before it is done; the early launch hides its launch latency
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)l.grid, (unsigned)(C::MT * (C::D / 32)), 1);
-  cfg.blockDim = dim3(kRows, 1, 1);
-  cfg.stream = c.stream;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<C>, c.p) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 // The instance for a call: fn.template operator()<Cfg>().
 template <int D, int MT, class F>
 static int with_terms(int terms, bool fp16, F fn) {
   if (fp16) return terms == 1 ? fn(Cfg<D, MT, 1, true>{}) : fn(Cfg<D, MT, 2, true>{});
-  if constexpr (MT <= max_row_tiles<D, 3>()) {
+  if constexpr (MT <= Cfg<D, 1, 3, false>::STREAMS) {
     if (terms == 3) return fn(Cfg<D, MT, 3, false>{});
   }
   return fn(Cfg<D, MT, 1, false>{});
