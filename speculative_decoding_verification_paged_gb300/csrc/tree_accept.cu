@@ -7,17 +7,33 @@
 // because max(0, max(0, x) / Z - q) = max(0, x / Z - q): two scalars hold it.
 // Without draft probabilities the residual is p without the refused tokens.
 //
-// Plain form of the kernel: one CTA per row walks its nodes.
+// Design (GB300): the chain call's (accept.cu): one thread-block cluster per row,
+// its CTAs splitting the vocabulary, partials pushed into every CTA of the
+// cluster and counted by mbarriers, so that all warps reach the same decision
+// without a block-wide or cluster-wide barrier. The walk reads the rows of the
+// nodes that it visits and no others: per node one pass for the statistics (or
+// the argmax), one pass for every refused child but the last (the mass of the
+// next residual; none without draft probabilities, where it is 1 minus the
+// refused tokens' share), and one exponential race at the last node; all but the
+// first pass over a row come from L2. Lane l of every warp holds nodes l and
+// l + 32: parent, token, the uniform of its test and, for the children of the
+// current node, the target logit and the draft probability, whose loads are in
+// flight during the statistics pass.
 #include <math.h>
 
+#include <type_traits>
+
+#include "accept_device.cuh"
 #include "tree_device.cuh"
 
 namespace specv {
 namespace tacc {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxVocab = 1 << 30;
+using namespace acc;
+
+constexpr int kNB = 8;  // float4 groups per thread in flight together (statistics, argmax)
+constexpr int kRB = 2;  // float4 groups per thread in flight together (residual passes)
+constexpr float kExactMass = 0.0625f;  // remaining mass below which it is summed instead of subtracted
 
 struct Params {
   const float* logits;
@@ -31,137 +47,455 @@ struct Params {
   int32_t* accept_len;
   int32_t* dev_err;
   uint32_t seed_lo, seed_hi;
-  int nodes, vocab;
+  int batch, nodes, vocab, slice, csize;
+  int vec;  // rows are 16-byte aligned: float4 loads
 };
 
-__global__ void __launch_bounds__(kThreads) tree_accept_kernel(const Params p) {
-  __shared__ int32_t s_par[tree::kMaxNodes], s_tok[tree::kMaxNodes], s_out[tree::kMaxNodes], s_path[tree::kMaxNodes];
-  __shared__ int32_t s_gone[tree::kMaxNodes];
-  __shared__ float s_f[kWarps];
-  __shared__ int32_t s_i[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x, N = p.nodes, V = p.vocab;
-  if (tid < N) {
-    s_par[tid] = p.parents[(int64_t)b * N + tid];
-    s_tok[tid] = p.tokens[(int64_t)b * N + tid];
-    s_out[tid] = s_path[tid] = -1;
+// Registers bound the CTAs resident per SM (768 threads at 80 registers each).
+template <int T>
+__global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p) {
+  constexpr int kWarps = T / 32;
+  constexpr int kStep = kNB * T, kRStep = kRB * T;  // groups per batch of the block
+  constexpr uint32_t kAll = 0xffffffffu;
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int csize = p.csize, rank = (int)cluster_ctarank(), nclusters = (int)(gridDim.x / (unsigned)csize);
+  const int N = p.nodes, V = p.vocab;
+  const int x0 = rank * p.slice;       // a multiple of 4: group g holds Philox counter x0/4 + g
+  const int n = min(p.slice, V - x0);  // >= 1 by construction of the slice
+  const int ngroups = (n + 3) >> 2;
+  const bool vec = p.vec != 0;
+  const int nparts = csize * kWarps;
+  int xs = 0;           // exchanges so far (slot parity)
+  bool joined = false;  // the start-up cluster barrier was waited on
+  if (tid == 0) {
+    mbar_init(&sh.xbar[0], 1);  // the local arrival sets the exchange's byte count
+    mbar_init(&sh.xbar[1], 1);
+    fence_mbar_init();  // visible to the cluster before any peer can push
   }
   __syncthreads();
-  auto block_sum = [&](float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (lane == 0) s_f[warp] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int w = 0; w < kWarps; ++w) v += s_f[w];
+  cluster_arrive_relaxed();
+
+  auto load4 = [&](const float* src, int g, float fill) -> float4 {
+    if (g >= ngroups) return make_float4(fill, fill, fill, fill);
+    if (vec) return __ldg(reinterpret_cast<const float4*>(src) + g);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = 4 * g + e < n ? __ldg(src + 4 * g + e) : fill;
+    return make_float4(v[0], v[1], v[2], v[3]);
+  };
+  auto load_batch = [&](const float* src, int gb, float4 (&v)[kNB]) {
+    if (vec && gb + kStep <= ngroups) {
+      const float4* s4 = reinterpret_cast<const float4*>(src) + gb + tid;
+#pragma unroll
+      for (int i = 0; i < kNB; ++i) v[i] = __ldg(s4 + i * T);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kNB; ++i) v[i] = load4(src, gb + i * T + tid, -INFINITY);
+    }
+  };
+  auto batch_max = [&](const float4 (&v)[kNB]) -> float {
+    float m4[kNB];
+#pragma unroll
+    for (int i = 0; i < kNB; ++i) m4[i] = fmaxf(max3f(v[i].x, v[i].y, v[i].z), v[i].w);
+#pragma unroll
+    for (int w = 1; w < kNB; w *= 2)
+#pragma unroll
+      for (int i = 0; i + w < kNB; i += 2 * w) m4[i] = fmaxf(m4[i], m4[i + w]);
+    return m4[0];
+  };
+  // Push this warp's partial into every CTA of the cluster, then wait for the cluster's partials.
+  auto exchange = [&](float f0, float f1, int i0) -> const Part* {
+    const int slot = xs & 1;
+    const uint32_t parity = (uint32_t)((xs >> 1) & 1);
+    ++xs;
+    if (tid == 0) mbar_arrive_expect_tx(&sh.xbar[slot], (uint32_t)(nparts * (int)sizeof(Part)));
+    if (lane < csize)
+      st_async_v4(map_to_rank(smem_u32(&sh.xch[slot][rank * kWarps + warp]), (uint32_t)lane), f0, f1, i0, 0,
+                  map_to_rank(smem_u32(&sh.xbar[slot]), (uint32_t)lane));
+    if (!mbar_wait_cluster_bounded(&sh.xbar[slot], parity) && lane == 0) raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
+    return sh.xch[slot];
+  };
+  auto warp_best = [&](float& v, int& i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) vi_combine(v, i, __shfl_xor_sync(kAll, v, o), __shfl_xor_sync(kAll, i, o));
+  };
+  auto row_best = [&](const Part* x, float& bv, int& bi) {
+    bv = -INFINITY;
+    bi = INT32_MAX;
+    for (int t = lane; t < nparts; t += 32) vi_combine(bv, bi, x[t].f0, x[t].i0);
+    warp_best(bv, bi);
+  };
+  auto warp_sum = [&](float v) -> float {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
   };
-  auto block_best = [&](float v, int i, float& bv, int& bi) {  // largest value, lowest index on ties
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, v, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, i, o);
-      if (ov > v || (ov == v && oi < i)) v = ov, i = oi;
+
+  for (int b = (int)(blockIdx.x / (unsigned)csize); b < p.batch; b += nclusters) {
+    const float* lrow = p.logits + (int64_t)b * N * V + x0;  // node i's slice at lrow + i V
+    const float* qrow = p.probs ? p.probs + (int64_t)b * N * V + x0 : nullptr;
+    const int md = p.mode[b];
+    const float t_row = p.temperature[b];
+    int par[2], tok[2];  // of nodes lane and lane + 32
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = lane + 32 * i;
+      par[i] = c < N ? p.parents[(int64_t)b * N + c] : SPEC_TREE_UNUSED;
+      tok[i] = c < N ? p.tokens[(int64_t)b * N + c] : 0;
     }
-    __syncthreads();
-    if (lane == 0) s_f[warp] = v, s_i[warp] = i;
-    __syncthreads();
-    bv = s_f[0];
-    bi = s_i[0];
-    for (int w = 1; w < kWarps; ++w)
-      if (s_f[w] > bv || (s_f[w] == bv && s_i[w] < bi)) bv = s_f[w], bi = s_i[w];
-  };
-  const int mode = p.mode[b];
-  const float T = mode == SPEC_MODE_SAMPLE ? p.temperature[b] : 1.f;
-  int m = -1;
-  if (s_par[0] != SPEC_TREE_UNUSED) {
+    float4 v[kNB];
+    load_batch(lrow, 0, v);  // node 0's first batch, in flight during the checks
+    // value of node c out of the two registers that hold all nodes
+    auto of_node = [&](const int (&x)[2], int c) -> int {
+      const int lo = __shfl_sync(kAll, x[0], c & 31), hi = __shfl_sync(kAll, x[1], c & 31);
+      return c & 32 ? hi : lo;
+    };
+    auto of_node_f = [&](const float (&x)[2], int c) -> float {
+      const float lo = __shfl_sync(kAll, x[0], c & 31), hi = __shfl_sync(kAll, x[1], c & 31);
+      return c & 32 ? hi : lo;
+    };
+    // nodes with a property, as a 64-bit mask
+    auto nodes_with = [&](bool a, bool c) -> uint64_t {
+      return (uint64_t)__ballot_sync(kAll, a) | ((uint64_t)__ballot_sync(kAll, c) << 32);
+    };
+    const int par0 = __shfl_sync(kAll, par[0], 0);
     int err = 0;
-    if (mode != SPEC_MODE_GREEDY && mode != SPEC_MODE_SAMPLE) err |= SPEC_DEVERR_MODE;
-    if (!(T > 0.f) || !isfinite(T)) err |= SPEC_DEVERR_TEMPERATURE;
-    if (__syncthreads_or(tid < N && !tree::parent_ok(s_par, tid))) err |= SPEC_DEVERR_TREE;
-    if (__syncthreads_or(tid > 0 && tid < N && s_par[tid] != SPEC_TREE_UNUSED && (s_tok[tid] < 0 || s_tok[tid] >= V)))
-      err |= SPEC_DEVERR_TOKEN;
-    if (err) {
-      if (tid == 0) raise_error(p.dev_err, err);
-    } else {
-      const float c2 = (1.0f / T) * 1.4426950408889634f;
-      int cur = 0;
-      m = 0;
-      for (;;) {
-        const float* l = p.logits + ((int64_t)b * N + cur) * V;
-        const float* q = p.probs ? p.probs + ((int64_t)b * N + cur) * V : nullptr;
-        float mx = -INFINITY;
-        int at = INT32_MAX;
-        for (int x = tid; x < V; x += kThreads)
-          if (l[x] > mx || at == INT32_MAX) mx = l[x], at = x;
-        float M;
-        int top;
-        block_best(mx, at, M, top);
-        int next = -1, last = top;
-        if (mode == SPEC_MODE_GREEDY) {
-          for (int c = N - 1; c > cur; --c)
-            if (s_par[c] == cur && s_tok[c] == top) next = c;
-        } else {
-          float s = 0.f;
-          for (int x = tid; x < V; x += kThreads) s += exp2f((l[x] - M) * c2);
-          const float invZ = 1.f / block_sum(s);
-          float a = 1.f, bq = 0.f;
-          int gone = 0;  // refused tokens (no draft probabilities)
-          // the residual's weight of x, for given scalars and number of refused tokens
-          auto weight = [&](int x, float a_, float b_, int n_) {
-            const float w = exp2f((l[x] - M) * c2) * invZ * a_;
-            if (q) return fmaxf(0.f, w - b_ * q[x]);
-            for (int k = 0; k < n_; ++k)
-              if (s_gone[k] == x) return 0.f;
-            return w;
-          };
-          for (int c = cur + 1; c < N && next < 0; ++c) {
-            if (s_par[c] != cur) continue;
-            const int x = s_tok[c];
-            const float u = word_to_uniform(philox4x32_10(0u, (uint32_t)(c - 1), (uint32_t)b, 0u, p.seed_lo, p.seed_hi).v[0]);
-            if (u * (q ? q[x] : 1.f) < weight(x, a, bq, gone)) {
-              next = c;
-              break;
-            }
-            __syncthreads();
-            if (tid == 0) s_gone[gone] = x;
-            __syncthreads();
-            float z = 0.f;
-            for (int y = tid; y < V; y += kThreads) z += weight(y, a, bq + 1.f, gone + 1);
-            z = block_sum(z);
-            if (z > 0.f) {
-              a /= z;
-              bq = (bq + 1.f) / z;
-              ++gone;
-            }
-          }
-          if (next < 0) {
-            float best = -1.f;
-            int bx = INT32_MAX;
-            for (int x = tid; x < V; x += kThreads) {
-              const float w = weight(x, a, bq, gone);
-              const uint32_t r = philox4x32_10((uint32_t)(x / 4), (uint32_t)cur, (uint32_t)b, 1u, p.seed_lo, p.seed_hi).v[x % 4];
-              const float key = w / -logf(word_to_uniform(r));
-              if (key > best) best = key, bx = x;
-            }
-            float kv;
-            block_best(best, bx, kv, last);
-          }
-        }
-        if (tid == 0) {
-          s_path[m] = cur;
-          s_out[m] = next < 0 ? last : s_tok[next];
-        }
-        if (next < 0) break;
-        cur = next;
-        ++m;
+    if (par0 != SPEC_TREE_UNUSED) {
+      if (md != SPEC_MODE_GREEDY && md != SPEC_MODE_SAMPLE) err |= SPEC_DEVERR_MODE;
+      if (md == SPEC_MODE_SAMPLE && (!(t_row > 0.f) || !isfinite(t_row))) err |= SPEC_DEVERR_TEMPERATURE;
+      const uint64_t used = nodes_with(par[0] != SPEC_TREE_UNUSED, par[1] != SPEC_TREE_UNUSED);
+      bool bad_tree = false, bad_token = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = lane + 32 * i, q = par[i];
+        if (q != SPEC_TREE_UNUSED && q != SPEC_TREE_ROOT) bad_tree |= q < 0 || q >= c || !((used >> (q & 63)) & 1);
+        bad_token |= c > 0 && q != SPEC_TREE_UNUSED && (tok[i] < 0 || tok[i] >= V);
       }
+      if (__any_sync(kAll, bad_tree)) err |= SPEC_DEVERR_TREE;
+      if (__any_sync(kAll, bad_token)) err |= SPEC_DEVERR_TOKEN;
+    }
+    if (par0 == SPEC_TREE_UNUSED || err) {  // uniform across the cluster: no exchange for this row
+      if (rank == 0 && warp == 0) {
+        if (lane == 0) {
+          if (err) raise_error(p.dev_err, err);
+          p.accept_len[b] = -1;
+        }
+        for (int j = lane; j < N; j += 32) p.out_tokens[(int64_t)b * N + j] = p.path[(int64_t)b * N + j] = -1;
+      }
+      continue;
+    }
+    const bool greedy = md == SPEC_MODE_GREEDY;
+    const float c2 = (1.0f / (greedy ? 1.f : t_row)) * 1.4426950408889634f;  // logit -> log2 units of p
+    float u[2] = {0.f, 0.f};
+    if (!greedy) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        u[i] = word_to_uniform(
+            philox4x32_10(0u, (uint32_t)(lane + 32 * i - 1), (uint32_t)b, 0u, p.seed_lo, p.seed_hi).v[0]);
+    }
+    if (!joined) {
+      cluster_wait();  // every CTA of the cluster is running
+      joined = true;
+    }
+
+    int cur = 0, m = 0, last = 0;
+    int step[2] = {lane == 0 ? 0 : -1, -1};  // the path: lane l holds steps l and l + 32
+    bool loaded = true;                      // v holds the node's first batch already
+    for (;;) {
+      const float* src = lrow + (int64_t)cur * V;
+      const float* qsrc = qrow ? qrow + (int64_t)cur * V : nullptr;
+      if (!loaded) load_batch(src, 0, v);
+      loaded = false;
+      const bool mine[2] = {par[0] == cur, par[1] == cur};  // children of the node
+      const uint64_t children = nodes_with(mine[0], mine[1]);
+      int next = -1;
+      if (greedy) {
+        // ---- argmax of the slice (lowest index on ties), then of the row: see accept.cu
+        float bv = -INFINITY;
+        int idx = tid < ngroups ? x0 + 4 * tid : INT32_MAX;
+        for (int gb = 0;;) {
+          const float bm = batch_max(v);
+          if (bm > bv) {
+            bv = bm;
+#pragma unroll
+            for (int i = kNB - 1; i >= 0; --i) {
+              const float lv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+              for (int e = 3; e >= 0; --e)
+                if (lv[e] == bm) idx = x0 + 4 * (gb + i * T + tid) + e;
+            }
+          }
+          gb += kStep;
+          if (gb >= ngroups) break;
+          load_batch(src, gb, v);
+        }
+        warp_best(bv, idx);
+        const Part* x = exchange(bv, 0.f, idx);
+        float rv;
+        row_best(x, rv, last);
+        const uint64_t hit = nodes_with(mine[0] && tok[0] == last, mine[1] && tok[1] == last);
+        if (hit) next = __ffsll((long long)hit) - 1;
+      } else {
+        // the children's target logits and draft probabilities: first used after the statistics
+        float ld[2] = {0.f, 0.f}, qd[2] = {1.f, 1.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (mine[i]) {
+            ld[i] = __ldg(src - x0 + tok[i]);
+            if (qsrc) qd[i] = __ldg(qsrc - x0 + tok[i]);
+          }
+        // ---- max and sum of exp2((l - max) c2) in one pass
+        float mx = -INFINITY, s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        for (int gb = 0;;) {
+          const float bm = batch_max(v);
+          if (bm > mx) {
+            if (mx != -INFINITY) {
+              const float rs = fast_exp2((mx - bm) * c2);
+              s0 *= rs;
+              s1 *= rs;
+              s2 *= rs;
+              s3 *= rs;
+            }
+            mx = bm;
+          }
+          if (mx != -INFINITY) {
+            const float mc = mx * c2;
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) {
+              s0 += fast_exp2(fmaf(v[i].x, c2, -mc));
+              s1 += fast_exp2(fmaf(v[i].y, c2, -mc));
+              s2 += fast_exp2(fmaf(v[i].z, c2, -mc));
+              s3 += fast_exp2(fmaf(v[i].w, c2, -mc));
+            }
+          }
+          gb += kStep;
+          if (gb >= ngroups) break;
+          load_batch(src, gb, v);
+        }
+        float s = (s0 + s1) + (s2 + s3);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float om = __shfl_xor_sync(kAll, mx, o), os = __shfl_xor_sync(kAll, s, o);
+          ms_combine(mx, s, om, os, c2);
+        }
+        const Part* x = exchange(mx, s, 0);
+        float M = -INFINITY, Z = 0.f;
+        for (int i = lane; i < nparts; i += 32) ms_combine(M, Z, x[i].f0, x[i].f1, c2);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float om = __shfl_xor_sync(kAll, M, o), os = __shfl_xor_sync(kAll, Z, o);
+          ms_combine(M, Z, om, os, c2);
+        }
+        const float invZ = 1.f / Z, mc2 = M * c2;
+
+        int gone[2] = {-1, -1};  // refused tokens (no draft probabilities): lane l holds refusals l and l + 32
+        int n_gone = 0;
+        // One pass over the slice with the residual's weights: their sum over the row, or (race) the winner of the
+        // exponential race, -1 if every weight is 0. Keys and bounds as in accept.cu.
+        // Weight of an entry with pe = 2^((l - M) c2): max(0, A pe - bq q), or without q (bq 0) pe itself, 0 for a
+        // refused token.
+        auto pass = [&](auto race, float A, float bq, float& total) -> int {
+          constexpr bool kRace = decltype(race)::value;
+          const bool resid = bq > 0.f;
+          const uint32_t cbase = (uint32_t)x0 >> 2;
+          float thr = 0.f, best = -1.f, sum = 0.f;
+          int bx = INT32_MAX;
+          auto iteration = [&](auto checked, int gb) {
+            float4 l4[kRB], q4[kRB];
+#pragma unroll
+            for (int i = 0; i < kRB; ++i) {
+              const int g = gb + i * T + tid;
+              const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+              if constexpr (decltype(checked)::value) {
+                l4[i] = load4(src, g, -INFINITY);
+                q4[i] = resid ? load4(qsrc, g, 0.f) : zero;
+              } else {
+                l4[i] = __ldg(reinterpret_cast<const float4*>(src) + g);
+                q4[i] = resid ? __ldg(reinterpret_cast<const float4*>(qsrc) + g) : zero;
+              }
+            }
+            [[maybe_unused]] Philox4 r[kRB];
+            if constexpr (kRace) {
+#pragma unroll
+              for (int i = 0; i < kRB; ++i)
+                r[i] = philox4x32_10(cbase + (uint32_t)(gb + i * T + tid), (uint32_t)cur, (uint32_t)b, 1u, p.seed_lo,
+                                     p.seed_hi);
+            }
+            float w[kRB * 4];
+#pragma unroll
+            for (int i = 0; i < kRB; ++i) {
+              const float lv[4] = {l4[i].x, l4[i].y, l4[i].z, l4[i].w};
+              const float qv[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float pe = fast_exp2(fmaf(lv[e], c2, -mc2));  // 0 past the slice (-inf logit)
+                w[4 * i + e] = resid ? fmaxf(fmaf(pe, A, -bq * qv[e]), 0.f) : pe;
+              }
+              if (n_gone > 0) {
+                // refused tokens among the warp's 128 entries of this group row (hardly ever)
+                const int base = x0 + 4 * (gb + i * T + warp * 32);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint32_t in = __ballot_sync(kAll, gone[k] >= base && gone[k] < base + 128);
+                  while (in) {
+                    const int t = __shfl_sync(kAll, gone[k], __ffs((int)in) - 1) - base;
+                    in &= in - 1;
+                    if (t >> 2 == lane) {
+#pragma unroll
+                      for (int e = 0; e < 4; ++e)
+                        if ((t & 3) == e) w[4 * i + e] = 0.f;
+                    }
+                  }
+                }
+              }
+            }
+            if constexpr (kRace) {
+              float ub[kRB * 4], lb = thr, ubm = 0.f;
+#pragma unroll
+              for (int i = 0; i < kRB; ++i) {
+                float lbe[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  // U = (2j + 1) 2^-24 for the word's top 23 bits j; U and 1 - U are exact
+                  const float f1 = __uint_as_float(0x3F800000u + (r[i].v[e] >> 9));
+                  const float uu = f1 - 0.999999940395355224609375f;
+                  ub[4 * i + e] = w[4 * i + e] * fast_rcp(1.f - uu);
+                  lbe[e] = ub[4 * i + e] * uu;
+                }
+                lb = max3f(lb, max3f(lbe[0], lbe[1], lbe[2]), lbe[3]);
+                ubm = max3f(ubm, max3f(ub[4 * i], ub[4 * i + 1], ub[4 * i + 2]), ub[4 * i + 3]);
+              }
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) lb = fmaxf(lb, __shfl_xor_sync(kAll, lb, o));
+              thr = lb;
+              if (ubm > 0.f && ubm >= thr) {
+#pragma unroll
+                for (int i = 0; i < kRB; ++i) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if (ub[4 * i + e] > 0.f && ub[4 * i + e] >= thr) {
+                      const float key = w[4 * i + e] / -logf(word_to_uniform(r[i].v[e]));
+                      if (key > best) {  // entries are visited in increasing x: ties keep the lower index
+                        best = key;
+                        bx = x0 + 4 * (gb + i * T + tid) + e;
+                      }
+                    }
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kRB; ++i) sum += (w[4 * i] + w[4 * i + 1]) + (w[4 * i + 2] + w[4 * i + 3]);
+            }
+          };
+          int gb = 0;
+          if (vec)
+            for (; gb + kRStep <= ngroups; gb += kRStep) iteration(std::false_type{}, gb);
+          for (; gb < ngroups; gb += kRStep) iteration(std::true_type{}, gb);  // uniform: every lane shuffles
+          if constexpr (kRace) {
+            warp_best(best, bx);
+            const Part* xp = exchange(best, 0.f, bx);
+            float kv;
+            int win;
+            row_best(xp, kv, win);
+            return kv > 0.f ? win : -1;
+          } else {
+            const Part* xp = exchange(warp_sum(sum), 0.f, 0);
+            float t = 0.f;
+            for (int i = lane; i < nparts; i += 32) t += xp[i].f0;
+            total = warp_sum(t);
+            return 0;
+          }
+        };
+
+        // ---- the children in turn
+        float a = 1.f, bq = 0.f;    // with draft probabilities: the residual is max(0, a p - bq q)
+        float a0 = 1.f, bq0 = 0.f;  // ... before the last refusal
+        float rem = 1.f;            // without: the mass of p that the refused tokens left
+        for (uint64_t left = children; left;) {
+          const int c = __ffsll((long long)left) - 1;
+          left &= left - 1;
+          const float pd = fast_exp2((of_node_f(ld, c) - M) * c2) / Z;
+          const float uc = of_node_f(u, c), qc = of_node_f(qd, c);
+          const int t = of_node(tok, c);
+          const bool again = !qsrc && __any_sync(kAll, gone[0] == t || gone[1] == t);  // a refused token once more
+          const float r = qsrc ? (bq == 0.f ? pd : fmaxf(0.f, fmaf(a, pd, -bq * qc))) : pd;
+          if (!again && uc * (qsrc ? qc : rem) < r) {
+            next = c;
+            break;
+          }
+          if (again) continue;
+          a0 = a;
+          bq0 = bq;
+          if (qsrc) {
+            bq += 1.f;
+            if (!left) break;  // the race needs no mass
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (lane + 32 * i == n_gone) gone[i] = t;
+            ++n_gone;
+          }
+          float mass = rem - pd;
+          if (qsrc || mass < kExactMass) {
+            pass(std::false_type{}, a * invZ, bq, mass);
+            if (!qsrc) mass *= invZ;
+          }
+          if (mass > 0.f) {
+            if (qsrc) {
+              a /= mass;
+              bq /= mass;
+            } else {
+              rem = mass;
+            }
+          } else {  // all zero: the residual stays as it was
+            bq = bq0;
+            if (!qsrc) {
+              --n_gone;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (lane + 32 * i == n_gone) gone[i] = -1;
+            }
+          }
+        }
+        // ---- the last token, from the residual; where that is all zero, from the one before
+        if (next < 0) {
+          float dummy;
+          for (int attempt = 0; attempt < 3; ++attempt) {
+            last = pass(std::true_type{}, a * invZ, bq, dummy);
+            if (last >= 0 || bq == 0.f) break;
+            a = a0;
+            bq = bq0;
+            bq0 = 0.f;
+          }
+        }
+      }
+      if (next < 0) break;
+      ++m;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i == m) step[i] = next;
+      cur = next;
+    }
+    // ---- the row's result: accepted tokens, the last token, -1 padding (one warp)
+    if (rank == 0 && warp == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = lane + 32 * i;
+        // the node after step j, and its token
+        const int down = __shfl_down_sync(kAll, step[i], 1), wrap = __shfl_sync(kAll, step[1], 0);
+        const int node = lane < 31 ? down : (i == 0 ? wrap : -1);
+        const int lo = __shfl_sync(kAll, tok[0], node & 31), hi = __shfl_sync(kAll, tok[1], node & 31);
+        if (j < N) {
+          p.out_tokens[(int64_t)b * N + j] = j < m ? (node & 32 ? hi : lo) : (j == m ? last : -1);
+          p.path[(int64_t)b * N + j] = step[i];
+        }
+      }
+      if (lane == 0) p.accept_len[b] = m;
     }
   }
-  __syncthreads();
-  if (tid < N) {
-    p.out_tokens[(int64_t)b * N + tid] = s_out[tid];
-    p.path[(int64_t)b * N + tid] = s_path[tid];
-  }
-  if (tid == 0) p.accept_len[b] = m;
+  if (!joined) cluster_wait();
 }
 
 }  // namespace tacc
@@ -178,7 +512,12 @@ extern "C" int spec_tree_accept(const float* target_logits, const int32_t* token
   if (batch == 0) return SPEC_OK;
   if (!target_logits || !tokens || !parents || !mode || !temperature || !out_tokens || !path || !accept_len)
     return SPEC_ERR_INVALID_ARG;
-  if (num_nodes > tree::kMaxNodes || vocab > tacc::kMaxVocab) return SPEC_ERR_UNSUPPORTED;
+  if (num_nodes > tree::kMaxNodes || vocab > acc::kMaxVocab) return SPEC_ERR_UNSUPPORTED;
+  const int dev = current_device();
+  if (dev < 0) return SPEC_ERR_LAUNCH;
+  acc::Config c;
+  if (!acc::choose_config<tacc::tree_accept_kernel<256>, tacc::tree_accept_kernel<128>>(dev, batch, vocab, c))
+    return SPEC_ERR_LAUNCH;
   tacc::Params p;
   p.logits = target_logits;
   p.tokens = tokens;
@@ -192,8 +531,25 @@ extern "C" int spec_tree_accept(const float* target_logits, const int32_t* token
   p.dev_err = dev_err;
   p.seed_lo = (uint32_t)(philox_seed & 0xFFFFFFFFu);
   p.seed_hi = (uint32_t)(philox_seed >> 32);
+  p.batch = batch;
   p.nodes = num_nodes;
   p.vocab = vocab;
-  tacc::tree_accept_kernel<<<(unsigned)batch, tacc::kThreads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  p.slice = c.slice;
+  p.csize = c.csize;
+  p.vec = (vocab % 4 == 0) && ((reinterpret_cast<uintptr_t>(target_logits) | reinterpret_cast<uintptr_t>(draft_probs)) & 15) == 0;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c.csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int clusters = batch < c.clusters ? batch : c.clusters;
+  cfg.gridDim = dim3((unsigned)(clusters * c.csize), 1, 1);
+  cfg.blockDim = dim3((unsigned)c.threads, 1, 1);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream_);
+  const cudaError_t e = c.threads == 256 ? cudaLaunchKernelEx(&cfg, tacc::tree_accept_kernel<256>, p)
+                                         : cudaLaunchKernelEx(&cfg, tacc::tree_accept_kernel<128>, p);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
