@@ -15,10 +15,11 @@
 // the argmax), one pass for every refused child but the last (the mass of the
 // next residual; none without draft probabilities, where it is 1 minus the
 // refused tokens' share), and one exponential race at the last node; all but the
-// first pass over a row come from L2. Lane l of every warp holds nodes l and
-// l + 32: parent, token, the uniform of its test and, for the children of the
-// current node, the target logit and the draft probability, whose loads are in
-// flight during the statistics pass.
+// first pass over a row come from L2. Every warp keeps the row's nodes in shared
+// memory of its own (lane l writes nodes l and l + 32; no block-wide barrier):
+// parent, token, the uniform of its test and, for the children of the current
+// node, the target logit and the draft probability, whose loads are in flight
+// during the statistics pass. In registers they would spill in the race.
 #include <math.h>
 
 #include <type_traits>
@@ -32,7 +33,9 @@ namespace tacc {
 using namespace acc;
 
 constexpr int kNB = 8;  // float4 groups per thread in flight together (statistics, argmax)
-constexpr int kRB = 2;  // float4 groups per thread in flight together (residual passes)
+constexpr int kRB = 2;  // ... in the race, whose Philox words and bounds fill the registers
+constexpr int kSB = 4;  // ... in a residual's sum
+constexpr int64_t kPrefetchMaxBytes = 32ll << 20;  // one node's rows over the batch, at most, to prefetch
 constexpr float kExactMass = 0.0625f;  // remaining mass below which it is summed instead of subtracted
 
 struct Params {
@@ -48,19 +51,29 @@ struct Params {
   int32_t* dev_err;
   uint32_t seed_lo, seed_hi;
   int batch, nodes, vocab, slice, csize;
-  int vec;  // rows are 16-byte aligned: float4 loads
+  int vec;       // rows are 16-byte aligned: float4 loads
+  int prefetch;  // see the walk
 };
 
-// Registers bound the CTAs resident per SM (768 threads at 80 registers each).
+// A warp's copy of the row.
+struct Nodes {
+  int32_t par[tree::kMaxNodes], tok[tree::kMaxNodes], path[tree::kMaxNodes];
+  int32_t gone[tree::kMaxNodes];  // refused tokens of the current node (no draft probabilities)
+  float u[tree::kMaxNodes], ld[tree::kMaxNodes], qd[tree::kMaxNodes];
+};
+
+// Registers bound the CTAs resident per SM (512 threads at 128 registers each: with less the passes spill).
 template <int T>
-__global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p) {
+__global__ void __launch_bounds__(T, 512 / T) tree_accept_kernel(const Params p) {
   constexpr int kWarps = T / 32;
-  constexpr int kStep = kNB * T, kRStep = kRB * T;  // groups per batch of the block
+  constexpr int kStep = kNB * T;  // groups per batch of the block
   constexpr uint32_t kAll = 0xffffffffu;
   __shared__ Shared sh;
+  __shared__ Nodes nodes_of_warp[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int csize = p.csize, rank = (int)cluster_ctarank(), nclusters = (int)(gridDim.x / (unsigned)csize);
   const int N = p.nodes, V = p.vocab;
+  Nodes& nd = nodes_of_warp[warp];
   const int x0 = rank * p.slice;       // a multiple of 4: group g holds Philox counter x0/4 + g
   const int n = min(p.slice, V - x0);  // >= 1 by construction of the slice
   const int ngroups = (n + 3) >> 2;
@@ -137,25 +150,18 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
     const float* qrow = p.probs ? p.probs + (int64_t)b * N * V + x0 : nullptr;
     const int md = p.mode[b];
     const float t_row = p.temperature[b];
-    int par[2], tok[2];  // of nodes lane and lane + 32
+    float4 v[kNB];
+    load_batch(lrow, 0, v);  // node 0's first batch, in flight during the checks
+    __syncwarp();            // the row before is done with
+    int par[2], tok[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int c = lane + 32 * i;
-      par[i] = c < N ? p.parents[(int64_t)b * N + c] : SPEC_TREE_UNUSED;
-      tok[i] = c < N ? p.tokens[(int64_t)b * N + c] : 0;
+      nd.par[c] = par[i] = c < N ? p.parents[(int64_t)b * N + c] : SPEC_TREE_UNUSED;
+      nd.tok[c] = tok[i] = c < N ? p.tokens[(int64_t)b * N + c] : 0;
+      nd.path[c] = c == 0 ? 0 : -1;
     }
-    float4 v[kNB];
-    load_batch(lrow, 0, v);  // node 0's first batch, in flight during the checks
-    // value of node c out of the two registers that hold all nodes
-    auto of_node = [&](const int (&x)[2], int c) -> int {
-      const int lo = __shfl_sync(kAll, x[0], c & 31), hi = __shfl_sync(kAll, x[1], c & 31);
-      return c & 32 ? hi : lo;
-    };
-    auto of_node_f = [&](const float (&x)[2], int c) -> float {
-      const float lo = __shfl_sync(kAll, x[0], c & 31), hi = __shfl_sync(kAll, x[1], c & 31);
-      return c & 32 ? hi : lo;
-    };
-    // nodes with a property, as a 64-bit mask
+    // nodes with a property (of nodes lane and lane + 32), as a 64-bit mask
     auto nodes_with = [&](bool a, bool c) -> uint64_t {
       return (uint64_t)__ballot_sync(kAll, a) | ((uint64_t)__ballot_sync(kAll, c) << 32);
     };
@@ -187,28 +193,32 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
     }
     const bool greedy = md == SPEC_MODE_GREEDY;
     const float c2 = (1.0f / (greedy ? 1.f : t_row)) * 1.4426950408889634f;  // logit -> log2 units of p
-    float u[2] = {0.f, 0.f};
     if (!greedy) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        u[i] = word_to_uniform(
+        nd.u[lane + 32 * i] = word_to_uniform(
             philox4x32_10(0u, (uint32_t)(lane + 32 * i - 1), (uint32_t)b, 0u, p.seed_lo, p.seed_hi).v[0]);
     }
+    __syncwarp();
     if (!joined) {
       cluster_wait();  // every CTA of the cluster is running
       joined = true;
     }
 
     int cur = 0, m = 0, last = 0;
-    int step[2] = {lane == 0 ? 0 : -1, -1};  // the path: lane l holds steps l and l + 32
     bool loaded = true;                      // v holds the node's first batch already
     for (;;) {
       const float* src = lrow + (int64_t)cur * V;
       const float* qsrc = qrow ? qrow + (int64_t)cur * V : nullptr;
       if (!loaded) load_batch(src, 0, v);
       loaded = false;
-      const bool mine[2] = {par[0] == cur, par[1] == cur};  // children of the node
-      const uint64_t children = nodes_with(mine[0], mine[1]);
+      const uint64_t children = nodes_with(nd.par[lane] == cur, nd.par[lane + 32] == cur);
+      // Rows that the node's decision may ask for, on their way to L2 while it is made: its draft probabilities (needed as
+      // soon as a child is refused) and the first child's logits.
+      if (p.prefetch && children && tid == 0) {
+        if (qsrc && !greedy) bulk_prefetch_l2(qsrc, (uint32_t)n * 4);
+        bulk_prefetch_l2(lrow + (int64_t)(__ffsll((long long)children) - 1) * V, (uint32_t)n * 4);
+      }
       int next = -1;
       if (greedy) {
         // ---- argmax of the slice (lowest index on ties), then of the row: see accept.cu
@@ -234,16 +244,16 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
         const Part* x = exchange(bv, 0.f, idx);
         float rv;
         row_best(x, rv, last);
-        const uint64_t hit = nodes_with(mine[0] && tok[0] == last, mine[1] && tok[1] == last);
+        const uint64_t hit = children & nodes_with(nd.tok[lane] == last, nd.tok[lane + 32] == last);
         if (hit) next = __ffsll((long long)hit) - 1;
       } else {
         // the children's target logits and draft probabilities: first used after the statistics
         float ld[2] = {0.f, 0.f}, qd[2] = {1.f, 1.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (mine[i]) {
-            ld[i] = __ldg(src - x0 + tok[i]);
-            if (qsrc) qd[i] = __ldg(qsrc - x0 + tok[i]);
+          if ((children >> (lane + 32 * i)) & 1) {
+            ld[i] = __ldg(src - x0 + nd.tok[lane + 32 * i]);
+            if (qsrc) qd[i] = __ldg(qsrc - x0 + nd.tok[lane + 32 * i]);
           }
         // ---- max and sum of exp2((l - max) c2) in one pass
         float mx = -INFINITY, s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
@@ -279,6 +289,11 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
           const float om = __shfl_xor_sync(kAll, mx, o), os = __shfl_xor_sync(kAll, s, o);
           ms_combine(mx, s, om, os, c2);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          nd.ld[lane + 32 * i] = ld[i];
+          nd.qd[lane + 32 * i] = qd[i];
+        }
         const Part* x = exchange(mx, s, 0);
         float M = -INFINITY, Z = 0.f;
         for (int i = lane; i < nparts; i += 32) ms_combine(M, Z, x[i].f0, x[i].f1, c2);
@@ -289,71 +304,68 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
         }
         const float invZ = 1.f / Z, mc2 = M * c2;
 
-        int gone[2] = {-1, -1};  // refused tokens (no draft probabilities): lane l holds refusals l and l + 32
-        int n_gone = 0;
+        __syncwarp();
+        int n_gone = 0;  // refused tokens (no draft probabilities)
         // One pass over the slice with the residual's weights: their sum over the row, or (race) the winner of the
         // exponential race, -1 if every weight is 0. Keys and bounds as in accept.cu.
         // Weight of an entry with pe = 2^((l - M) c2): max(0, A pe - bq q), or without q (bq 0) pe itself, 0 for a
         // refused token.
-        auto pass = [&](auto race, float A, float bq, float& total) -> int {
-          constexpr bool kRace = decltype(race)::value;
-          const bool resid = bq > 0.f;
-          const uint32_t cbase = (uint32_t)x0 >> 2;
+        auto pass = [&](auto race, auto with_q, float A, float bq, float& total) -> int {
+          constexpr bool kRace = decltype(race)::value, kResid = decltype(with_q)::value;
+          constexpr int NBat = kRace ? kRB : kSB, kRStep = NBat * T;
+          bool strikes = false;  // a refused token is among this thread's entries
+          for (int k = 0; k < (kResid ? 0 : n_gone); ++k) {
+            const int t = nd.gone[k] - x0;
+            strikes |= t >= 0 && t < n && (t >> 2) % T == tid;
+          }
           float thr = 0.f, best = -1.f, sum = 0.f;
           int bx = INT32_MAX;
           auto iteration = [&](auto checked, int gb) {
-            float4 l4[kRB], q4[kRB];
+            float4 l4[NBat], q4[NBat];
 #pragma unroll
-            for (int i = 0; i < kRB; ++i) {
+            for (int i = 0; i < NBat; ++i) {
               const int g = gb + i * T + tid;
               const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
               if constexpr (decltype(checked)::value) {
                 l4[i] = load4(src, g, -INFINITY);
-                q4[i] = resid ? load4(qsrc, g, 0.f) : zero;
+                q4[i] = kResid ? load4(qsrc, g, 0.f) : zero;
               } else {
                 l4[i] = __ldg(reinterpret_cast<const float4*>(src) + g);
-                q4[i] = resid ? __ldg(reinterpret_cast<const float4*>(qsrc) + g) : zero;
+                q4[i] = kResid ? __ldg(reinterpret_cast<const float4*>(qsrc) + g) : zero;
               }
             }
-            [[maybe_unused]] Philox4 r[kRB];
+            [[maybe_unused]] Philox4 r[NBat];
             if constexpr (kRace) {
 #pragma unroll
-              for (int i = 0; i < kRB; ++i)
-                r[i] = philox4x32_10(cbase + (uint32_t)(gb + i * T + tid), (uint32_t)cur, (uint32_t)b, 1u, p.seed_lo,
+              for (int i = 0; i < NBat; ++i)
+                r[i] = philox4x32_10((uint32_t)(x0 / 4 + gb + i * T + tid), (uint32_t)cur, (uint32_t)b, 1u, p.seed_lo,
                                      p.seed_hi);
             }
-            float w[kRB * 4];
+            float w[NBat * 4];
 #pragma unroll
-            for (int i = 0; i < kRB; ++i) {
+            for (int i = 0; i < NBat; ++i) {
               const float lv[4] = {l4[i].x, l4[i].y, l4[i].z, l4[i].w};
-              const float qv[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
+              [[maybe_unused]] const float qv[4] = {q4[i].x, q4[i].y, q4[i].z, q4[i].w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float pe = fast_exp2(fmaf(lv[e], c2, -mc2));  // 0 past the slice (-inf logit)
-                w[4 * i + e] = resid ? fmaxf(fmaf(pe, A, -bq * qv[e]), 0.f) : pe;
+                w[4 * i + e] = kResid ? fmaxf(fmaf(pe, A, -bq * qv[e]), 0.f) : pe;
               }
-              if (n_gone > 0) {
-                // refused tokens among the warp's 128 entries of this group row (hardly ever)
-                const int base = x0 + 4 * (gb + i * T + warp * 32);
+            }
+            if (!kResid && strikes) {
+              for (int k = 0; k < n_gone; ++k) {
+                const int t = nd.gone[k] - x0 - 4 * (gb + tid);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  uint32_t in = __ballot_sync(kAll, gone[k] >= base && gone[k] < base + 128);
-                  while (in) {
-                    const int t = __shfl_sync(kAll, gone[k], __ffs((int)in) - 1) - base;
-                    in &= in - 1;
-                    if (t >> 2 == lane) {
+                for (int i = 0; i < NBat; ++i)
 #pragma unroll
-                      for (int e = 0; e < 4; ++e)
-                        if ((t & 3) == e) w[4 * i + e] = 0.f;
-                    }
-                  }
-                }
+                  for (int e = 0; e < 4; ++e)
+                    if (t == 4 * i * T + e) w[4 * i + e] = 0.f;
               }
             }
             if constexpr (kRace) {
-              float ub[kRB * 4], lb = thr, ubm = 0.f;
+              float ub[NBat * 4], lb = thr, ubm = 0.f;
 #pragma unroll
-              for (int i = 0; i < kRB; ++i) {
+              for (int i = 0; i < NBat; ++i) {
                 float lbe[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
               thr = lb;
               if (ubm > 0.f && ubm >= thr) {
 #pragma unroll
-                for (int i = 0; i < kRB; ++i) {
+                for (int i = 0; i < NBat; ++i) {
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
                     if (ub[4 * i + e] > 0.f && ub[4 * i + e] >= thr) {
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < kRB; ++i) sum += (w[4 * i] + w[4 * i + 1]) + (w[4 * i + 2] + w[4 * i + 3]);
+              for (int i = 0; i < NBat; ++i) sum += (w[4 * i] + w[4 * i + 1]) + (w[4 * i + 2] + w[4 * i + 3]);
             }
           };
           int gb = 0;
@@ -416,10 +428,10 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
         for (uint64_t left = children; left;) {
           const int c = __ffsll((long long)left) - 1;
           left &= left - 1;
-          const float pd = fast_exp2((of_node_f(ld, c) - M) * c2) / Z;
-          const float uc = of_node_f(u, c), qc = of_node_f(qd, c);
-          const int t = of_node(tok, c);
-          const bool again = !qsrc && __any_sync(kAll, gone[0] == t || gone[1] == t);  // a refused token once more
+          const float pd = fast_exp2((nd.ld[c] - M) * c2) / Z, uc = nd.u[c], qc = nd.qd[c];
+          const int t = nd.tok[c];
+          bool again = false;  // a refused token once more
+          for (int k = 0; k < n_gone; ++k) again |= nd.gone[k] == t;
           const float r = qsrc ? (bq == 0.f ? pd : fmaxf(0.f, fmaf(a, pd, -bq * qc))) : pd;
           if (!again && uc * (qsrc ? qc : rem) < r) {
             next = c;
@@ -432,15 +444,18 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
             bq += 1.f;
             if (!left) break;  // the race needs no mass
           } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (lane + 32 * i == n_gone) gone[i] = t;
+            if (lane == 0) nd.gone[n_gone] = t;
+            __syncwarp();
             ++n_gone;
           }
           float mass = rem - pd;
           if (qsrc || mass < kExactMass) {
-            pass(std::false_type{}, a * invZ, bq, mass);
-            if (!qsrc) mass *= invZ;
+            if (qsrc) {
+              pass(std::false_type{}, std::true_type{}, a * invZ, bq, mass);
+            } else {
+              pass(std::false_type{}, std::false_type{}, 0.f, 0.f, mass);
+              mass *= invZ;
+            }
           }
           if (mass > 0.f) {
             if (qsrc) {
@@ -451,19 +466,15 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
             }
           } else {  // all zero: the residual stays as it was
             bq = bq0;
-            if (!qsrc) {
-              --n_gone;
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (lane + 32 * i == n_gone) gone[i] = -1;
-            }
+            if (!qsrc) --n_gone;
           }
         }
         // ---- the last token, from the residual; where that is all zero, from the one before
         if (next < 0) {
           float dummy;
           for (int attempt = 0; attempt < 3; ++attempt) {
-            last = pass(std::true_type{}, a * invZ, bq, dummy);
+            last = bq > 0.f ? pass(std::true_type{}, std::true_type{}, a * invZ, bq, dummy)
+                            : pass(std::true_type{}, std::false_type{}, 0.f, 0.f, dummy);
             if (last >= 0 || bq == 0.f) break;
             a = a0;
             bq = bq0;
@@ -473,24 +484,15 @@ __global__ void __launch_bounds__(T, 768 / T) tree_accept_kernel(const Params p)
       }
       if (next < 0) break;
       ++m;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i == m) step[i] = next;
+      if (lane == 0) nd.path[m] = next;
       cur = next;
     }
     // ---- the row's result: accepted tokens, the last token, -1 padding (one warp)
     if (rank == 0 && warp == 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = lane + 32 * i;
-        // the node after step j, and its token
-        const int down = __shfl_down_sync(kAll, step[i], 1), wrap = __shfl_sync(kAll, step[1], 0);
-        const int node = lane < 31 ? down : (i == 0 ? wrap : -1);
-        const int lo = __shfl_sync(kAll, tok[0], node & 31), hi = __shfl_sync(kAll, tok[1], node & 31);
-        if (j < N) {
-          p.out_tokens[(int64_t)b * N + j] = j < m ? (node & 32 ? hi : lo) : (j == m ? last : -1);
-          p.path[(int64_t)b * N + j] = step[i];
-        }
+      __syncwarp();
+      for (int j = lane; j < N; j += 32) {
+        p.out_tokens[(int64_t)b * N + j] = j < m ? nd.tok[nd.path[j + 1]] : (j == m ? last : -1);
+        p.path[(int64_t)b * N + j] = nd.path[j];
       }
       if (lane == 0) p.accept_len[b] = m;
     }
@@ -537,6 +539,9 @@ extern "C" int spec_tree_accept(const float* target_logits, const int32_t* token
   p.slice = c.slice;
   p.csize = c.csize;
   p.vec = (vocab % 4 == 0) && ((reinterpret_cast<uintptr_t>(target_logits) | reinterpret_cast<uintptr_t>(draft_probs)) & 15) == 0;
+  // Prefetches are free where a node's rows of the whole batch are small; on larger batches they compete with reads that
+  // are sure to be needed.
+  p.prefetch = p.vec && (int64_t)batch * vocab * 4 <= tacc::kPrefetchMaxBytes;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
