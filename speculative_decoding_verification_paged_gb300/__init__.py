@@ -438,8 +438,15 @@ def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
 
 
 def _is(t, dtype, shape, dev: int) -> bool:
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev \
-        and t.shape == shape and t.is_contiguous()
+    return isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape \
+        and t.is_contiguous()
+
+
+def _need_dims(t, name: str, dtype, ndim: int, dev: int):
+    """_need, with the tensor that is right checked first and the rest left to the errors."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.dim() == ndim
+            and t.is_contiguous()):
+        _need(t, name, dtype, ndim)
 
 
 def _need_shape(t, name: str, dtype, shape, dev: int):
@@ -465,11 +472,11 @@ def spec_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, parents, out
     dev = torch.cuda.current_device()
     if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("q must be a bfloat16 or float16 tensor")
-    _need(q, "q", q.dtype, 4)
-    _need(k_cache, "k_cache", q.dtype, 4)
+    _need_dims(q, "q", q.dtype, 4, dev)
+    _need_dims(k_cache, "k_cache", q.dtype, 4, dev)
     _need_shape(v_cache, "v_cache", q.dtype, k_cache.shape, dev)
     B, N, _, _ = q.shape
-    _need(block_table, "block_table", torch.int32, 2)
+    _need_dims(block_table, "block_table", torch.int32, 2, dev)
     if block_table.shape[0] != B:
         raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
     _need_shape(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
@@ -480,7 +487,7 @@ def spec_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, parents, out
     d = _attn_desc(q, k_cache, block_table)
     if workspace is None:
         workspace = new_attention_workspace(int(lib.spec_tree_attention_workspace(ctypes.byref(d), N)), q.device)
-    _need(workspace, "workspace", torch.uint8, 1)
+    _need_dims(workspace, "workspace", torch.uint8, 1, dev)
     rc = lib.spec_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  ctx_lens.data_ptr(), parents.data_ptr(), N, out.data_ptr(), _DTYPE_CODES[q.dtype],
                                  _DTYPE_CODES[out.dtype], ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
@@ -494,7 +501,7 @@ def spec_tree_accept(target_logits, tokens, parents, draft_probs, philox_seed: i
     """Walk of every row's tree, greedy or by speculative sampling (see spec_verify.h)."""
     lib = load_library()
     dev = torch.cuda.current_device()
-    _need(target_logits, "target_logits", torch.float32, 3)
+    _need_dims(target_logits, "target_logits", torch.float32, 3, dev)
     B, N, V = target_logits.shape
     _need_shape(tokens, "tokens", torch.int32, (B, N), dev)
     _need_shape(parents, "parents", torch.int32, (B, N), dev)
@@ -520,7 +527,7 @@ def _need_caches(k_cache, v_cache, dev: int):
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() not in (4, 5):
         raise ValueError("k_cache must be a tensor [num_layers, num_blocks, block_size, heads, head_dim] "
                          "or [num_blocks, block_size, heads, head_dim]")
-    _need(k_cache, "k_cache", k_cache.dtype, k_cache.dim())
+    _need_dims(k_cache, "k_cache", k_cache.dtype, k_cache.dim(), dev)
     _need_shape(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
     layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
     pages, page, heads, dim = k_cache.shape[-4:]
@@ -534,8 +541,8 @@ def spec_cache_commit_path(k_cache, v_cache, block_table, ctx_lens, path, accept
     lib = load_library()
     dev = torch.cuda.current_device()
     layers, pages, page, token_bytes = _need_caches(k_cache, v_cache, dev)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(path, "path", torch.int32, 2)
+    _need_dims(block_table, "block_table", torch.int32, 2, dev)
+    _need_dims(path, "path", torch.int32, 2, dev)
     B, N = path.shape
     if block_table.shape[0] != B:
         raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
@@ -565,8 +572,8 @@ def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: in
     caches, if given."""
     lib = load_library()
     dev = torch.cuda.current_device()
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(page_refs, "page_refs", torch.int32, 1)
+    _need_dims(block_table, "block_table", torch.int32, 2, dev)
+    _need_dims(page_refs, "page_refs", torch.int32, 1, dev)
     B, W = block_table.shape
     _need_shape(cur_lens, "cur_lens", torch.int32, (B,), dev)
     _need_shape(new_lens, "new_lens", torch.int32, (B,), dev)
@@ -584,7 +591,7 @@ def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: in
     if workspace is None:
         workspace = torch.empty(int(lib.spec_cache_update_workspace(ctypes.byref(d))), dtype=torch.uint8,
                                 device=block_table.device)
-    _need(workspace, "workspace", torch.uint8, 1)
+    _need_dims(workspace, "workspace", torch.uint8, 1, dev)
     rc = lib.spec_cache_update(block_table.data_ptr(), page_refs.data_ptr(), cur_lens.data_ptr(), new_lens.data_ptr(),
                                None if src_rows is None else src_rows.data_ptr(),
                                None if k_cache is None else k_cache.data_ptr(),

@@ -287,9 +287,11 @@ __device__ __forceinline__ int64_t row_offset(const Params& p, int D, int MT, in
   return (((int64_t)b * p.nodes + i) * p.heads + g * p.gqa + j) * D;
 }
 
-// Tiles per CTA. An even split cuts a unit at every CTA's border; each cut costs the end of a unit (2 to 4 us) on two
-// CTAs, and the first one the merge (7 us). Where all units have the same length (unit_tiles > 0), whole units are taken
-// instead if the busiest CTA then has at most kCutBytes of K more than the even split gives it.
+// Tiles per CTA. An even split cuts a unit at every CTA's border, and each cut unit is joined from its pieces. Where all
+// units have the same length (unit_tiles > 0), whole units are taken instead if the busiest CTA then has at most kCutBytes
+// of K more than the even split gives it. In a graph, inputs in L2 where they fit: batch 32 with 64 nodes 65.0 us in whole
+// units, 77.0 cut evenly; one sequence 11.4 and 13.9. Cuts are not limited to longer pieces: for short ragged sequences
+// pieces of at least two tiles take 31 us, of three 34, of one 22.
 template <class C>
 __device__ __forceinline__ int tiles_per_cta(int T, int unit_tiles, int grid) {
   const int even = (T + grid - 1) / grid;
