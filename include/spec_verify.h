@@ -460,7 +460,9 @@ int spec_gdn_verify_pooled(const float* q, const float* k, const float* v, const
  * block id (SPEC_DEVERR_BLOCK_ID) or tree (SPEC_DEVERR_TREE) gets out rows of
  * zeros. Device pointers 16-byte aligned.
  * Supported: D in {64,128,256}; bs in {16,32,64,128}; N <= 64; G <= 128;
- * B <= 4096.
+ * B <= 4096; with tiles = ceil(N / floor(128 / G)), at most 2^31 - 1 key tiles:
+ * (max_blocks_per_seq * bs / 64 + 1) * B * Hkv * tiles; num_blocks * bs at most
+ * 2^31 - 1.
  */
 size_t spec_tree_attention_workspace(const spec_attn_desc* d, int32_t num_nodes);
 
@@ -508,7 +510,9 @@ int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
  *  path          [B, N] int32: 0, the accepted nodes in order, -1s
  *  accept_len    [B] int32: accepted nodes, node 0 not counted
  *
- * Rows are read only along the accepted path.
+ * Rows are read only along the accepted path; of small batches (B * V * 4 bytes
+ * at most 32 MB) rows that the next decision may ask for are also prefetched.
+ * SPEC_ACCEPT_CONFIG acts as in spec_accept.
  * Device errors: a row with a used node's token outside [0, V)
  * (SPEC_DEVERR_TOKEN), a bad tree (SPEC_DEVERR_TREE), mode (SPEC_DEVERR_MODE) or
  * temperature (SPEC_DEVERR_TEMPERATURE), and an empty row of a padded batch (no

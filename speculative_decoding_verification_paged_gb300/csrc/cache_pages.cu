@@ -12,6 +12,8 @@ namespace pages {
 // path[j] >= j: a thread that owns one column of a row's tokens and moves them
 // in the order of j, reading a batch of tokens before it writes them, never
 // overwrites a token it still has to read, and no two threads share a byte.
+// In a graph one layer takes 2 us; 32 layers of batch 32 (34 MB moved, 4.9 us at copy
+// rate) 6 us warm and 11 us a call, of which the host's part is about 9 us.
 constexpr int kPathThreads = 128;
 constexpr int kPathBatch = 8;
 
@@ -82,7 +84,8 @@ __global__ void __launch_bounds__(kPathThreads) commit_path_kernel(const PathPar
 // cluster barrier is the cheapest such point on the device. A warp works on a
 // row, its lanes on the row's entries; free pages are found in order by a prefix
 // over contiguous ranges of the reference counts. Latency bounds it: about a
-// dozen dependent trips to L2.
+// dozen dependent trips to L2. Two updates of 128 rows take 23 or 30 us in a graph,
+// depending on what the process ran before; the cause of the two levels is not known.
 constexpr int kTableThreads = 1024;
 constexpr int kTableCtas = 8;     // the largest portable cluster
 constexpr int32_t kNeed = -2;     // an entry that waits for a free page
@@ -290,7 +293,8 @@ __global__ void __launch_bounds__(kTableThreads, 1) update_table_kernel(const Ta
 }
 
 // Copies of partly filled pages: CTA (row, layer, K or V). A stream at HBM speed; eight 16-byte loads a thread are in
-// flight before the first store. Launched early behind the table kernel, it waits for that kernel's results.
+// flight before the first store. Launched early behind the table kernel, it waits for that kernel's results. A fork with
+// 235 MB of partial pages takes 46 us with the table's update, 34.6 us at copy rate.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBatch = 8;
 

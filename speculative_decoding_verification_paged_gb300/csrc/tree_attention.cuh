@@ -1,6 +1,5 @@
-// Kernels of the tree verify attention (see the comment at the top of
-// tree_attention.cu): the tcgen05 kernel, the merge of units that were cut over
-// several CTAs, and their parameters, shared with the host side.
+// Kernel of the tree verify attention (see the comment at the top of
+// tree_attention.cu) and its parameters, shared with the host side.
 #pragma once
 
 #include <cuda.h>

@@ -220,6 +220,32 @@ def test_attention_reports_and_skips_bad_rows(sv):
         assert np.abs(ref[0]).max() > 0 and not ref[1:].any() and not got[1:].any()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_attention_output_on_a_16_byte_boundary(sv, D, out_dtype):
+    """An output that is 16- but not 32-byte aligned gives the same bits, and nothing around it is written."""
+    c = attention_case(np.random.default_rng(31), (40, 300), 13, 8, 2, D, 64, torch.bfloat16)
+    whole, err = run_attention(sv, c, out_dtype)
+    pad = 16 // whole.element_size()
+    flat = torch.full((whole.numel() + 2 * pad,), 7.0, dtype=out_dtype, device=DEV)
+    out = flat[pad:-pad].view(whole.shape)
+    assert err == 0 and out.data_ptr() % 32 == 16
+    sv.spec_tree_attention(c["q"], c["k"], c["v"], c["table"], c["ctx"], c["par"], out)
+    torch.cuda.synchronize()
+    check_attention(c, out)
+    assert torch.equal(out, whole) and bool((flat[:pad] == 7).all()) and bool((flat[-pad:] == 7).all())
+
+
+def test_empty_batches(sv):
+    i = lambda *s: torch.empty(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    q, kv = torch.empty((0, 4, 2, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((3, 16, 1, 64), dtype=torch.bfloat16, device=DEV)
+    out = torch.empty((0, 4, 2, 64), device=DEV)
+    sv.spec_tree_attention(q, kv, kv.clone(), i(0, 2), i(0), i(0, 4), out)
+    f = torch.empty((0, 4, 50), device=DEV)
+    sv.spec_tree_accept(f, i(0, 4), i(0, 4), None, 1, i(0), torch.empty(0, device=DEV), i(0, 4), i(0, 4), i(0))
+    torch.cuda.synchronize()
+
+
 def test_attention_reuses_its_workspace(sv):
     """One workspace, alternating shapes and inputs, bit-equal repeats; a bad row leaves it usable."""
     rng = np.random.default_rng(6)
@@ -444,6 +470,18 @@ def test_accept_reports_bad_rows(sv):
     assert err == bits
     for a, b in zip(got, good):
         assert np.array_equal(a[0], b[0]) and np.all(a[1:] == -1)
+
+
+@pytest.mark.parametrize("probs", [True, False])
+def test_accept_under_every_cluster_shape(sv, monkeypatch, probs):
+    """Threads a CTA and CTAs a cluster forced in turn; 16 CTAs of 256 threads need 4 * 256 logits each."""
+    c = accept_case(np.random.default_rng(21), 40, 9, 16 * 1024 + 3, "mixed", probs)
+    for threads in (128, 256):
+        for csize in (1, 2, 4, 8, 16):
+            monkeypatch.setenv("SPEC_ACCEPT_CONFIG", f"{threads}x{csize}")
+            got, err = run_accept(sv, c)
+            assert err == 0, (threads, csize)
+            check_accept(c, got)
 
 
 def test_accept_unaligned_rows_and_graph(sv):
