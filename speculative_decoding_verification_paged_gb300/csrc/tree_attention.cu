@@ -29,8 +29,9 @@
 // 128, context 2K: 71 us of 44.5 us for its bytes; tensor pipe 39% active, DRAM 50%,
 // so neither: the chain scores -> softmax -> product and the ends of units. Contexts of
 // 32K to 128K: 573 to 628 us of 395 us, at about 1370 W, where the clock falls to about
-// 1.6 GHz. Head dim 256, fp32 output: 480 to 521 us of 341 us; the second part of P
-// and the folds (256 KB a CTA through L2, about 5000 cycles each) are on its chain.
+// 1.6 GHz. Head dim 256, fp32 output: 480 to 521 us of 341 us, in a graph 480; there
+// 430 without folds (256 KB a CTA through L2, about 5000 cycles each) and 398 with
+// 16-bit output.
 #include <math.h>
 
 #include "launch_memo.h"

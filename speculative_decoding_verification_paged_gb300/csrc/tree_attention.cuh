@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     const int bs = 1 << p.page_shift;
     const int BH = bs < TK ? bs : TK;  // tokens of a copy: a page, or a tile of it
     const int pieces = TK / BH;
-    const uint64_t pol = l2_evict_first_policy();  // K and V that no other unit reads again
+    // K and V that no other unit reads again (in a graph: head dim 256 480 us, 518 without; batch 32 65 and 69)
+    const uint64_t pol = l2_evict_first_policy();
     // Two walks over the tiles, K's AHEAD tiles before V's. The lanes hold a window of 32 entries of the block table's row
     // as token rows; entries past the context and bad ones lie far outside the cache and read zeros.
     constexpr int kNowhere = -(1 << 20);
