@@ -34,7 +34,8 @@ template <typename Vec>
 __global__ void __launch_bounds__(kPathThreads) commit_path_kernel(const PathParams p) {
   __shared__ int64_t s_src[tree::kMaxNodes], s_dst[tree::kMaxNodes];
   const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x, N = p.nodes;
-  const int ctx = p.ctx_lens[b], m = p.accept_len[b], base = ctx - N;
+  const int ctx = p.ctx_lens[b], m = p.accept_len[b], base = ctx < N ? 0 : ctx - N;  // (rows that
+  // moved nothing may hold any length)
   int err = 0;
   if (m < -1 || m >= N) err |= SPEC_DEVERR_ACCEPT_LEN;
   if (m >= 0 && (ctx < N || (int64_t)ctx > (int64_t)p.max_blocks * p.page)) err |= SPEC_DEVERR_CTX_LEN;
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kPathThreads) commit_path_kernel(const PathPar
   if (__syncthreads_or(bad_page)) err |= SPEC_DEVERR_BLOCK_ID;
   if (layer == 0 && tid == 0) {
     if (err) raise_error(p.dev_err, err);
-    p.new_lens[b] = (err || m < 0) ? max(0, base) : base + m + 1;
+    p.new_lens[b] = (err || m < 0) ? base : base + m + 1;
   }
   if (err) return;
   const int64_t cols = p.token_bytes / (int64_t)sizeof(Vec);

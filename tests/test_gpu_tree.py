@@ -580,6 +580,18 @@ def test_commit_path_one_layer_and_bad_rows(sv):
         assert np.array_equal(new.cpu().numpy(), want[2]) and want[2][0] == 29
 
 
+def test_commit_path_padded_rows_of_any_length(sv):
+    """Rows that accepted nothing may hold any length: their new length is max(0, length - N)."""
+    N, ctx = 8, [-2 ** 31, -2 ** 31 + 3, -1, 0, 7, 8, 9, 2 ** 31 - 1]
+    B = len(ctx)
+    k, v = (torch.zeros((2, 4, 4, 1, 8), device=DEV) for _ in range(2))
+    new = torch.full((B,), -9, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    path = np.full((B, N), -1)
+    sv.spec_cache_commit_path(k, v, cuda(np.zeros((B, 2))), cuda(np.array(ctx)), cuda(path), cuda(np.full(B, -1)), new, dev_err=err)
+    assert int(err.item()) == 0 and new.tolist() == [max(0, c - N) for c in ctx]
+
+
 @pytest.mark.parametrize("entry", [6, 7])
 @pytest.mark.parametrize("page", [-1, 100])
 def test_commit_path_bad_page(sv, entry, page):
