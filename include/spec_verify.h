@@ -550,6 +550,7 @@ typedef struct spec_cache_desc {
  *  path [B, N] int32 and accept_len [B] int32 as written by spec_tree_accept
  *  new_lens [B] int32, not overlapping ctx_lens
  *
+ * K and V are two caches: one pointer for both is refused.
  * A row with accept_len -1 moves nothing and gets new_lens = max(0, base).
  * Device errors, with the same treatment: accept_len outside [-1, N - 1] or a
  * path that does not increase from 0 within [0, N) (SPEC_DEVERR_ACCEPT_LEN), a
@@ -589,7 +590,7 @@ int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_t* block_ta
  * handed out lowest index first, in the order of rows and entries, so the result
  * does not depend on timing.
  *
- *  k_cache, v_cache: both, or both NULL (then num_layers and token_bytes are not
+ *  k_cache, v_cache: two caches, or both NULL (then num_layers and token_bytes are not
  *              looked at and nothing is copied: for callers whose rows never
  *              share partly filled pages)
  *  workspace   >= spec_cache_update_workspace(d) bytes, 256-byte aligned, no

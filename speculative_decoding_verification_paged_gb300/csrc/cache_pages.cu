@@ -386,6 +386,7 @@ extern "C" int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_
   if ((d->num_layers > 0 && (!k_cache || !v_cache)) || !block_table || !ctx_lens || !path || !accept_len || !new_lens || new_lens == ctx_lens)
     return SPEC_ERR_INVALID_ARG;
   if (num_nodes > tree::kMaxNodes || !pages::tables_supported(d) || d->num_layers > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (d->num_layers > 0 && k_cache == v_cache) return SPEC_ERR_INVALID_ARG;  // two threads would move the same bytes
   pages::PathParams p;
   p.k = static_cast<uint8_t*>(k_cache);
   p.v = static_cast<uint8_t*>(v_cache);
@@ -430,6 +431,7 @@ extern "C" int spec_cache_update(int32_t* block_table, int32_t* page_refs, const
   if (!pages::tables_supported(d) || (copies && d->num_layers > 65535)) return SPEC_ERR_UNSUPPORTED;
   const pages::Layout L = pages::layout_for(d);
   if (workspace == nullptr || workspace_bytes < L.total) return SPEC_ERR_WORKSPACE;
+  if (copies && d->num_layers > 0 && k_cache == v_cache) return SPEC_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return SPEC_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pages::TableParams p;

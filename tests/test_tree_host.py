@@ -155,3 +155,11 @@ def test_plain_update_keeps_references_consistent():
         for b in range(B):
             n = -(-int(want[b]) // bs) if src[b] >= 0 else 0
             assert np.all(table[b, :n] >= 0) and np.all(table[b, n:] == -1)
+
+
+def test_one_tensor_for_both_caches_is_refused(lib):
+    d = ctypes.byref(_cdesc())
+    ws = lib.spec_cache_update_workspace(d)
+    a, b, c, e, f = (ctypes.c_void_p(256 * i) for i in range(2, 7))
+    assert lib.spec_cache_commit_path(FAKE, FAKE, a, b, c, e, f, 4, d, None, None) == -1
+    assert lib.spec_cache_update(a, b, c, e, None, FAKE, FAKE, d, f, ws, None, None) == -1
