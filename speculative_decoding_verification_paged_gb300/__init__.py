@@ -22,6 +22,7 @@ and, for a tree of drafts instead of a chain:
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -233,7 +234,8 @@ def spec_verify_attention_plan(q: torch.Tensor, k_cache: torch.Tensor, block_tab
 
 
 def new_attention_workspace(nbytes: int, device) -> torch.Tensor:
-    """A workspace for spec_verify_attention: zero-filled once, reusable by later calls on one stream."""
+    """A workspace for spec_verify_attention or spec_tree_attention: zero-filled once (on the current stream), reusable
+    by later calls on one stream."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
@@ -437,6 +439,12 @@ def _stream_of(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
 
 
+def _on(stream: Optional[torch.cuda.Stream]):
+    """Where a call's own workspace is made: on the call's stream, so that its zeros are written before the kernel and
+    its memory is not handed on while the kernel runs."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _is(t, dtype, shape, dev: int) -> bool:
     return isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape \
         and t.is_contiguous()
@@ -486,7 +494,8 @@ def spec_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, parents, out
     _need_shape(out, "out", out.dtype, q.shape, dev)
     d = _attn_desc(q, k_cache, block_table)
     if workspace is None:
-        workspace = new_attention_workspace(int(lib.spec_tree_attention_workspace(ctypes.byref(d), N)), q.device)
+        with _on(stream):
+            workspace = new_attention_workspace(int(lib.spec_tree_attention_workspace(ctypes.byref(d), N)), q.device)
     _need_dims(workspace, "workspace", torch.uint8, 1, dev)
     rc = lib.spec_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  ctx_lens.data_ptr(), parents.data_ptr(), N, out.data_ptr(), _DTYPE_CODES[q.dtype],
@@ -589,8 +598,9 @@ def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: in
                              f"and block_size {block_size}")
         d.num_layers, d.token_bytes = layers, token_bytes
     if workspace is None:
-        workspace = torch.empty(int(lib.spec_cache_update_workspace(ctypes.byref(d))), dtype=torch.uint8,
-                                device=block_table.device)
+        with _on(stream):
+            workspace = torch.empty(int(lib.spec_cache_update_workspace(ctypes.byref(d))), dtype=torch.uint8,
+                                    device=block_table.device)
     _need_dims(workspace, "workspace", torch.uint8, 1, dev)
     rc = lib.spec_cache_update(block_table.data_ptr(), page_refs.data_ptr(), cur_lens.data_ptr(), new_lens.data_ptr(),
                                None if src_rows is None else src_rows.data_ptr(),

@@ -246,6 +246,28 @@ def test_empty_batches(sv):
     torch.cuda.synchronize()
 
 
+def test_own_workspaces_belong_to_the_calls_stream(sv):
+    """A call on a given stream without a workspace waits for nothing on the current one, and is right when that is busy."""
+    c = attention_case(np.random.default_rng(51), (700, 1500, 90), 16, 8, 2, 128, 64, torch.bfloat16)
+    want, _ = run_attention(sv, c, torch.bfloat16)
+    out = torch.full_like(want, float("nan"))
+    table, refs, cur = cuda([[0, -1, -1], [1, -1, -1]]), cuda([1, 1, 0, 0, 0]), cuda([3, 4])
+    new = cuda([9, 5])
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    dirty = torch.full((96 << 20,), 255, dtype=torch.uint8, device=DEV)  # what a reused block would hold
+    del dirty
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    done.record()
+    sv.spec_tree_attention(c["q"], c["k"], c["v"], c["table"], c["ctx"], c["par"], out, stream=side)
+    sv.spec_cache_update(table, refs, cur, new, 4, stream=side)
+    side.synchronize()
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert table.tolist() == [[0, 2, 3], [1, 4, -1]] and refs.tolist() == [1] * 5
+
+
 def test_attention_reuses_its_workspace(sv):
     """One workspace, alternating shapes and inputs, bit-equal repeats; a bad row leaves it usable."""
     rng = np.random.default_rng(6)
