@@ -510,6 +510,8 @@ int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
  *  path          [B, N] int32: 0, the accepted nodes in order, -1s
  *  accept_len    [B] int32: accepted nodes, node 0 not counted
  *
+ * A visited node of a sampling row whose logits hold no distribution (all -inf, a
+ * NaN, a +inf) ends the row: no child of it is accepted, the last token is -1.
  * Rows are read only along the accepted path; of small batches (B * V * 4 bytes
  * at most 32 MB) rows that the next decision may ask for are also prefetched.
  * SPEC_ACCEPT_CONFIG acts as in spec_accept.

@@ -506,6 +506,26 @@ def test_accept_under_every_cluster_shape(sv, monkeypatch, probs):
             check_accept(c, got)
 
 
+@pytest.mark.parametrize("probs", [True, False])
+def test_accept_rows_that_hold_no_distribution(sv, probs):
+    """Logits of node 0 all -inf, all NaN, or with a +inf: no probability is defined. The row ends there: no child is
+    accepted by sampling and its last token is -1; other rows are as they would be without it."""
+    c = accept_case(np.random.default_rng(41), 6, 5, 700, "sample", probs)
+    c["par"][:] = [-1, 0, 0, 1, 2]
+    c["tok"][:, 1:] %= 700
+    good, err = run_accept(sv, c)
+    bad = dict(c, logits=c["logits"].copy())
+    bad["logits"][1, 0] = -np.inf
+    bad["logits"][2, 0] = np.nan
+    bad["logits"][3, 0, 17] = np.inf
+    got, err2 = run_accept(sv, bad)
+    assert err == 0 and err2 == 0
+    for x, y in zip(got, good):
+        assert np.array_equal(x[[0, 4, 5]], y[[0, 4, 5]])
+    for b in (1, 2, 3):
+        assert got[2][b] == 0 and got[1][b].tolist() == [0, -1, -1, -1, -1] and got[0][b].tolist() == [-1] * 5
+
+
 def test_accept_unaligned_rows_and_graph(sv):
     """Logits that start 4 bytes off a 16-byte boundary, and a captured call replayed on new inputs."""
     rng = np.random.default_rng(12)
