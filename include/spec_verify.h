@@ -558,8 +558,9 @@ typedef struct spec_cache_desc {
  * path that does not increase from 0 within [0, N) (SPEC_DEVERR_ACCEPT_LEN), a
  * ctx_len outside [N, max_blocks_per_seq * block_size] (SPEC_DEVERR_CTX_LEN), a
  * page outside [0, num_blocks) (SPEC_DEVERR_BLOCK_ID). Rows must not share the
- * pages of their tree slots. Without layers (L = 0) only new_lens is written.
- * Supported: N <= 64; L <= 65535; the table's limits of spec_cache_update.
+ * pages of their tree slots. Without a row or a layer (B or L = 0) the call does
+ * nothing, new_lens included. Supported: N <= 64; L <= 65535; the table's limits
+ * of spec_cache_update.
  */
 int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_t* block_table,
                            const int32_t* ctx_lens, const int32_t* path,

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kPathThreads) commit_path_kernel(const PathPar
     if (err) raise_error(p.dev_err, err);
     p.new_lens[b] = (err || m < 0) ? base : base + m + 1;
   }
-  if (err || layer >= p.layers) return;
+  if (err) return;
   const int64_t cols = p.token_bytes / (int64_t)sizeof(Vec);
   const int64_t plane = (int64_t)layer * p.num_blocks * p.page;
   for (int64_t c = tid; c < 2 * cols; c += kPathThreads) {
@@ -382,8 +382,8 @@ extern "C" int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_
                                       int32_t num_nodes, const spec_cache_desc* d, int32_t* dev_err,
                                       spec_stream_t stream_) {
   if (!pages::tables_ok(d) || num_nodes < 1 || d->num_layers < 0 || d->token_bytes < 1) return SPEC_ERR_INVALID_ARG;
-  if (d->batch == 0) return SPEC_OK;
-  if ((d->num_layers > 0 && (!k_cache || !v_cache)) || !block_table || !ctx_lens || !path || !accept_len || !new_lens || new_lens == ctx_lens)
+  if (d->batch == 0 || d->num_layers == 0) return SPEC_OK;
+  if (!k_cache || !v_cache || !block_table || !ctx_lens || !path || !accept_len || !new_lens || new_lens == ctx_lens)
     return SPEC_ERR_INVALID_ARG;
   if (num_nodes > tree::kMaxNodes || !pages::tables_supported(d) || d->num_layers > 65535) return SPEC_ERR_UNSUPPORTED;
   if (d->num_layers > 0 && k_cache == v_cache) return SPEC_ERR_INVALID_ARG;  // two threads would move the same bytes
@@ -403,7 +403,7 @@ extern "C" int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_
   p.nodes = num_nodes;
   p.page = d->block_size;
   p.max_blocks = d->max_blocks_per_seq;
-  const dim3 grid((unsigned)d->batch, d->num_layers > 0 ? (unsigned)d->num_layers : 1, 1);  // without layers: the lengths
+  const dim3 grid((unsigned)d->batch, (unsigned)d->num_layers, 1);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   switch (pages::vector_bytes(k_cache, v_cache, d->token_bytes)) {
     case 16: pages::commit_path_kernel<uint4><<<grid, pages::kPathThreads, 0, stream>>>(p); break;

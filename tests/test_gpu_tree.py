@@ -634,14 +634,6 @@ def test_commit_path_padded_rows_of_any_length(sv):
     assert int(err.item()) == 0 and new.tolist() == [max(0, c - N) for c in ctx]
 
 
-def test_commit_path_without_layers_writes_the_lengths(sv):
-    k, v = (torch.zeros((0, 4, 4, 1, 8), device=DEV) for _ in range(2))
-    new = torch.full((2,), -9, dtype=torch.int32, device=DEV)
-    sv.spec_cache_commit_path(k, v, cuda([[0, 1, 2], [3, 2, 1]]), cuda([10, 11]), cuda([[0, 2, 3, -1], [0, -1, -1, -1]]),
-                              cuda([2, 0]), new)
-    assert new.tolist() == [10 - 4 + 3, 11 - 4 + 1]
-
-
 @pytest.mark.parametrize("entry", [6, 7])
 @pytest.mark.parametrize("page", [-1, 100])
 def test_commit_path_bad_page(sv, entry, page):
