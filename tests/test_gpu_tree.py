@@ -254,6 +254,8 @@ def test_own_workspaces_belong_to_the_calls_stream(sv):
     table, refs, cur = cuda([[0, -1, -1], [1, -1, -1]]), cuda([1, 1, 0, 0, 0]), cuda([3, 4])
     new = cuda([9, 5])
     side, done = torch.cuda.Stream(), torch.cuda.Event()
+    # A kernel's first launch in a process waits for the device (it is loaded then: 193 ms here, 0.1 ms afterwards).
+    sv.spec_cache_update(table.clone(), refs.clone(), cur, new, 4)
     dirty = torch.full((96 << 20,), 255, dtype=torch.uint8, device=DEV)  # what a reused block would hold
     del dirty
     torch.cuda.synchronize()
