@@ -9,7 +9,7 @@
 // 128 (the M of the tensor core), up to two row tiles to a unit (sequence, kv head,
 // group of rows). The key tiles of all units form one list that is cut over one CTA
 // per SM; a unit that was cut is joined by its log-sum-exp inside the kernel: the
-// pieces meet in pairs at a counter for each border, and who comes later joins.
+// pieces meet, eight at a time, at a counter, and who comes last joins.
 //
 // A CTA: warp 0 loads K and V pages by TMA into two rings, K ahead of V; warp 1
 // issues every product as a whole uniform warp (one elected lane issues; operands in

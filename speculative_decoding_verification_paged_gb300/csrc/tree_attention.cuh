@@ -23,7 +23,8 @@ constexpr int kMaxGrid = 160;  // one CTA per SM, at most
 constexpr int kMaxSlots = 10;  // K and V tiles in shared memory
 constexpr int kTmemCols = 512;
 constexpr int kLaunchRegs = 96;  // registers a thread that a kernel of 640 threads is launched with
-constexpr int kCutBytes = 8 * 32768;  // see tiles_per_cta
+constexpr int kCutBytes = 6 * 32768;  // see tiles_per_cta
+constexpr int kRadix = 8;  // runs of pieces that are joined at once
 constexpr int kTables = 576;   // bytes of shared memory for barriers and small tables
 constexpr int kRows = 128;     // packed query rows of a row tile (MMA M)
 constexpr int kBarStream = 1;  // named barriers: the softmax threads of a stream (1, 2),
@@ -288,9 +289,10 @@ __device__ __forceinline__ int64_t row_offset(const Params& p, int D, int MT, in
 
 // Tiles per CTA. An even split cuts a unit at every CTA's border, and each cut unit is joined from its pieces. Where all
 // units have the same length (unit_tiles > 0), whole units are taken instead if the busiest CTA then has at most kCutBytes
-// of K more than the even split gives it. In a graph, inputs in L2 where they fit: batch 32 with 64 nodes 65.0 us in whole
-// units, 77.0 cut evenly; one sequence 11.4 and 13.9. Cuts are not limited to longer pieces: for short ragged sequences
-// pieces of at least two tiles take 31 us, of three 34, of one 22.
+// of K (six tiles of 32 KB) more than the even split gives it. In a graph, inputs in L2 where they fit, whole and cut: one
+// tile more (one sequence of 200) 14.9 and 18.5 us, five more (batch 32, 64 nodes) 65.5 and 77.4, seven more (one of 1000;
+// 40 of 1024) 26.4 and 21.0; 74.6 and 68.1. Cuts are not limited to longer pieces: for short ragged sequences pieces of at
+// least two tiles take 31 us, of three 34, of one 22.
 template <class C>
 __device__ __forceinline__ int tiles_per_cta(int T, int unit_tiles, int grid) {
   const int even = (T + grid - 1) / grid;
@@ -945,70 +947,82 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
   tc_fence_before();
   named_sync(kBarTail, 32 + kSoftmaxThreads);
 
-  // ---- join the pieces of cut units, in pairs: of two neighbouring runs of pieces the CTA that comes second joins them
+  // ---- join the pieces of cut units, kRadix neighbouring runs of pieces at a time: the CTA that comes last joins them, in
+  // the order of the pieces,
   //   out = sum w_k part_k / sum w_k, w_k = 2^(lse_k - max lse),
-  // and goes on with the longer run; nobody waits. The counter of a pair is that of the border CTA between its runs.
+  // and goes on with the longer run; nobody waits. A group's counter is that of the border CTA behind its first run: borders
+  // 1 mod kRadix on the first level, kRadix mod kRadix^2 on the second, and so on; no two groups share one. Each level costs
+  // a fence, an atomic and a round trip; one CTA reads what it joins. Radix 2, 4, 8, 16, 32 in a graph: one sequence of 8000
+  // 64.6, 54.6, 52.6, 57.5, 53.9 us; of 2000 at head dim 256 42.9, 37.6, 34.9, 45.0, 52.4; the largest batch at head dim
+  // 256 479, 481, 482, 482, 482.
   constexpr int COLS = JOIN ? D / 4 : D / 2;
   const int part = JOIN ? wg : half;
   for (int k = 0; k < n_cut; ++k) {
     const Piece c = cut[k];
     const int u0 = s_prefix[c.b] * U + c.u * (s_prefix[c.b + 1] - s_prefix[c.b]);
+    const int64_t row = row_offset(p, D, MT, c.b, c.u, mt, r);
+    auto slot_of = [&](int piece) -> int64_t {  // in units of 128 rows
+      return (int64_t)(piece == 0 ? piece_slot(c.c0, c.c0, u0, W) : 2 * (c.c0 + piece)) * MT + mt;
+    };
     int me = (int)blockIdx.x - c.c0;
-    bool going = true;
-    for (int run = 1; run < c.nseg && going; run *= 2) {
-      const int left = me / (2 * run) * (2 * run), right = left + run;
-      if (right >= c.nseg) continue;  // no neighbour on this level
+    for (int run = 1; run < c.nseg; run *= kRadix) {
+      const int left = me / (kRadix * run) * (kRadix * run), runs = min(kRadix, (c.nseg - left + run - 1) / run);
+      if (runs == 1) continue;                   // no neighbour on this level
       named_sync(kBarSoftmax, kSoftmaxThreads);  // the run's stores are issued, s_misc is read
       if (tid == 128) {
+        int32_t* met = p.counters + c.c0 + left + run;
         __threadfence();
-        const int before = atomicAdd(p.counters + c.c0 + right, 1);
-        if (before != 0) p.counters[c.c0 + right] = 0;
+        const int before = atomicAdd(met, 1);
+        if (before == runs - 1) *met = 0;
         __threadfence();
         s_misc[0] = before;
       }
       named_sync(kBarSoftmax, kSoftmaxThreads);
-      going = s_misc[0] != 0;
-      if (!going) break;
+      if (s_misc[0] != runs - 1) break;
       me = left;
-      const bool last = left == 0 && 2 * run >= c.nseg;
-      const int64_t sl = (int64_t)piece_slot(c.c0 + left, c.c0, u0, W) * MT + mt, sr = (int64_t)2 * (c.c0 + right) * MT + mt;
-      const float ll = __ldcg(p.lse + sl * kRows + r), lr = __ldcg(p.lse + sr * kRows + r);
-      const float M = fmaxf(ll, lr);
-      const bool some = ll == ll && lr == lr && M > -INFINITY;
-      const float wl = some ? fast_exp2(ll - M) : 0.f, wr = some ? fast_exp2(lr - M) : 0.f, inv = some ? 1.f / (wl + wr) : 0.f;
-      const float fl = wl * inv, fr = wr * inv;
-      const int64_t row = row_offset(p, D, MT, c.b, c.u, mt, r);
-      float4* a = p.opart + sl * (D / 4) * kRows + r;
-      const float4* o = p.opart + sr * (D / 4) * kRows + r;
-#pragma unroll 2
+      const bool last = left == 0 && kRadix * run >= c.nseg;
+      auto lse_at = [&](int i) { return p.lse + slot_of(left + i * run) * kRows + r; };
+      float M = -INFINITY, sum = 0.f;
+      bool valid = true;
+#pragma unroll 8
+      for (int i = 0; i < runs; ++i) {
+        const float x = __ldcg(lse_at(i));
+        valid = valid && x == x;
+        M = fmaxf(M, x);
+      }
+      const bool some = valid && M > -INFINITY;
+#pragma unroll 8
+      for (int i = 0; i < runs; ++i) sum += some ? fast_exp2(__ldcg(lse_at(i)) - M) : 0.f;
+      const float inv = some ? 1.f / sum : 0.f;
+#pragma unroll 1
       for (int q = part * COLS; q < (part + 1) * COLS; q += 16) {
         float v[16];
-        float4 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = __ldcg(a + (q / 4 + i) * kRows);
-          y[i] = __ldcg(o + (q / 4 + i) * kRows);
-        }
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < runs; ++i) {
+          const float w = some ? fast_exp2(__ldcg(lse_at(i)) - M) * inv : 0.f;
+          const float4* a = p.opart + (slot_of(left + i * run) * (D / 4) + q / 4) * kRows + r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[4 * i] = x[i].x * fl + y[i].x * fr;
-          v[4 * i + 1] = x[i].y * fl + y[i].y * fr;
-          v[4 * i + 2] = x[i].z * fl + y[i].z * fr;
-          v[4 * i + 3] = x[i].w * fl + y[i].w * fr;
+          for (int e = 0; e < 4; ++e) {
+            const float4 x = __ldcg(a + e * kRows);
+            v[4 * e] = fmaf(x.x, w, v[4 * e]);
+            v[4 * e + 1] = fmaf(x.y, w, v[4 * e + 1]);
+            v[4 * e + 2] = fmaf(x.z, w, v[4 * e + 2]);
+            v[4 * e + 3] = fmaf(x.w, w, v[4 * e + 3]);
+          }
         }
         if (last) {
           if (row >= 0) store_row<C::FP16>(p, row + q, v);
         } else {
+          float4* to = p.opart + (slot_of(left) * (D / 4) + q / 4) * kRows + r;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            __stcg(a + (q / 4 + i) * kRows, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          for (int e = 0; e < 4; ++e) __stcg(to + e * kRows, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
         }
       }
       if (!last) {
-        named_sync(kBarSoftmax, kSoftmaxThreads);  // everyone has read the run's lse
-        if (part == 0)
-          __stcg(p.lse + sl * kRows + r,
-                 ll == ll && lr == lr ? (some ? M + __log2f(wl + wr) : -INFINITY) : __int_as_float(0x7fc00000));
+        named_sync(kBarSoftmax, kSoftmaxThreads);  // everyone has read the runs' lse
+        if (part == 0) __stcg(lse_at(0), valid ? (some ? M + __log2f(sum) : -INFINITY) : __int_as_float(0x7fc00000));
       }
     }
   }
