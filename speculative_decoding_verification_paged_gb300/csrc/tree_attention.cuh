@@ -25,6 +25,7 @@ constexpr int kTmemCols = 512;
 constexpr int kLaunchRegs = 96;  // registers a thread that a kernel of 640 threads is launched with
 constexpr int kCutBytes = 6 * 32768;  // see tiles_per_cta
 constexpr int kRadix = 8;  // runs of pieces that are joined at once
+constexpr int kAlignBatch = 256;  // rows whose tile counts fit the statistics' area
 constexpr int kTables = 576;   // bytes of shared memory for barriers and small tables
 constexpr int kRows = 128;     // packed query rows of a row tile (MMA M)
 constexpr int kBarStream = 1;  // named barriers: the softmax threads of a stream (1, 2),
@@ -81,6 +82,7 @@ struct Cfg {
   // to instead of rounding it, so an accumulator loses about 1.3e-8 of itself with every MMA; 512 keys keep that at the
   // size of fp32's own errors. (Output of 16 bits does not show it: 1e-4 after 128K keys.)
   static constexpr int FOLD = TERMS > 1 ? 512 / TK : 0;
+  static_assert(X_BYTES >= kAlignBatch * 4 && kThreads >= kAlignBatch, "");
   static_assert(MT <= STREAMS, "two row tiles need two accumulators");
   static_assert(COL_O + STREAMS * D <= kTmemCols, "S / P buffers and accumulators fit tensor memory");
   static_assert(TERMS >= 1 && TERMS <= 3 && kMinV >= AHEAD, "");
@@ -293,12 +295,27 @@ __device__ __forceinline__ int64_t row_offset(const Params& p, int D, int MT, in
 // tile more (one sequence of 200) 14.9 and 18.5 us, five more (batch 32, 64 nodes) 65.5 and 77.4, seven more (one of 1000;
 // 40 of 1024) 26.4 and 21.0; 74.6 and 68.1. Cuts are not limited to longer pieces: for short ragged sequences pieces of at
 // least two tiles take 31 us, of three 34, of one 22.
+// Where there are at most as many units as CTAs (`units`, the longest of `longest` tiles), pieces do not reach over a
+// unit's end (`aligned`), under the same limit: a CTA with pieces of two units ends and joins twice. One sequence in a
+// graph, reaching over and aligned: 3968 tokens 46.9 and 28.2 us, 8064 51.0 and 32.9, 16000 54.1 and 40.4; four of 8000
+// 63.6 and 51.1. The plan for it costs the calls that do not need it up to 0.7 us.
 template <class C>
-__device__ __forceinline__ int tiles_per_cta(int T, int unit_tiles, int grid) {
+__device__ __forceinline__ int tiles_per_cta(int T, int unit_tiles, int units, int longest, int grid, int batch, bool& aligned) {
+  constexpr int kMore = kCutBytes / C::SLOT;
   const int even = (T + grid - 1) / grid;
+  aligned = false;
   if (unit_tiles > 0) {
     const int whole = (T / unit_tiles + grid - 1) / grid * unit_tiles;
-    if (whole <= even + kCutBytes / C::SLOT) return whole;
+    if (whole <= even + kMore) return whole;
+  }
+  if (units <= grid && batch <= kAlignBatch) {  // (padded rows can make the batch larger than its units)
+    int w = longest;  // then the pieces are at most T / w + units
+    if (unit_tiles > 0) w = (longest + grid / units - 1) / (grid / units);
+    else if (units < grid) w = min(w, (T + grid - units - 1) / (grid - units));
+    if (w <= even + kMore) {
+      aligned = w > 1 && (unit_tiles == 0 || unit_tiles % w != 0);  // else they end there anyway
+      return w;
+    }
   }
   return even;
 }
@@ -346,6 +363,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     ctx = p.ctx_lens[b];
     return (ctx >= N && (int64_t)ctx <= max_ctx) ? (ctx + TK - 1) / TK : 0;
   };
+  int live;  // sequences with work, where B <= kThreads
   {
     const int per = (B + kThreads - 1) / kThreads;
     const int b0 = tid * per;
@@ -398,7 +416,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       mbar_init(q_empty, 1);
       fence_mbar_init();
     }
-    __syncthreads();
+    live = __syncthreads_count(mine > 0);
   }
   // rows of sequences without work
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
@@ -412,8 +430,33 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
   }
   const int T = s_prefix[B] * U;  // the host made sure that it fits
   if (T == 0) return;
-  const int W = tiles_per_cta<C>(T, s_misc[22] == s_misc[23] ? s_misc[23] : 0, (int)gridDim.x);
-  const int f0 = min(T, (int)blockIdx.x * W), f1 = min(T, f0 + W);
+  bool aligned;
+  const int W = tiles_per_cta<C>(T, s_misc[22] == s_misc[23] ? s_misc[23] : 0, live * U, s_misc[23], (int)gridDim.x, B,
+                                 aligned);
+  int f0 = min(T, (int)blockIdx.x * W), f1 = min(T, f0 + W);
+  if (aligned) {  // uniform over the grid; the prefix then counts whole pieces, B <= kAlignBatch
+    const int nt = tid < B ? s_prefix[tid + 1] - s_prefix[tid] : 0, padded = (nt + W - 1) / W * W;
+    int incl = padded;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();  // the tile counts and s_misc are read
+    if (lane == 31) s_misc[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s_misc[w];
+    int32_t* real = reinterpret_cast<int32_t*>(s_x);
+    if (tid < B) {
+      s_prefix[tid + 1] = incl;  // s_prefix[0] is 0
+      real[tid] = nt;
+    }
+    __syncthreads();
+    f0 = (int)blockIdx.x * W;
+    if (f0 >= s_prefix[B] * U) return;
+    const Cursor c = cursor_at(f0, s_prefix, B, U);
+    f1 = f0 + min(W, real[c.b] - c.tile);  // a unit's last piece may be shorter
+  }
   if (f0 >= f1) return;
   const int n_tiles = f1 - f0;
 
@@ -865,12 +908,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     }
 
     // ---- the unit's rows: output, or a normalised partial and its log-sum-exp
-    const bool whole = cu.tile == 0 && n == cu.ntiles;
-    int slot = 0;
+    bool whole = cu.tile == 0 && n == cu.ntiles;
+    int slot = 0, c0 = 0, nseg = 1;
     if (!whole) {
-      const int u0 = s_prefix[cu.b] * U + cu.g * cu.ntiles, c0 = u0 / W;
-      slot = piece_slot((int)blockIdx.x, c0, u0, W);
-      cut[n_cut++] = Piece{cu.b, cu.g, c0, (u0 + cu.ntiles - 1) / W - c0 + 1};
+      const int u0 = s_prefix[cu.b] * U + cu.g * cu.ntiles;
+      c0 = u0 / W;
+      nseg = (u0 + cu.ntiles - 1) / W - c0 + 1;
+      whole = nseg == 1;  // one piece, padded
+      if (!whole) {
+        slot = piece_slot((int)blockIdx.x, c0, u0, W);
+        cut[n_cut++] = Piece{cu.b, cu.g, c0, nseg};
+      }
     }
     if (mine > 0) wait_pv(item - 1);
     if constexpr (C::FOLD > 0) {

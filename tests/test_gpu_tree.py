@@ -220,6 +220,23 @@ def test_attention_reports_and_skips_bad_rows(sv):
         assert np.abs(ref[0]).max() > 0 and not ref[1:].any() and not got[1:].any()
 
 
+@pytest.mark.parametrize("D,out_dtype", [(64, torch.float32), (128, torch.bfloat16), (256, torch.float32)])
+@pytest.mark.parametrize("live", [1, 2, 5])
+@pytest.mark.parametrize("B", [5, 256, 257, 700])
+def test_attention_few_long_rows_of_a_padded_batch(sv, B, live, D, out_dtype):
+    """A few sequences of unlike lengths, cut over many CTAs, among rows that are empty: at the batch's ends and within."""
+    rng = np.random.default_rng(B + live)
+    ctx = np.full(B, 8)
+    par = np.full((B, 8), to.UNUSED)
+    at = np.unique(np.linspace(0, B - 1, live).astype(int))
+    ctx[at] = [2000, 1111, 129, 900, 8][: len(at)]
+    par[at] = random_trees(rng, len(at), 8)
+    c = attention_case(rng, ctx, 8, 4, 2, D, 64, torch.bfloat16, par=par)
+    out, err = run_attention(sv, c, out_dtype)
+    assert err == 0
+    check_attention(c, out)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_attention_output_on_a_16_byte_boundary(sv, D, out_dtype):
