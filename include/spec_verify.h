@@ -91,6 +91,12 @@ typedef struct spec_attn_desc {
   int64_t num_blocks;         /* physical blocks in k_cache / v_cache          */
 } spec_attn_desc;
 
+/* The first bytes of an attention workspace hold arrival counters that every
+ * call, of spec_verify_attention and of spec_tree_attention, returns to zero;
+ * nothing else is ever written there. They alone have to be zero before the
+ * workspace's first use. */
+#define SPEC_ATTN_COUNTER_BYTES 4096
+
 /*
  * Bytes of device workspace spec_verify_attention needs for `d`: room for the
  * split-KV partial results (normalised partial outputs and their log-sum-exp)
@@ -115,10 +121,11 @@ size_t spec_verify_attention_workspace(const spec_attn_desc* d, int32_t k_draft)
  *              included; must lie in [k_draft+1, max_blocks_per_seq * bs].
  *  out         [B, k_draft+1, Hq, D] fp32
  *  workspace   >= spec_verify_attention_workspace(d, k_draft) bytes, 256-byte
- *              aligned, ZERO-FILLED before its first use (it holds per-unit
- *              arrival counters that every call returns to zero; the rest is
- *              scratch). Reuse it for later calls on the same stream; two calls
- *              in flight at once need two workspaces.
+ *              aligned, its first SPEC_ATTN_COUNTER_BYTES bytes ZERO-FILLED
+ *              before its first use; the rest is scratch. Reuse it for later
+ *              calls of any shape that it is large enough for, and of
+ *              spec_tree_attention, on the same stream; two calls in flight at
+ *              once need two workspaces.
  *
  * The key tiles of all (sequence, kv head) units are split evenly over the
  * CTAs (split-KV); a unit held by several CTAs is merged by its log-sum-exp
@@ -452,9 +459,11 @@ int spec_gdn_verify_pooled(const float* q, const float* k, const float* v, const
  *  parents     [B, N] int32
  *  out         [B, N, Hq, D] of type `out_dtype`: fp32, or `dtype`
  *  workspace   >= spec_tree_attention_workspace(d, N) bytes, 256-byte aligned,
- *              ZERO-FILLED before its first use; reusable by later calls on the
- *              same stream (two calls in flight at once, or two captured graphs
- *              that may run at once, need two workspaces).
+ *              its first SPEC_ATTN_COUNTER_BYTES bytes ZERO-FILLED before its
+ *              first use; reusable by later calls of any shape, and of
+ *              spec_verify_attention, on the same stream (two calls in flight at
+ *              once, or two captured graphs that may run at once, need two
+ *              workspaces).
  *
  * Device errors: a sequence with an out-of-range ctx_len (SPEC_DEVERR_CTX_LEN),
  * block id (SPEC_DEVERR_BLOCK_ID) or tree (SPEC_DEVERR_TREE) gets out rows of

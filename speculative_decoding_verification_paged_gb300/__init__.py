@@ -40,9 +40,10 @@ __all__ = [
     "spec_gdn_verify_pooled", "status_string",
     "spec_tree_attention", "spec_tree_attention_workspace", "spec_tree_accept", "spec_cache_commit_path",
     "spec_cache_update", "spec_cache_update_workspace",
-    "DEVERR", "MODE_GREEDY", "MODE_SAMPLE", "ALIGN_TOKEN", "ALIGN_LAST", "TREE_ROOT", "TREE_UNUSED",
+    "ATTN_COUNTER_BYTES", "DEVERR", "MODE_GREEDY", "MODE_SAMPLE", "ALIGN_TOKEN", "ALIGN_LAST", "TREE_ROOT", "TREE_UNUSED",
 ]
 
+ATTN_COUNTER_BYTES = 4096  # of an attention workspace: zero before its first use and after every call
 MODE_GREEDY = 0
 MODE_SAMPLE = 1
 DEVERR = {
@@ -234,8 +235,8 @@ def spec_verify_attention_plan(q: torch.Tensor, k_cache: torch.Tensor, block_tab
 
 
 def new_attention_workspace(nbytes: int, device) -> torch.Tensor:
-    """A workspace for spec_verify_attention or spec_tree_attention: zero-filled once (on the current stream), reusable
-    by later calls on one stream."""
+    """A workspace for spec_verify_attention and spec_tree_attention: zero-filled once (on the current stream), reusable
+    on one stream by later calls of both, of any shape that it is large enough for."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 

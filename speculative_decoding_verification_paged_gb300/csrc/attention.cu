@@ -92,9 +92,12 @@ static Layout layout_for(const spec_attn_desc* d, int k_draft) {
   Layout L;
   const int64_t n_rows = (int64_t)(k_draft + 1) * (d->num_q_heads / d->num_kv_heads);
   const int64_t slots = 2 * (int64_t)kMaxGrid;
-  L.lse_off = align256((size_t)d->batch * d->num_kv_heads * 4);
+  L.lse_off = SPEC_ATTN_COUNTER_BYTES;
   L.opart_off = L.lse_off + align256((size_t)(slots * n_rows * 4));
-  L.total = L.opart_off + align256((size_t)(slots * n_rows * d->head_dim * 4));
+  // The last term is not used. It keeps the size growing with the batch, so that the workspace of a call's largest batch
+  // is still the largest, as callers that compare sizes expect.
+  L.total = L.opart_off + align256((size_t)(slots * n_rows * d->head_dim * 4)) +
+            align256((size_t)d->batch * d->num_kv_heads * 4);
   return L;
 }
 
@@ -475,16 +478,17 @@ extern "C" int spec_verify_attention_noalloc(const void* q, const void* k_cache,
   if (rc != SPEC_OK) return rc;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  // Scratch this shape needs at most: arrival counters, then two partial slots
-  // per CTA of the largest persistent grid. A shape that cannot fit even then
-  // is rejected before any device call.
+  // Scratch this shape needs at most, laid out and sized as a workspace: arrival
+  // counters, two partial slots per CTA of the largest persistent grid, a word
+  // per unit. A shape that cannot fit even then is rejected before any device
+  // call.
   const int64_t n_rows = (int64_t)(k_draft + 1) * (d->num_q_heads / d->num_kv_heads);
-  const size_t counters_bytes = attn::align256((size_t)d->batch * d->num_kv_heads * 4);
+  const size_t unit_bytes = attn::align256((size_t)d->batch * d->num_kv_heads * 4);
   auto scratch_total = [&](int64_t grid, size_t* lse_off, size_t* opart_off) {
     const int64_t slots = 2 * grid;
-    *lse_off = counters_bytes;
+    *lse_off = SPEC_ATTN_COUNTER_BYTES;
     *opart_off = *lse_off + attn::align256((size_t)(slots * n_rows * 4));
-    return *opart_off + attn::align256((size_t)(slots * n_rows * d->head_dim * 4));
+    return *opart_off + attn::align256((size_t)(slots * n_rows * d->head_dim * 4)) + unit_bytes;
   };
   size_t lse_off = 0, opart_off = 0;
   if (scratch_total(1, &lse_off, &opart_off) > attn::kNoAllocScratchBytes) return SPEC_ERR_SCRATCH_LIMIT;
@@ -516,7 +520,7 @@ extern "C" int spec_verify_attention_noalloc(const void* q, const void* k_cache,
 
   uint8_t* ws = static_cast<uint8_t*>(scratch);
   // The counters must start at zero; every call shares the array, so clear them here.
-  if (cudaMemsetAsync(ws, 0, counters_bytes, stream) != cudaSuccess) return SPEC_ERR_LAUNCH;
+  if (cudaMemsetAsync(ws, 0, SPEC_ATTN_COUNTER_BYTES, stream) != cudaSuccess) return SPEC_ERR_LAUNCH;
   const attn::Params p = attn::make_params(block_table, ctx_lens, k_draft, out, d, ws, lse_off, opart_off, dev_err);
   return attn::dispatch(p, pr, d->head_dim, d->block_size, q, k_cache, v_cache, d->num_blocks, stream);
 }

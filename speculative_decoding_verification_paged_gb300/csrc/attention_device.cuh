@@ -25,7 +25,7 @@ struct Params {
   const int32_t* block_table;
   const int32_t* ctx_lens;
   float* out;
-  int32_t* counters;  // [B * Hkv] arrival counters, zero between calls
+  int32_t* counters;  // [kMaxGrid] arrival counters, zero between calls; a cut unit's is that of the CTA of its first piece
   float* lse;         // [2 * kMaxGrid][n_rows], log2 units
   float* opart;       // [2 * kMaxGrid][n_rows][D]
   int32_t* dev_err;
@@ -135,6 +135,11 @@ __device__ __forceinline__ Cursor cursor_at(int64_t f, const int32_t* s_prefix, 
   c.seq = 0;
   return c;
 }
+
+// A cut unit reaches over the end of the CTA that holds its first piece, and only one unit does, so that CTA's number is
+// an arrival counter of its own. The counters are the workspace's first SPEC_ATTN_COUNTER_BYTES bytes whatever the shapes,
+// and nothing else is written there: calls of other shapes, the tree call's included, may follow in the same workspace.
+static_assert(kMaxGrid * 4 <= SPEC_ATTN_COUNTER_BYTES, "a counter for every CTA");
 
 // What the finaliser of a unit needs once the unit's last tile in range is done.
 struct Fin {

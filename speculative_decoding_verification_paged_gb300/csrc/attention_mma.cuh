@@ -374,10 +374,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::MIN_BLOCKS) verify_atten
     if (!F.complete) {
       // release: every partial store of the CTA precedes the arrival
       named_sync(kBarConsumers, kConsumers);
-      const int unit = F.b * Hkv + F.g;
       if (tid == 0) {
         __threadfence();
-        const int last = atomicAdd(p.counters + unit, 1) == F.nseg - 1;
+        const int last = atomicAdd(p.counters + F.c0, 1) == F.nseg - 1;
         if (last) __threadfence();  // acquire: the other pieces are visible
         s_misc[8] = last;
       }
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MT>::MIN_BLOCKS) verify_atten
             }
           }
         }
-        if (tid == 0) p.counters[unit] = 0;  // ready for the next call
+        if (tid == 0) p.counters[F.c0] = 0;  // ready for the next call
       }
     }
     fence_proxy_async_smem();  // scratch writes before the next TMA into this stage

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kRegBudgetThreads, 1) verify_atten
       __threadfence();  // release the partials
       int last[2] = {0, 0};
       for (int k = 0; k < n_pend; ++k)
-        last[k] = atomicAdd(p.counters + pend[k].b * Hkv + pend[k].g, 1) == pend[k].nseg - 1;
+        last[k] = atomicAdd(p.counters + pend[k].c0, 1) == pend[k].nseg - 1;
       if (last[0] | last[1]) __threadfence();  // acquire the other pieces
       s_misc[8] = last[0];
       s_misc[9] = last[1];
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kRegBudgetThreads, 1) verify_atten
       fence_proxy_async_smem();  // the merged rows are read by the bulk copies
       named_sync(kBarSoftmax, kSoftmaxThreads);
       if (st == 0) {
-        p.counters[F.b * Hkv + F.g] = 0;
+        p.counters[F.c0] = 0;
         // rows i*G .. i*G + G - 1 are the G query heads of position i: contiguous in out
         for (int i = 0; i < R; ++i)
           bulk_s2g(p.out + (((int64_t)F.b * R + i) * p.num_q_heads + F.g * G) * D,

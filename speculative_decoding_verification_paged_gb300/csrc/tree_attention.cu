@@ -92,7 +92,7 @@ struct Layout {
 static Layout layout_for(const spec_attn_desc* d, int nodes) {  // room for any output type
   Layout L;
   const size_t slots = 2 * (size_t)kMaxGrid * rows_for(d, nodes, 1).mt, row_tile = (size_t)kRows * d->head_dim * 4;
-  L.lse = attn::align256(kMaxGrid * 4);
+  L.lse = SPEC_ATTN_COUNTER_BYTES;
   L.opart = L.lse + attn::align256(slots * kRows * 4);
   L.folds = L.opart + slots * row_tile;
   L.total = L.folds + (size_t)kMaxGrid * streams_for(d->head_dim, 1) * row_tile;

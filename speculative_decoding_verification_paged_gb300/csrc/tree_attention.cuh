@@ -20,6 +20,7 @@ using attn::cursor_at;
 __device__ __forceinline__ int piece_slot(int c, int c0, int u0, int W) { return 2 * c + ((c == c0 && u0 > c * W) ? 1 : 0); }
 
 constexpr int kMaxGrid = 160;  // one CTA per SM, at most
+static_assert(kMaxGrid * 4 <= SPEC_ATTN_COUNTER_BYTES, "the counters keep to their area, which the chain call shares");
 constexpr int kMaxSlots = 10;  // K and V tiles in shared memory
 constexpr int kTmemCols = 512;
 constexpr int kLaunchRegs = 96;  // registers a thread that a kernel of 640 threads is launched with
