@@ -16,8 +16,8 @@
 // a branch of one lane cost a register move each: four MMAs 340 cycles, here 110);
 // two softmax warpgroups for each accumulator take half of a tile's keys each. The
 // scores stay in tensor memory, where P replaces them as operand A of the second
-// product. The running maximum follows only when it grows by more than 2^8, so that
-// the accumulator is rarely rescaled; the row sum is fp32.
+// product. The running maximum follows only when it grows by more than 2^8 (fp16: 2^4,
+// and it may fall too), so that the accumulator is rarely rescaled; the row sum is fp32.
 //
 // Numbers: 16-bit output rounds P to 16 bits once. fp32 output adds a second part of
 // P (fp16) or two (bf16), since a single part would leave an error of half a step of
@@ -127,7 +127,8 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return SPEC_ERR_INVALID_ARG;
 
   // Parts of P: one where the output is rounded to the input type anyway; for fp32 output as many as keep 22 to 24 bits
-  // of it (two fp16 parts, three bf16 ones; two bf16 parts alone would be 2.2e-6 off).
+  // of it (two fp16 parts, down to fp16's smallest step, see Cfg::SHIFT; three bf16 ones; two bf16 parts alone would be
+  // 2.2e-6 off).
   const bool fp16 = dtype == SPEC_DTYPE_FP16;
   const int D = d->head_dim, terms = out_dtype != SPEC_DTYPE_FP32 ? 1 : fp16 ? 2 : 3;
   const tattn::Rows rows = tattn::rows_for(d, num_nodes, terms);

@@ -83,6 +83,15 @@ struct Cfg {
   // to instead of rounding it, so an accumulator loses about 1.3e-8 of itself with every MMA; 512 keys keep that at the
   // size of fp32's own errors. (Output of 16 bits does not show it: 1e-4 after 128K keys.)
   static constexpr int FOLD = TERMS > 1 ? 512 / TK : 0;
+  // Weights are 2^SHIFT e^(s - m) for a reference m of the row that may lag behind the largest score, by up to LAG (in log2
+  // units). bf16 holds weights of any size. fp16's steps are never below 2^-24: there the reference is as low as its
+  // largest value allows (weights up to 2^15), and follows scores that stay more than FALL below it down, by up to DEPTH
+  // in all (the fp32 accumulator and row sum have that room). A step then leaves 2^-36 min(p, 2^FALL w) of a key, p the
+  // row's and w the tile's largest weight; with LAG 8 and neither shift nor fall it was 2^-25 p, all of a key 17 nats
+  // below a first token that takes most of the attention. What it costs (32 sequences of 2048, 64 nodes, head dim 128, in
+  // a graph, with and without): scores of standard deviation 1 66.3 and 65.6 us, of 3 78.6 and 70.1, of 6 78.5 and 76.5.
+  static constexpr float SHIFT = FP16 ? 11.f : 0.f, LAG = FP16 ? 4.f : 8.f, FALL = FP16 ? 10.f : 0.f, DEPTH = 40.f;
+  static_assert(!FP16 || SHIFT + LAG <= 15.f, "weights stay below fp16's largest value");
   static_assert(X_BYTES >= kAlignBatch * 4 && kThreads >= kAlignBatch, "");
   static_assert(MT <= STREAMS, "two row tiles need two accumulators");
   static_assert(COL_O + STREAMS * D <= kTmemCols, "S / P buffers and accumulators fit tensor memory");
@@ -710,7 +719,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
   };
 
   // Adds the stream's accumulator, which holds the products up to item `last`, to its sums in memory (`again`: they hold
-  // earlier folds, relative to the maximum m_fold), and leaves the result there, or in the accumulator (`back`). Each half
+  // earlier folds, relative to the reference m_fold), and leaves the result there, or in the accumulator (`back`). Each half
   // of the stream does half of the columns. The loads go out before the product is waited for, 64 columns at a time.
   auto fold = [&](float m_, float m_fold, bool again, bool back, int last) {
     constexpr int CH = D / 2 < 64 ? D / 2 : 64;
@@ -764,11 +773,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       cursor_advance(nx, s_prefix, B, U);
       base_next = p.ctx_lens[nx.b] - N;
     }
-    float m = -INFINITY, l = 0.f;  // running maximum (scaled; it may lag by up to 8), the thread's share of the row's sum
+    float m = -INFINITY, l = 0.f;  // reference (scaled scores, see SHIFT), the thread's share of the row's sum
+    [[maybe_unused]] float m_top = -INFINITY;  // the largest reference so far
     bool tree_bad = false, dead = false, have_tree = false;
     uint64_t sees = 0;
     int mine = 0;  // items of this stream in the unit so far
-    [[maybe_unused]] float m_fold = -INFINITY;  // the maximum that the folded sums are relative to
+    [[maybe_unused]] float m_fold = -INFINITY;  // the reference of the folded sums
     // the stream's first tile: every tile, or every other one of the CTA's
 #pragma unroll 1
     for (int tt = JOIN ? ((done & 1) == h ? 0 : 1) : 0; tt < n; tt += JOIN ? 2 : 1, ++item, ++mine) {
@@ -835,20 +845,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
           for (int i = 0; i < 8; ++i) a[i] = max3(a[i], v[k + i], v[k + 8 + i]);
         mx = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7])) * p.scale_log2;
       }
-      // Both halves of a row use one maximum. The barrier also tells that both have read their scores, which the weights
+      // Both halves of a row use one reference. The barrier also tells that both have read their scores, which the weights
       // overwrite.
       tc_fence_before();
-      const bool any = named_sync_or(bar, 256, mx > m + 8.f);
+      const bool any = named_sync_or(bar, 256, mx > m + C::LAG || (C::FALL > 0.f && mx < m - C::FALL && mx > -INFINITY));
       tc_fence_after();
       if (any) {
         s_x[wg * kRows + r] = mx;
         named_sync(bar, 256);
         mx = fmaxf(mx, s_x[(wg ^ 1) * kRows + r]);
-        const bool grow = mx > m + 8.f;
-        const float a = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mx)) : 1.f;
-        m = grow ? mx : m;
+        float to = mx > m + C::LAG ? mx : m;
+        bool moved = true;
+        if constexpr (C::FALL > 0.f) {
+          if (mx < m - C::FALL && mx > -INFINITY) to = fmaxf(mx, m_top - C::DEPTH);
+          m_top = fmaxf(m_top, to);
+          moved = named_sync_or(bar, 256, to != m);  // not if it was one half that is low
+        }
+        const float a = to == m ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - to);
+        m = to;
         l *= a;
-        if (mine > 0) {  // the accumulator holds earlier tiles; each half of the stream rescales half of its columns
+        if (mine > 0 && moved) {  // the accumulator holds earlier tiles; each half of the stream rescales half of its columns
           wait_pv(item - 1);
 #pragma unroll 1
           for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
@@ -861,7 +877,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
           }
         }
       }
-      const float ms = m == -INFINITY ? 0.f : m;
+      const float ms = (m == -INFINITY ? 0.f : m) - C::SHIFT;
       const float2 sc = make_float2(p.scale_log2, p.scale_log2), mm = make_float2(-ms, -ms);
       float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
