@@ -450,9 +450,10 @@ int spec_gdn_verify_pooled(const float* q, const float* k, const float* v, const
  *  q           [B, N, Hq, D] of type `dtype` (SPEC_DTYPE_BF16 or _FP16)
  *  k_cache     [num_blocks, bs, Hkv, D] of type `dtype`; node j's K and V are in
  *  v_cache     the cache at token base + j. Slots of unused nodes and slots at
- *              or past ctx_lens[b] may hold anything, NaN included; a NaN or
- *              infinity in the V of any other slot may reach every row of the
- *              sequence.
+ *              or past ctx_lens[b] may hold anything, NaN included. A NaN or
+ *              +inf among the scores that a row sees makes that row NaN, a score
+ *              of -inf is a weight of 0; a NaN or infinity in the V of any other
+ *              slot may reach every row of the sequence.
  *  block_table [B, max_blocks_per_seq] int32
  *  ctx_lens    [B] int32, tokens in the cache, the N tree slots included; must
  *              lie in [N, max_blocks_per_seq * bs]

@@ -39,7 +39,7 @@ struct Params {
   const int32_t* parents;
   void* out;
   int32_t* counters;  // [kMaxGrid], zero between calls: pieces that met at the border before CTA c
-  float* lse;         // [2 * kMaxGrid][row tiles of a unit][128], log2 units; NaN: no result
+  float* lse;         // [2 * kMaxGrid][row tiles of a unit][128], log2 units; +inf: no result (NaN: scores without a value)
   float4* opart;      // [2 * kMaxGrid][row tiles of a unit][D / 4][128], normalised
   float4* folds;      // [kMaxGrid][streams][D / 4][128], see fold
   int32_t* dev_err;
@@ -942,10 +942,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       if (mine > C::FOLD) fold(m, m_fold, true, true, item - 1);
     }
     if (tree_bad && st == 0) raise_error(p.dev_err, SPEC_DEVERR_TREE);
-    if (tree_bad || dead) l = __int_as_float(0x7fc00000);  // no result: the row is zeros
+    if (tree_bad || dead) l = -1.f;  // no result: the row is zeros, whatever its scores were
     // Threads of a row: the two halves of its stream; with one row tile on two streams all four, which then write a
     // quarter of the columns of both accumulators' sum each.
     float L, M = m, f[2] = {1.f, 0.f};  // factors of the accumulators
+    bool none;
     s_x[wg * kRows + r] = l;
     if (JOIN) s_x[(4 + wg) * kRows + r] = m;
     tc_fence_before();
@@ -957,15 +958,19 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       M = fmaxf(m0, m1);
       f[0] = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M);
       f[1] = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
-      L = (s_x[r] + s_x[kRows + r]) * f[0] + (s_x[2 * kRows + r] + s_x[3 * kRows + r]) * f[1];
+      const float l0 = s_x[r], l1 = s_x[kRows + r], l2 = s_x[2 * kRows + r], l3 = s_x[3 * kRows + r];
+      L = (l0 + l1) * f[0] + (l2 + l3) * f[1];
+      none = l0 < 0.f || l1 < 0.f || l2 < 0.f || l3 < 0.f;
     } else {
-      L = s_x[2 * h * kRows + r] + s_x[(2 * h + 1) * kRows + r];
+      const float l0 = s_x[2 * h * kRows + r], l1 = s_x[(2 * h + 1) * kRows + r];
+      L = l0 + l1;
+      none = l0 < 0.f || l1 < 0.f;
     }
     // read here: a stream without a tile of the unit knows only now that the unit was loaded
     const bool bad = s_bad[seq & 7] != 0;
     if (bad && tid == 128) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
-    if (bad) L = __int_as_float(0x7fc00000);
-    const bool some = L > 0.f;
+    none |= bad;
+    const bool some = !none && L != 0.f;  // a NaN makes the row NaN, by its factor
     const float inv = some ? 1.f / L : 0.f;
     f[0] *= inv;
     f[1] *= inv;
@@ -973,7 +978,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
     constexpr int COLS = JOIN ? D / 4 : D / 2;  // columns of a thread
     const int part = JOIN ? wg : half;
     if (!whole && part == 0)
-      p.lse[((int64_t)slot * MT + mt) * kRows + r] = some ? M + __log2f(L) : (L == 0.f ? -INFINITY : L);
+      p.lse[((int64_t)slot * MT + mt) * kRows + r] = some ? M + __log2f(L) : none ? INFINITY : -INFINITY;
     const uint32_t t_acc = JOIN ? tmem + (uint32_t)C::COL_O + lanes : t_o;
     // an accumulator that got no tile of the unit holds anything
     const bool has0 = !JOIN || (done & 1) == 0 || n > 1, has1 = JOIN && ((done & 1) == 1 || n > 1);
@@ -1048,14 +1053,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       const bool last = left == 0 && kRadix * run >= c.nseg;
       auto lse_at = [&](int i) { return p.lse + slot_of(left + i * run) * kRows + r; };
       float M = -INFINITY, sum = 0.f;
-      bool valid = true;
+      bool none = false, nan = false;
 #pragma unroll 8
       for (int i = 0; i < runs; ++i) {
         const float x = __ldcg(lse_at(i));
-        valid = valid && x == x;
+        none |= x == INFINITY;
+        nan |= x != x;
         M = fmaxf(M, x);
       }
-      const bool some = valid && M > -INFINITY;
+      const bool some = !none && (M > -INFINITY || nan);
 #pragma unroll 8
       for (int i = 0; i < runs; ++i) sum += some ? fast_exp2(__ldcg(lse_at(i)) - M) : 0.f;
       const float inv = some ? 1.f / sum : 0.f;
@@ -1077,6 +1083,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
             v[4 * e + 3] = fmaf(x.w, w, v[4 * e + 3]);
           }
         }
+        if (!some) {  // (parts of a row without a result may be NaN)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        }
         if (last) {
           if (row >= 0) store_row<C::FP16>(p, row + q, v);
         } else {
@@ -1087,7 +1097,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention_kernel(const Pa
       }
       if (!last) {
         named_sync(kBarSoftmax, kSoftmaxThreads);  // everyone has read the runs' lse
-        if (part == 0) __stcg(lse_at(0), valid ? (some ? M + __log2f(sum) : -INFINITY) : __int_as_float(0x7fc00000));
+        if (part == 0) __stcg(lse_at(0), some ? M + __log2f(sum) : none ? INFINITY : -INFINITY);
       }
     }
   }

@@ -90,3 +90,59 @@ def test_fp16_scores_that_rise_and_fall(sv, out_dtype):
         if out_dtype == torch.float16:
             tol = tol + HALF[out_dtype] * (S + np.abs(ref)) * (1 + 2.0 ** -6) + torch.finfo(out_dtype).smallest_normal
         assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
+
+
+# ---------------------------------------------------------------------------
+# NaN and infinities that a row sees
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16),
+                                             (torch.float16, torch.float32)], ids=["bf16_f32", "bf16", "fp16_f32"])
+@pytest.mark.parametrize("D,ctx", [(64, (300, 2500, 70)), (128, (300, 2500, 70)), (128, (2304, 2304, 2304)), (256, (300, 2500, 70))])
+def test_attention_scores_without_a_value(sv, dtype, out_dtype, D, ctx):
+    """A NaN or +inf among the scores that a row sees makes that row NaN, as the formula does, and no other; a score of
+    -inf is a weight of zero."""
+    rng = np.random.default_rng(D + ctx[0])
+    N, H, K, bs = 12, 8, 2, 64
+    par = random_line_trees(rng, len(ctx), N)
+    c = tg.attention_case(rng, ctx, N, H, K, D, bs, dtype, par=par)
+    table, lens, par = c["host"]
+    q, k = c["q"], c["k"]
+    q[..., 5] = q[..., 5].abs() + 0.5                                    # signs of infinities are then known
+    row = lambda b, t: (int(table[b, t // bs]), t % bs)  # noqa: E731
+    q[0, 2, 3, 7] = float("nan")                                         # one row of one head
+    k[(*row(0, int(lens[0]) - N + 4), 1, 9)] = float("nan")              # a node: itself and its descendants
+    k[(*row(1, 1200 if lens[1] > 1300 else 40), 0, 5)] = float("nan")    # a committed token: all rows of a kv head
+    k[(*row(1, 30), 1, 5)] = float("-inf")                               # a weight of zero
+    k[(*row(2, 10), 0, 5)] = float("inf")
+    got, err = tg.run_attention(sv, c, out_dtype)
+    assert err == 0
+    keep = k.float().cpu().numpy()
+    for b in range(len(ctx)):                                            # slots that no row sees
+        for j in range(N):
+            if par[b, j] == to.UNUSED:
+                keep[row(b, int(lens[b]) - N + j)] = 0
+        for t in range(int(lens[b]), -(-int(lens[b]) // bs) * bs):
+            keep[row(b, t)] = 0
+    with np.errstate(invalid="ignore"):
+        ref, S = to.attention(q.float().cpu().numpy(), keep, c["clean"][2], table, lens, par)
+    x = got.double().cpu().numpy()
+    used = np.asarray(par) != to.UNUSED
+    nan = np.isnan(ref)
+    assert nan[0, 2, 3].all() and nan[1, used[1], :4].all() and nan[2, used[2], :4].all()
+    assert not nan[1, :, 4:].any() and not nan[2, :, 4:].any() and not nan[0, 0].any()
+    assert np.array_equal(np.isnan(x), nan)
+    tol = 2.0 ** -16 * S
+    if out_dtype != torch.float32:
+        tol = tol + HALF[out_dtype] * (S + np.abs(ref)) * (1 + 2.0 ** -6) + torch.finfo(out_dtype).smallest_normal
+    tol = tol + (2.0 ** -19 * np.abs(c["clean"][2]).max() if dtype == torch.float16 else 0.0)
+    assert np.all(np.abs(x - ref)[~nan] <= tol[~nan])
+
+
+def random_line_trees(rng, B, N):
+    par = np.zeros((B, N), np.int64)
+    for b in range(B):
+        for i in range(1, N):
+            par[b, i] = to.UNUSED if i >= N - b else rng.integers(0, i)
+        par[b, 0] = to.ROOT
+        par[b, 4] = 1
+    return par
