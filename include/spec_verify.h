@@ -507,7 +507,9 @@ int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
  *
  *  Random numbers as in spec_accept with the node index in place of the
  *  position: u_c uses word 0 of counter (0, c - 1, b, 0), the race at node n
- *  counter (x / 4, n, b, 1). On a chain the call computes what spec_accept does.
+ *  counter (x / 4, n, b, 1). On a chain the call computes what spec_accept does,
+ *  with exponents that stay exact to fp32 rounding at any T (spec_accept's lose
+ *  bits where max |logit| / T is past 2^12 or so).
  *
  *  target_logits [B, N, V] fp32, row n the target's logits after node n
  *  tokens        [B, N] int32; the token of node n (node 0's is not looked at)

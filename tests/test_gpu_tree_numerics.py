@@ -146,3 +146,47 @@ def random_line_trees(rng, B, N):
         par[b, 0] = to.ROOT
         par[b, 4] = 1
     return par
+
+
+# ---------------------------------------------------------------------------
+# Acceptance at temperatures near zero
+# ---------------------------------------------------------------------------
+def cold_case(rng, B, V, temperature, probs, offset=0.0):
+    """Rows whose node 0 has a largest logit of 10 to 30 and one, at some rows, within a few temperatures of it; the
+    children of every node hold the largest logit's token, the second's and one more."""
+    N = 7
+    c = tg.accept_case(rng, B, N, V, "sample", probs)
+    c["par"] = np.tile([-1, 0, 0, 0, 1, 1, 2], (B, 1))
+    c["temp"][:] = temperature
+    l = np.minimum(c["logits"], 9.0)
+    for b in range(B):
+        for n in range(N):
+            x, y = rng.choice(V, 2, replace=False)
+            top = np.float32(rng.uniform(10, 30))
+            l[b, n, x] = top
+            if (b + n) % 3 == 0:
+                l[b, n, y] = top - np.float32(temperature * rng.uniform(0, 3))
+            for j, i in enumerate(np.flatnonzero(c["par"][b] == n)):
+                c["tok"][b, i] = (x, y, (x + 1) % V)[(j + b) % 3]
+            if probs:
+                q = np.full(V, 0.2 / V, np.float32)
+                q[x] += 0.5
+                q[y] += 0.3
+                c["probs"][b, n] = q
+    c["logits"] = (l + np.float32(offset)).astype(np.float32)
+    return c
+
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("temperature,offset", [(1e-3, 0.0), (1e-5, 0.0), (1e-6, 0.0), (1e-8, 0.0), (1e-30, 0.0),
+                                                (1e-40, 0.0), (1.0, 1e4), (0.05, -3e4), (1e4, 0.0)])
+@pytest.mark.parametrize("B,V", [(160, 512), (24, 33000)])
+def test_accept_at_small_temperatures_and_large_logits(sv, B, V, temperature, offset, probs):
+    """Exponents of the softmax reach 10^9 and more; the decisions are those of 64 bits, and no row ends without a
+    token."""
+    c = cold_case(np.random.default_rng(V + int(probs)), B, V, temperature, probs, offset)
+    got, err = tg.run_accept(sv, c)
+    assert err == 0
+    m = tg.check_accept(c, got)
+    at = got[0][np.arange(B), np.maximum(m, 0)]
+    assert np.all(at >= 0) and (m.max() > 0 or temperature > 1)  # (a flat distribution accepts next to nothing)
