@@ -286,6 +286,15 @@ __global__ void __launch_bounds__(T, 512 / T) tree_accept_kernel(const Params p)
               s2 += fast_exp2((v[i].z - mx) * c2);
               s3 += fast_exp2((v[i].w - mx) * c2);
             }
+          } else {  // -inf all, or a NaN that the maximum passes over: as +inf, so that it reaches the row's sum
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < kNB; ++i)
+              nan |= v[i].x != v[i].x || v[i].y != v[i].y || v[i].z != v[i].z || v[i].w != v[i].w;
+            if (nan) {
+              mx = INFINITY;
+              s0 = __int_as_float(0x7fc00000);
+            }
           }
           gb += kStep;
           if (gb >= ngroups) break;
@@ -309,6 +318,12 @@ __global__ void __launch_bounds__(T, 512 / T) tree_accept_kernel(const Params p)
         for (int o = 16; o > 0; o >>= 1) {
           const float om = __shfl_xor_sync(kAll, M, o), os = __shfl_xor_sync(kAll, Z, o);
           ms_combine(M, Z, om, os, c2);
+        }
+        // A row without a distribution: no logit above -inf, or a NaN or +inf among them (the sum is then NaN). Uniform over
+        // the cluster: every warp holds the same values.
+        if (!(M > -INFINITY && Z < INFINITY)) {
+          last = -1;
+          break;
         }
         const float invZ = 1.f / Z;
 

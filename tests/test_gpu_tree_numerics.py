@@ -190,3 +190,58 @@ def test_accept_at_small_temperatures_and_large_logits(sv, B, V, temperature, of
     m = tg.check_accept(c, got)
     at = got[0][np.arange(B), np.maximum(m, 0)]
     assert np.all(at >= 0) and (m.max() > 0 or temperature > 1)  # (a flat distribution accepts next to nothing)
+
+
+# ---------------------------------------------------------------------------
+# Acceptance of rows that hold a NaN or an infinity
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("V", [700, 33000, 33001])
+def test_accept_one_entry_without_a_value(sv, V, value, probs):
+    """One NaN or +inf among the logits of an inner node (rows 1 to 3) or of a leaf (rows 4 to 6), in the first, a
+    middle and the last part of the vocabulary: the row ends there with -1; the others are as without it."""
+    B, N = 8, 5
+    c = tg.accept_case(np.random.default_rng(81), B, N, V, "sample", probs)
+    c["par"][:] = [-1, 0, 0, 1, 2]
+    c["tok"][:] = np.arange(B)[:, None] * 3 + np.arange(N)
+    c["logits"][4:7, 0] = -50.0
+    c["logits"][[4, 5, 6], 0, c["tok"][4:7, 1]] = 50.0        # node 1 is accepted for certain,
+    c["logits"][4:7, 1] = -50.0
+    c["logits"][[4, 5, 6], 1, c["tok"][4:7, 3]] = 50.0        # then its child, a leaf
+    good, err = tg.run_accept(sv, c)
+    bad = dict(c, logits=c["logits"].copy())
+    for r, x in enumerate((0, V // 2, V - 1)):
+        bad["logits"][1 + r, 0, x] = value
+        bad["logits"][4 + r, 3, x] = value
+    got, err2 = tg.run_accept(sv, bad)
+    assert err == 0 and err2 == 0
+    for x, y in zip(got, good):
+        assert np.array_equal(x[[0, 7]], y[[0, 7]])
+    for b in (1, 2, 3):
+        assert got[2][b] == 0 and got[1][b].tolist() == [0, -1, -1, -1, -1] and got[0][b].tolist() == [-1] * 5
+    for b in (4, 5, 6):
+        assert got[2][b] == 2 and got[1][b].tolist() == [0, 1, 3, -1, -1]
+        assert got[0][b].tolist() == [int(c["tok"][b, 1]), int(c["tok"][b, 3]), -1, -1, -1]
+
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("V", [1, 5, 700, 40000, 128256])
+def test_accept_a_nan_among_impossible_tokens(sv, V, probs):
+    """One NaN where all other entries of its neighbourhood are -inf (a masked vocabulary), or the only entry."""
+    B, N = 9, 3
+    c = tg.accept_case(np.random.default_rng(82), B, N, V, "sample", probs)
+    c["par"][:] = [-1, 0, 0]
+    keep = c["logits"][:, 0, : max(1, V // 50)].copy()
+    c["logits"][:, 0] = -np.inf
+    c["logits"][:, 0, : keep.shape[1]] = keep
+    good, err = tg.run_accept(sv, c)
+    bad = dict(c, logits=c["logits"].copy())
+    for b in range(1, B):
+        bad["logits"][b, 0, min(V - 1, V * b // (B - 1))] = np.nan
+    got, err2 = tg.run_accept(sv, bad)
+    assert err == 0 and err2 == 0
+    for x, y in zip(got, good):
+        assert np.array_equal(x[0], y[0])
+    assert np.all(good[0][:, 0] >= 0)
+    assert np.all(got[2][1:] == 0) and np.all(got[0][1:] == -1) and np.all(got[1][1:] == [0, -1, -1])
