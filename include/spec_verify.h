@@ -562,7 +562,7 @@ typedef struct spec_cache_desc {
  *
  *  block_table [B, max_blocks_per_seq] int32; ctx_lens [B] int32
  *  path [B, N] int32 and accept_len [B] int32 as written by spec_tree_accept
- *  new_lens [B] int32, not overlapping ctx_lens
+ *  new_lens [B] int32; shares no byte with the inputs above
  *
  * K and V are two caches: one pointer for both is refused.
  * A row with accept_len -1 moves nothing and gets new_lens = max(0, base).

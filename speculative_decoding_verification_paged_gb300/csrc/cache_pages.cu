@@ -383,10 +383,15 @@ extern "C" int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_
                                       spec_stream_t stream_) {
   if (!pages::tables_ok(d) || num_nodes < 1 || d->num_layers < 0 || d->token_bytes < 1) return SPEC_ERR_INVALID_ARG;
   if (d->batch == 0 || d->num_layers == 0) return SPEC_OK;
-  if (!k_cache || !v_cache || !block_table || !ctx_lens || !path || !accept_len || !new_lens || new_lens == ctx_lens)
-    return SPEC_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || !block_table || !ctx_lens || !path || !accept_len || !new_lens) return SPEC_ERR_INVALID_ARG;
   if (num_nodes > tree::kMaxNodes || !pages::tables_supported(d) || d->num_layers > 65535) return SPEC_ERR_UNSUPPORTED;
   if (d->num_layers > 0 && k_cache == v_cache) return SPEC_ERR_INVALID_ARG;  // two threads would move the same bytes
+  // new_lens is written while the blocks of other layers still read the inputs
+  const size_t rows = (size_t)d->batch * 4;
+  if (tree::overlap(new_lens, rows, ctx_lens, rows) || tree::overlap(new_lens, rows, accept_len, rows) ||
+      tree::overlap(new_lens, rows, path, rows * num_nodes) ||
+      tree::overlap(new_lens, rows, block_table, rows * d->max_blocks_per_seq))
+    return SPEC_ERR_INVALID_ARG;
   pages::PathParams p;
   p.k = static_cast<uint8_t*>(k_cache);
   p.v = static_cast<uint8_t*>(v_cache);

@@ -11,6 +11,12 @@ namespace tree {
 
 constexpr int kMaxNodes = 64;  // a node's ancestors fit one 64-bit word
 
+// Whether two arrays share a byte (host).
+inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // Whether entry i of the parent table `par` (any readable pointer) is allowed: unused, without a
 // parent, or the child of an earlier used node; node 0 has no parent.
 template <typename T>

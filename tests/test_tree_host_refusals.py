@@ -1,0 +1,26 @@
+"""Overlapping arguments and sizes past the limits, refused on the host (no GPU)."""
+
+import ctypes
+
+from test_tree_host import _cdesc, lib  # noqa: F401  (lib is a fixture)
+
+
+def at(n):
+    return ctypes.c_void_p(4096 * n)
+
+
+def inside(n, byte):
+    return ctypes.c_void_p(4096 * n + byte)
+
+
+def test_commit_path_refuses_results_over_its_inputs(lib):  # noqa: F811
+    """new_lens is written while other layers' blocks still read the inputs: batch 3, 4 nodes, 5 table columns."""
+    d = _cdesc(batch=3, max_blocks_per_seq=5)
+
+    def call(table=at(3), ctx=at(4), path=at(5), m=at(6), new=at(7)):
+        return lib.spec_cache_commit_path(at(1), at(2), table, ctx, path, m, new, 4, ctypes.byref(d), None, None)
+
+    for name, size in (("table", 60), ("ctx", 12), ("path", 48), ("m", 12)):
+        for byte in (0, 4, size - 4):
+            assert call(**{name: at(8), "new": inside(8, byte)}) == -1, (name, byte)
+        assert call(**{name: inside(8, 8), "new": at(8)}) == -1, name  # the result's last word
