@@ -27,7 +27,7 @@ struct PathParams {
   int32_t* new_lens;
   int32_t* dev_err;
   int64_t num_blocks, token_bytes;
-  int batch, layers, nodes, page, max_blocks;
+  int nodes, page, max_blocks;
 };
 
 template <typename Vec>
@@ -385,7 +385,7 @@ extern "C" int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_
   if (d->batch == 0 || d->num_layers == 0) return SPEC_OK;
   if (!k_cache || !v_cache || !block_table || !ctx_lens || !path || !accept_len || !new_lens) return SPEC_ERR_INVALID_ARG;
   if (num_nodes > tree::kMaxNodes || !pages::tables_supported(d) || d->num_layers > 65535) return SPEC_ERR_UNSUPPORTED;
-  if (d->num_layers > 0 && k_cache == v_cache) return SPEC_ERR_INVALID_ARG;  // two threads would move the same bytes
+  if (k_cache == v_cache) return SPEC_ERR_INVALID_ARG;  // two threads would move the same bytes
   // new_lens is written while the blocks of other layers still read the inputs
   const size_t rows = (size_t)d->batch * 4;
   if (tree::overlap(new_lens, rows, ctx_lens, rows) || tree::overlap(new_lens, rows, accept_len, rows) ||
@@ -403,8 +403,6 @@ extern "C" int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_
   p.dev_err = dev_err;
   p.num_blocks = d->num_blocks;
   p.token_bytes = d->token_bytes;
-  p.batch = d->batch;
-  p.layers = d->num_layers;
   p.nodes = num_nodes;
   p.page = d->block_size;
   p.max_blocks = d->max_blocks_per_seq;
