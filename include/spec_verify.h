@@ -521,6 +521,8 @@ int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
  *  out_tokens    [B, N] int32: the accepted nodes' tokens, the last token, -1s
  *  path          [B, N] int32: 0, the accepted nodes in order, -1s
  *  accept_len    [B] int32: accepted nodes, node 0 not counted
+ *  The three results share no byte with one another or with the int32 and
+ *  temperature inputs (refused otherwise).
  *
  * A visited node of a sampling row whose logits hold no distribution (all -inf, a
  * NaN, a +inf) ends the row: no child of it is accepted, the last token is -1.

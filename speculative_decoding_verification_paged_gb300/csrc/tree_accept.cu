@@ -538,6 +538,19 @@ extern "C" int spec_tree_accept(const float* target_logits, const int32_t* token
   if (!target_logits || !tokens || !parents || !mode || !temperature || !out_tokens || !path || !accept_len)
     return SPEC_ERR_INVALID_ARG;
   if (num_nodes > tree::kMaxNodes || vocab > acc::kMaxVocab) return SPEC_ERR_UNSUPPORTED;
+  // The results of a row with an error are written while other blocks of its cluster may still check it.
+  const size_t rows = (size_t)batch * 4, nodes = rows * num_nodes;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } results[3] = {{out_tokens, nodes}, {path, nodes}, {accept_len, rows}},
+    inputs[4] = {{tokens, nodes}, {parents, nodes}, {mode, rows}, {temperature, rows}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& x : inputs)
+      if (tree::overlap(results[i].at, results[i].bytes, x.at, x.bytes)) return SPEC_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (tree::overlap(results[i].at, results[i].bytes, results[j].at, results[j].bytes)) return SPEC_ERR_INVALID_ARG;
+  }
   const int dev = current_device();
   if (dev < 0) return SPEC_ERR_LAUNCH;
   acc::Config c;

@@ -24,3 +24,15 @@ def test_commit_path_refuses_results_over_its_inputs(lib):  # noqa: F811
         for byte in (0, 4, size - 4):
             assert call(**{name: at(8), "new": inside(8, byte)}) == -1, (name, byte)
         assert call(**{name: inside(8, 8), "new": at(8)}) == -1, name  # the result's last word
+
+
+def test_tree_accept_refuses_results_over_its_inputs(lib):  # noqa: F811
+    def call(tokens=at(2), par=at(3), mode=at(4), temp=at(5), out=at(6), path=at(7), m=at(8)):
+        return lib.spec_tree_accept(at(1), tokens, par, None, 1, mode, temp, out, path, m, 3, 4, 100, None, None)
+
+    for result in ("out", "path", "m"):
+        for name in ("tokens", "par", "mode", "temp"):
+            assert call(**{name: at(9), result: at(9)}) == -1, (result, name)
+    for a, b in (("out", "path"), ("out", "m"), ("path", "m")):
+        assert call(**{a: at(9), b: at(9)}) == -1
+    assert call(out=at(9), path=inside(9, 44)) == -1
