@@ -618,7 +618,7 @@ int spec_cache_commit_path(void* k_cache, void* v_cache, const int32_t* block_ta
  * token in an entry outside [0, num_blocks) (SPEC_DEVERR_BLOCK_ID) keeps its
  * entries as they are. Entries that find no free page are -1
  * (SPEC_DEVERR_NO_PAGE). Supported: B * max_blocks_per_seq <= 2^30;
- * num_blocks <= 2^30.
+ * num_blocks <= 2^30; (max_blocks_per_seq + 1) * bs <= 2^31.
  */
 size_t spec_cache_update_workspace(const spec_cache_desc* d);
 

@@ -363,7 +363,7 @@ static bool tables_ok(const spec_cache_desc* d) {
 
 static bool tables_supported(const spec_cache_desc* d) {
   return d->block_size <= 65536 && (int64_t)d->batch * d->max_blocks_per_seq <= (1 << 30) && d->num_blocks <= (1 << 30) &&
-         (int64_t)d->max_blocks_per_seq * d->block_size <= INT32_MAX;
+         (int64_t)d->max_blocks_per_seq * d->block_size + d->block_size - 1 <= INT32_MAX;  // lengths are rounded up to pages
 }
 
 // Bytes that every token row of both caches can be accessed with at once: 16, 4 or 1.

@@ -36,3 +36,12 @@ def test_tree_accept_refuses_results_over_its_inputs(lib):  # noqa: F811
     for a, b in (("out", "path"), ("out", "m"), ("path", "m")):
         assert call(**{a: at(9), b: at(9)}) == -1
     assert call(out=at(9), path=inside(9, 44)) == -1
+
+
+def test_tables_whose_token_counts_do_not_fit_are_refused(lib):  # noqa: F811
+    """ceil(length / block_size) is worked out in 32 bits: max_blocks_per_seq * block_size + block_size - 1 has to fit."""
+    most = (1 << 31) - 1
+    for page, width, ok in ((3, (most - 2) // 3, True), (3, (most - 2) // 3 + 1, False), (1, 1 << 30, True),
+                            (65536, 32766, True), (65536, 32767, True), (65536, 32768, False)):
+        size = lib.spec_cache_update_workspace(ctypes.byref(_cdesc(batch=1, block_size=page, max_blocks_per_seq=width)))
+        assert (size > 0) == ok, (page, width)
