@@ -589,7 +589,10 @@ def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: in
     _need_shape(new_lens, "new_lens", torch.int32, (B,), dev)
     if src_rows is not None:
         _need_shape(src_rows, "src_rows", torch.int32, (B,), dev)
-    d = _CacheDesc(B, 0, int(block_size), W, page_refs.shape[0], 1)
+    block_size = int(block_size)
+    if not -2 ** 31 <= block_size < 2 ** 31:  # the field would hold its low 32 bits
+        raise ValueError(f"block_size {block_size} does not fit 32 bits")
+    d = _CacheDesc(B, 0, block_size, W, page_refs.shape[0], 1)
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache and v_cache go together")
     if k_cache is not None:

@@ -245,3 +245,10 @@ def test_accept_a_nan_among_impossible_tokens(sv, V, probs):
         assert np.array_equal(x[0], y[0])
     assert np.all(good[0][:, 0] >= 0)
     assert np.all(got[2][1:] == 0) and np.all(got[0][1:] == -1) and np.all(got[1][1:] == [0, -1, -1])
+
+
+@pytest.mark.parametrize("size", [(1 << 32) + 4, 1 << 31, -(1 << 32) + 4])
+def test_update_refuses_block_sizes_past_32_bits(sv, size):
+    table, refs, n = (torch.zeros(s, dtype=torch.int32, device=DEV) for s in ((1, 2), (4,), (1,)))
+    with pytest.raises(ValueError):
+        sv.spec_cache_update(table, refs, n, n, size)
