@@ -97,6 +97,10 @@ typedef struct spec_attn_desc {
  * workspace's first use. */
 #define SPEC_ATTN_COUNTER_BYTES 4096
 
+/* Zeroes the counters of a new attention workspace (256-byte aligned, at least
+ * SPEC_ATTN_COUNTER_BYTES), asynchronously on `stream`. */
+int spec_attention_workspace_init(void* workspace, size_t workspace_bytes, spec_stream_t stream);
+
 /*
  * Bytes of device workspace spec_verify_attention needs for `d`: room for the
  * split-KV partial results (normalised partial outputs and their log-sum-exp)

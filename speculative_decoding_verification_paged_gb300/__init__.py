@@ -139,6 +139,8 @@ def load_library():
         lib.spec_gdn_verify_pooled.argtypes = [P, P, P, P, P, ctypes.c_float, P, i64, P, P, P, i32, i32, i32, i32,
                                                 i32, i32, i32, P, P]
         lib.spec_gdn_verify_pooled.restype = ctypes.c_int
+        lib.spec_attention_workspace_init.argtypes = [P, sz, P]
+        lib.spec_attention_workspace_init.restype = ctypes.c_int
         lib.spec_tree_attention_workspace.argtypes = [ctypes.POINTER(_AttnDesc), i32]
         lib.spec_tree_attention_workspace.restype = sz
         lib.spec_tree_attention.argtypes = [P, P, P, P, P, P, i32, P, i32, i32, ctypes.POINTER(_AttnDesc), P, sz, P, P]
@@ -235,9 +237,15 @@ def spec_verify_attention_plan(q: torch.Tensor, k_cache: torch.Tensor, block_tab
 
 
 def new_attention_workspace(nbytes: int, device) -> torch.Tensor:
-    """A workspace for spec_verify_attention and spec_tree_attention: zero-filled once (on the current stream), reusable
-    on one stream by later calls of both, of any shape that it is large enough for."""
-    return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    """A workspace for spec_verify_attention and spec_tree_attention: its counters zeroed once (on the current stream),
+    the rest left as it is; reusable on one stream by later calls of both, of any shape that it is large enough for."""
+    ws = torch.empty(max(int(nbytes), ATTN_COUNTER_BYTES), dtype=torch.uint8, device=device)
+    if ws.get_device() == torch.cuda.current_device():
+        _check("spec_attention_workspace_init",
+               load_library().spec_attention_workspace_init(ws.data_ptr(), ws.numel(), _stream_of(None, ws.get_device())))
+    else:
+        ws[:ATTN_COUNTER_BYTES].zero_()
+    return ws
 
 
 def spec_verify_attention(q, k_cache, v_cache, block_table, ctx_lens, k_draft: int, out,
@@ -466,8 +474,8 @@ def _need_shape(t, name: str, dtype, shape, dev: int):
 
 
 def spec_tree_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor) -> int:
-    """Workspace bytes spec_tree_attention needs for these shapes (zero-filled before its first use:
-    new_attention_workspace)."""
+    """Workspace bytes spec_tree_attention needs for these shapes (made by new_attention_workspace, or with its first
+    ATTN_COUNTER_BYTES bytes zeroed before its first use)."""
     d = _attn_desc(q, k_cache, block_table)
     return int(load_library().spec_tree_attention_workspace(ctypes.byref(d), int(q.shape[1])))
 

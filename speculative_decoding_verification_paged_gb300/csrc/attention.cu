@@ -352,6 +352,14 @@ static int dispatch(const Params& p, const Prepared& pr, int D, int bs, const vo
 
 using namespace specv;
 
+extern "C" int spec_attention_workspace_init(void* workspace, size_t workspace_bytes, spec_stream_t stream) {
+  if (workspace == nullptr || workspace_bytes < SPEC_ATTN_COUNTER_BYTES) return SPEC_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return SPEC_ERR_INVALID_ARG;
+  return cudaMemsetAsync(workspace, 0, SPEC_ATTN_COUNTER_BYTES, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_LAUNCH;
+}
+
 extern "C" size_t spec_verify_attention_workspace(const spec_attn_desc* d, int32_t k_draft) {
   if (!attn::desc_ok(d, k_draft)) return 0;
   return attn::layout_for(d, k_draft).total;

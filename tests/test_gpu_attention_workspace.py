@@ -84,3 +84,16 @@ def test_small_call_then_large_call_of_the_chain(sv):
     ws = sv.new_attention_workspace(max(bytes_for(sv, c) for c in (small, large)), DEV)
     call(sv, small, ws)
     tg.check_attention(large, call(sv, large, ws))
+
+
+def test_a_new_workspace_zeroes_its_counters_alone(sv):
+    """A call without a workspace pays for the counters, not for tens of megabytes: the rest is what the allocator's
+    block held."""
+    n = 48 << 20
+    old = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    at = old.data_ptr()
+    del old
+    ws = sv.new_attention_workspace(n, DEV)
+    assert ws.data_ptr() == at and not bool(ws[: sv.ATTN_COUNTER_BYTES].any())
+    assert bool((ws[sv.ATTN_COUNTER_BYTES:] == 255).all())
+    assert sv.new_attention_workspace(0, DEV).numel() == sv.ATTN_COUNTER_BYTES

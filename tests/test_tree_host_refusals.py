@@ -45,3 +45,9 @@ def test_tables_whose_token_counts_do_not_fit_are_refused(lib):  # noqa: F811
                             (65536, 32766, True), (65536, 32767, True), (65536, 32768, False)):
         size = lib.spec_cache_update_workspace(ctypes.byref(_cdesc(batch=1, block_size=page, max_blocks_per_seq=width)))
         assert (size > 0) == ok, (page, width)
+
+
+def test_workspace_init_refusals(lib):  # noqa: F811
+    assert lib.spec_attention_workspace_init(None, 1 << 20, None) == -4
+    assert lib.spec_attention_workspace_init(at(1), 4095, None) == -4
+    assert lib.spec_attention_workspace_init(inside(1, 16), 4096, None) == -1
