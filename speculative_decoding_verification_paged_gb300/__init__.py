@@ -267,7 +267,8 @@ def spec_verify_attention(q, k_cache, v_cache, block_table, ctx_lens, k_draft: i
     d = _attn_desc(q, k_cache, block_table)
     need = int(lib.spec_verify_attention_workspace(ctypes.byref(d), int(k_draft)))
     if workspace is None:
-        workspace = new_attention_workspace(need, q.device)
+        with _on(stream):
+            workspace = new_attention_workspace(need, q.device)
     _need(workspace, "workspace", torch.uint8, 1)
     rc = lib.spec_verify_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens),
                                    int(k_draft), _ptr(out), ctypes.byref(d), _ptr(workspace),

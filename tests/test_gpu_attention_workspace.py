@@ -97,3 +97,22 @@ def test_a_new_workspace_zeroes_its_counters_alone(sv):
     assert ws.data_ptr() == at and not bool(ws[: sv.ATTN_COUNTER_BYTES].any())
     assert bool((ws[sv.ATTN_COUNTER_BYTES:] == 255).all())
     assert sv.new_attention_workspace(0, DEV).numel() == sv.ATTN_COUNTER_BYTES
+
+
+def test_the_chain_calls_own_workspace_belongs_to_its_stream(sv):
+    """A chain call on a given stream without a workspace waits for nothing on the current one, and is right when that
+    is busy."""
+    c = chain_case(np.random.default_rng(63), (3000, 700, 90), 3, 32, 8, 128)
+    want = call(sv, c, None)
+    out = torch.full_like(want, float("nan"))
+    dirty = torch.full((96 << 20,), 255, dtype=torch.uint8, device=DEV)  # what a reused block would hold
+    del dirty
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    done.record()
+    sv.spec_verify_attention(c["q"], c["k"], c["v"], c["table"], c["ctx"], 3, out, stream=side)
+    side.synchronize()
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
