@@ -462,7 +462,11 @@ int spec_gdn_verify_pooled(const float* q, const float* k, const float* v, const
  *  ctx_lens    [B] int32, tokens in the cache, the N tree slots included; must
  *              lie in [N, max_blocks_per_seq * bs]
  *  parents     [B, N] int32
- *  out         [B, N, Hq, D] of type `out_dtype`: fp32, or `dtype`
+ *  out         [B, N, Hq, D] of type `out_dtype`: fp32, or `dtype`. For the latter
+ *              the softmax weights are rounded once to `dtype` before they meet V
+ *              (an error of up to half its step of sum p |v|, beside the output's
+ *              own rounding); for fp32 they keep 22 to 24 bits (fp16: down to
+ *              2^-36 of the row's largest weight).
  *  workspace   >= spec_tree_attention_workspace(d, N) bytes, 256-byte aligned,
  *              its first SPEC_ATTN_COUNTER_BYTES bytes ZERO-FILLED before its
  *              first use; reusable by later calls of any shape, and of

@@ -89,7 +89,9 @@ struct Cfg {
   // in all (the fp32 accumulator and row sum have that room). A step then leaves 2^-36 min(p, 2^FALL w) of a key, p the
   // row's and w the tile's largest weight; with LAG 8 and neither shift nor fall it was 2^-25 p, all of a key 17 nats
   // below a first token that takes most of the attention. What it costs (32 sequences of 2048, 64 nodes, head dim 128, in
-  // a graph, with and without): scores of standard deviation 1 66.3 and 65.6 us, of 3 78.6 and 70.1, of 6 78.5 and 76.5.
+  // a graph, with and without): scores of standard deviation 1 65.1 to 66.3 and 65.1 to 65.6 us, of 3 78 and 70, of 6 78
+  // and 76.5. The shift is added in the exponent, whose rounding grows with it: scores of deviation 1 at head dim 64 come
+  // out 3.6 to 4.9e-7 off instead of 2.6 to 3.3e-7. A multiplication after it (3.0 to 4.4e-7) takes up to 4% longer.
   static constexpr float SHIFT = FP16 ? 11.f : 0.f, LAG = FP16 ? 4.f : 8.f, FALL = FP16 ? 10.f : 0.f, DEPTH = 40.f;
   static_assert(!FP16 || SHIFT + LAG <= 15.f, "weights stay below fp16's largest value");
   static_assert(X_BYTES >= kAlignBatch * 4 && kThreads >= kAlignBatch, "");
