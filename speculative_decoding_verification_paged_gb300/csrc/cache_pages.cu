@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) update_table_kernel(const Ta
 
 // Copies of partly filled pages: CTA (row, layer, K or V). A stream at HBM speed; eight 16-byte loads a thread are in
 // flight before the first store. Launched early behind the table kernel, it waits for that kernel's results. A fork with
-// 235 MB of partial pages takes 35 to 46 us with the table's update, 34.6 us at copy rate.
+// 235 MB of partial pages takes 43 to 48 us with the table's update (41 in a graph), 34.6 us at copy rate.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBatch = 8;
 

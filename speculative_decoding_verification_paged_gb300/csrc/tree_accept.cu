@@ -21,8 +21,8 @@
 // node, the target logit and the draft probability, whose loads are in flight
 // during the statistics pass. In registers they would spill in the race.
 //
-// What bounds it (one GB300, L2 flushed): 32 rows of 128K entries, sampled, 42 us;
-// the roots alone are 16.4 MB, 2.4 us. DRAM is 26% busy and the stalls are on loads:
+// What bounds it (one GB300, L2 flushed): 32 rows of 128K entries, sampled, 38 to 45 us
+// by the draws; the roots alone are 16.4 MB, 2.4 us. DRAM is 26% busy and the stalls are on loads:
 // each visited node is a chain of dependent passes over its row, and the race after
 // the last one draws a uniform for every entry.
 #include <math.h>

@@ -32,8 +32,8 @@
 // What bounds it (one GB300, L2 flushed): batch 32, 64 nodes, 32/8 heads, head dim
 // 128, context 2K: 71 us of 44.5 us for its bytes; tensor pipe 38% active, DRAM 49%,
 // so neither: the chain scores -> softmax -> product and the ends of units. Contexts of
-// 32K to 128K: 508 to 628 us of 395 us, at about 1370 W, where the clock falls to about
-// 1.6 GHz. Head dim 256, fp32 output: 480 to 521 us of 341 us, in a graph 480; there
+// 32K to 128K: 491 to 628 us of 395 us, at about 1370 W, where the clock falls to about
+// 1.6 GHz. Head dim 256, fp32 output: 462 to 521 us of 341 us, in a graph 485; there
 // 430 without folds (256 KB a CTA through L2, about 5000 cycles each) and 398 with
 // 16-bit output.
 #include <math.h>
