@@ -240,7 +240,7 @@ def new_attention_workspace(nbytes: int, device) -> torch.Tensor:
     """A workspace for spec_verify_attention and spec_tree_attention: its counters zeroed once (on the current stream),
     the rest left as it is; reusable on one stream by later calls of both, of any shape that it is large enough for."""
     ws = torch.empty(max(int(nbytes), ATTN_COUNTER_BYTES), dtype=torch.uint8, device=device)
-    if ws.get_device() == torch.cuda.current_device():
+    if ws.is_cuda and ws.get_device() == torch.cuda.current_device():
         _check("spec_attention_workspace_init",
                load_library().spec_attention_workspace_init(ws.data_ptr(), ws.numel(), _stream_of(None, ws.get_device())))
     else:

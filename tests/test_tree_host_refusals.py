@@ -51,3 +51,9 @@ def test_workspace_init_refusals(lib):  # noqa: F811
     assert lib.spec_attention_workspace_init(None, 1 << 20, None) == -4
     assert lib.spec_attention_workspace_init(at(1), 4095, None) == -4
     assert lib.spec_attention_workspace_init(inside(1, 16), 4096, None) == -1
+
+
+def test_workspaces_on_the_host_need_no_device():
+    import speculative_decoding_verification_paged_gb300 as sv
+    ws = sv.new_attention_workspace(10000, "cpu")
+    assert ws.numel() == 10000 and not bool(ws[: sv.ATTN_COUNTER_BYTES].any())
