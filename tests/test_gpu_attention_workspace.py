@@ -116,3 +116,24 @@ def test_the_chain_calls_own_workspace_belongs_to_its_stream(sv):
     assert not done.query()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_calls_without_a_workspace_in_a_graph(sv):
+    """The clearing of the counters is captured with the call: replays on new inputs are right."""
+    rng = np.random.default_rng(64)
+    for make in (lambda: chain_case(rng, (3000, 700, 90), 3, 32, 8, 128), lambda: tree_case(rng, (2500, 900, 64), 16, 16, 2, 128)):
+        c = make()
+        call(sv, c, None)
+        out = torch.full(c["q"].shape, float("nan"), device=DEV)
+        args = (c["q"], c["k"], c["v"], c["table"], c["ctx"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if "k_draft" in c:
+                sv.spec_verify_attention(*args, c["k_draft"], out)
+            else:
+                sv.spec_tree_attention(*args, c["par"], out)
+        for _ in range(3):
+            c["q"].copy_(torch.randn(c["q"].shape, device=DEV))
+            out.fill_(float("nan"))
+            g.replay()
+            assert torch.equal(call(sv, c, None), out)
