@@ -635,6 +635,129 @@ int spec_cache_update(int32_t* block_table, int32_t* page_refs, const int32_t* c
                       void* v_cache, const spec_cache_desc* d, void* workspace,
                       size_t workspace_bytes, int32_t* dev_err, spec_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* 8. Verify attention over a window of the cache, and over a 4-bit cache     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * out[b, i, h, :] = softmax_t( q[b,i,h,:] . K[b,t,g,:] / sqrt(D) ) . V[b,t,g,:]
+ * for every sequence b, row i in [0, num_rows), query head h, with g = h / G
+ * (contiguous GQA groups). Row i is the token at p = ctx_lens[b] - num_rows + i;
+ * it sees the tokens
+ *
+ *   t <= p  with  window = 0, or t > p - window, or t < sinks,
+ *
+ * that is the last `window` tokens, itself included, and the first `sinks`.
+ * num_rows = 1 is a step of plain decoding; a verify step has k + 1 rows.
+ *
+ *  q           [B, num_rows, Hq, D] of type `dtype` (SPEC_DTYPE_BF16 or _FP16)
+ *  k_cache     [num_blocks, bs, Hkv, D] of type `dtype`; the rows' own K and V
+ *  v_cache     are in the cache already. Slots that no row of the sequence sees
+ *              may hold anything, NaN included, and pages that hold only such
+ *              slots are not looked at (their block_table entry may be anything).
+ *              A NaN or +inf among the scores that a row sees makes that row NaN,
+ *              a score of -inf is a weight of 0; a NaN or infinity in the V of a
+ *              slot that only other rows of the sequence see may reach the row.
+ *  block_table [B, max_blocks_per_seq] int32
+ *  ctx_lens    [B] int32, tokens in the cache, the rows' own included: 0 (an empty
+ *              row of a padded batch: out rows of zeros, no error), or in
+ *              [num_rows, max_blocks_per_seq * bs]
+ *  out         [B, num_rows, Hq, D] of type `dtype`. The softmax weights are rounded
+ *              once to 16 bits before they meet V (an error of up to half a step of
+ *              sum p |v|, beside the output's own rounding).
+ *  workspace   >= spec_window_attention_workspace(d, num_rows) bytes, 256-byte
+ *              aligned, its first SPEC_ATTN_COUNTER_BYTES bytes ZERO-FILLED before
+ *              its first use; one workspace serves every attention call of any
+ *              shape that it is large enough for, on one stream (two calls in
+ *              flight at once, or two captured graphs that may run at once, need two
+ *              workspaces).
+ *
+ * Device errors: a sequence with another ctx_len (SPEC_DEVERR_CTX_LEN) or a block
+ * id outside the cache among the pages that it sees (SPEC_DEVERR_BLOCK_ID) gets out
+ * rows of zeros. Device pointers 16-byte aligned.
+ * Supported: D in {64,128,256}; bs in {16,32,64,128}; num_rows <= 64; G <= 64;
+ * B <= 4096; with groups = ceil(num_rows / floor(64 / G)), at most 2^31 - 1 key
+ * tiles: (max_blocks_per_seq * bs / 128 + 2) * B * Hkv * groups;
+ * max_blocks_per_seq * bs at most 2^30; num_blocks * bs at most 2^31 - 1.
+ */
+size_t spec_window_attention_workspace(const spec_attn_desc* d, int32_t num_rows);
+
+int spec_window_attention(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, const int32_t* ctx_lens,
+                          int32_t num_rows, int32_t window, int32_t sinks, void* out,
+                          int32_t dtype, const spec_attn_desc* d, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_err, spec_stream_t stream);
+
+/*
+ * A cache in 4 bits. For every token and kv head the D elements x_e are held as
+ *
+ *   m = min x,  s = round16((max x - min x) / 15),  n_e = round((x_e - m) / s) in 0..15
+ *
+ * (the quotient rounded half to even; n = 0 where s = 0) and stand for n_e s + m. s
+ * and m have the 16-bit type of the model, `dtype` in every call; a NaN or infinity
+ * among the x makes all D elements NaN. The range is divided in fp32.
+ *
+ * k_cache and v_cache are [num_blocks, bs, row_bytes] bytes each, row_bytes =
+ * spec_q4_row_bytes(Hkv, D). A token's row holds, for every kv head in turn, D / 2
+ * bytes of codes (n_2i in the low, n_2i+1 in the high half of byte i); then, for
+ * every kv head, s and m; then padding to 16 bytes, which no call looks at. A row is
+ * whole in itself, so spec_cache_update and spec_cache_commit_path move tokens of
+ * such caches too, with token_bytes = row_bytes.
+ *
+ * spec_q4_row_bytes returns 0 for D not in {64,128,256} or Hkv outside [1, 65536].
+ */
+int64_t spec_q4_row_bytes(int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * Writes the newest num_rows tokens of every sequence into a 4-bit cache: row i of
+ * sequence b becomes token ctx_lens[b] - num_rows + i. Rows before token 0 are padding
+ * (a batch of prompts of several lengths, aligned at their ends) and are not read;
+ * nothing but the tokens' codes, s and m is written.
+ *
+ *  k, v        [B, num_rows, Hkv, D] of type `dtype`, k_stride and v_stride elements
+ *              from one row to the next (at least Hkv * D, a multiple of 8): slices
+ *              of a projection's output do
+ *  block_table [B, max_blocks_per_seq] int32
+ *  ctx_lens    [B] int32, tokens in the cache once these are in it
+ *  d           num_q_heads is not looked at
+ *
+ * Device errors: a sequence whose ctx_len lies outside [0, max_blocks_per_seq * bs]
+ * (SPEC_DEVERR_CTX_LEN) and a token whose page lies outside the cache
+ * (SPEC_DEVERR_BLOCK_ID) are not written. Tokens must not share a slot. K and V are
+ * two caches: one pointer for both is refused. Device pointers 16-byte aligned.
+ * Supported: D in {64,128,256}; bs in {16,32,64,128}; B * num_rows * Hkv * D / 8 and
+ * num_blocks * bs at most 2^31 - 1; max_blocks_per_seq * bs at most 2^30.
+ */
+int spec_cache_store_q4(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                        const int32_t* block_table, const int32_t* ctx_lens, int32_t num_rows,
+                        void* k_cache, void* v_cache, int32_t dtype, const spec_attn_desc* d,
+                        int32_t* dev_err, spec_stream_t stream);
+
+/*
+ * Reads the newest num_rows tokens of every sequence back: k_out, v_out
+ * [B, num_rows, Hkv, D] of type `out_dtype` (`dtype` or fp32; n s + m is rounded to
+ * fp32, then to `dtype`). Rows before token 0, rows of sequences with a bad ctx_len and
+ * of tokens with a bad page (errors as above) are zeros. Limits as above.
+ */
+int spec_cache_load_q4(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int32_t* ctx_lens, int32_t num_rows, void* k_out, void* v_out,
+                       int32_t dtype, int32_t out_dtype, const spec_attn_desc* d,
+                       int32_t* dev_err, spec_stream_t stream);
+
+/*
+ * spec_window_attention over a 4-bit cache: q and out of type `dtype`, which is that
+ * of the cache's s and m too. Arguments, visibility (window = 0 for all tokens),
+ * workspace, errors and limits are those of spec_window_attention; there is no
+ * exception for V: what a row does not see cannot reach it.
+ * q is held as fp16 times a power of two of its row (elements below 2^-24 of the row's
+ * largest lose bits), the weights times s as fp16 times a power of two of the row.
+ */
+int spec_q4_attention(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_table, const int32_t* ctx_lens, int32_t num_rows,
+                      int32_t window, int32_t sinks, void* out, int32_t dtype,
+                      const spec_attn_desc* d, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_err, spec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,13 @@ and, for a tree of drafts instead of a chain:
                      temperature, out_tokens, path, accept_len)
     spec_cache_commit_path(k_cache, v_cache, block_table, ctx_lens, path, accept_len, new_lens)
     spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size)
+
+over a window of the cache, and over a cache in 4 bits:
+
+    spec_window_attention(q, k_cache, v_cache, block_table, ctx_lens, out, window, sinks)
+    spec_cache_store_q4(k, v, block_table, ctx_lens, k_cache, v_cache)
+    spec_cache_load_q4(k_cache, v_cache, block_table, ctx_lens, k_out, v_out)
+    spec_q4_attention(q, k_cache, v_cache, block_table, ctx_lens, kv_heads, out, window, sinks)
 """
 
 from __future__ import annotations
@@ -40,6 +47,8 @@ __all__ = [
     "spec_gdn_verify_pooled", "status_string",
     "spec_tree_attention", "spec_tree_attention_workspace", "spec_tree_accept", "spec_cache_commit_path",
     "spec_cache_update", "spec_cache_update_workspace",
+    "spec_window_attention", "spec_window_attention_workspace", "spec_q4_attention", "spec_cache_store_q4",
+    "spec_cache_load_q4", "q4_row_bytes", "new_q4_cache",
     "ATTN_COUNTER_BYTES", "DEVERR", "MODE_GREEDY", "MODE_SAMPLE", "ALIGN_TOKEN", "ALIGN_LAST", "TREE_ROOT", "TREE_UNUSED",
 ]
 
@@ -153,6 +162,17 @@ def load_library():
         lib.spec_cache_update_workspace.restype = sz
         lib.spec_cache_update.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(_CacheDesc), P, sz, P, P]
         lib.spec_cache_update.restype = ctypes.c_int
+        lib.spec_window_attention_workspace.argtypes = [ctypes.POINTER(_AttnDesc), i32]
+        lib.spec_window_attention_workspace.restype = sz
+        for fn in (lib.spec_window_attention, lib.spec_q4_attention):
+            fn.argtypes = [P, P, P, P, P, i32, i32, i32, P, i32, ctypes.POINTER(_AttnDesc), P, sz, P, P]
+            fn.restype = ctypes.c_int
+        lib.spec_q4_row_bytes.argtypes = [i32, i32]
+        lib.spec_q4_row_bytes.restype = i64
+        lib.spec_cache_store_q4.argtypes = [P, P, i64, i64, P, P, i32, P, P, i32, ctypes.POINTER(_AttnDesc), P, P]
+        lib.spec_cache_store_q4.restype = ctypes.c_int
+        lib.spec_cache_load_q4.argtypes = [P, P, P, P, i32, P, P, i32, i32, ctypes.POINTER(_AttnDesc), P, P]
+        lib.spec_cache_load_q4.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -622,3 +642,172 @@ def spec_cache_update(block_table, page_refs, cur_lens, new_lens, block_size: in
                                workspace.numel(), _err_ptr(dev_err), _stream_of(stream, dev))
     _check("spec_cache_update", rc)
     return block_table, page_refs
+
+
+# ---------------------------------------------------------------------------
+# Windowed attention, and the cache in 4 bits
+# ---------------------------------------------------------------------------
+def spec_window_attention_workspace(q: torch.Tensor, kv_heads: int, block_table: torch.Tensor) -> int:
+    """Workspace bytes spec_window_attention and spec_q4_attention need for these shapes (made by
+    new_attention_workspace, or with its first ATTN_COUNTER_BYTES bytes zeroed before its first use)."""
+    B, R, Hq, D = q.shape
+    d = _AttnDesc(B, Hq, int(kv_heads), D, 16, 1, 1)  # the page size and the caches' sizes do not matter
+    return int(load_library().spec_window_attention_workspace(ctypes.byref(d), R))
+
+
+def _int32(value, name: str) -> int:
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} {value} does not fit 32 bits")
+    return value
+
+
+def _paged_attention(fn: str, q, block_table, ctx_lens, out, d, window, sinks, workspace, k_cache, v_cache, dev_err, stream,
+                     dev: int):
+    """What the two calls share once their caches are known to be right."""
+    lib = load_library()
+    B, R, _, _ = q.shape
+    _need_shape(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    _need_shape(out, "out", q.dtype, q.shape, dev)
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
+    if workspace is None:
+        with _on(stream):
+            workspace = new_attention_workspace(int(lib.spec_window_attention_workspace(ctypes.byref(d), R)), q.device)
+    _need_dims(workspace, "workspace", torch.uint8, 1, dev)
+    rc = getattr(lib, fn)(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(),
+                          R, window, sinks, out.data_ptr(), _DTYPE_CODES[q.dtype], ctypes.byref(d), workspace.data_ptr(),
+                          workspace.numel(), _err_ptr(dev_err), _stream_of(stream, dev))
+    _check(fn, rc)
+    return out
+
+
+def _need_queries(q, block_table, dev: int):
+    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be a bfloat16 or float16 tensor")
+    _need_dims(q, "q", q.dtype, 4, dev)
+    _need_dims(block_table, "block_table", torch.int32, 2, dev)
+    if block_table.shape[0] != q.shape[0]:
+        raise ValueError(f"block_table must have {q.shape[0]} rows, got {block_table.shape[0]}")
+
+
+def spec_window_attention(q, k_cache, v_cache, block_table, ctx_lens, out, window: int = 0, sinks: int = 0,
+                          workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of the newest R tokens of every sequence over a paged 16-bit cache into `out` [B, R, Hq, D]: a row sees
+    the last `window` tokens (0: all) and the first `sinks` ones (see spec_verify.h). q, caches and out are all bf16 or
+    all fp16."""
+    dev = torch.cuda.current_device()
+    _need_queries(q, block_table, dev)
+    _need_dims(k_cache, "k_cache", q.dtype, 4, dev)
+    _need_shape(v_cache, "v_cache", q.dtype, k_cache.shape, dev)
+    return _paged_attention("spec_window_attention", q, block_table, ctx_lens, out, _attn_desc(q, k_cache, block_table),
+                            window, sinks, workspace, k_cache, v_cache, dev_err, stream, dev)
+
+
+def q4_row_bytes(kv_heads: int, head_dim: int) -> int:
+    """Bytes of a token's row in a 4-bit cache."""
+    size = int(load_library().spec_q4_row_bytes(_int32(kv_heads, "kv_heads"), _int32(head_dim, "head_dim")))
+    if size == 0:
+        raise ValueError(f"no 4-bit cache for {kv_heads} kv heads of {head_dim}")
+    return size
+
+
+def new_q4_cache(num_blocks: int, block_size: int, kv_heads: int, head_dim: int, device,
+                 num_layers: Optional[int] = None) -> torch.Tensor:
+    """A zeroed 4-bit cache for K or V, [num_blocks, block_size, 1, row bytes] uint8, or with num_layers in front:
+    spec_cache_update and spec_cache_commit_path take it as they take 16-bit caches."""
+    shape = (num_blocks, block_size, 1, q4_row_bytes(kv_heads, head_dim))
+    return torch.zeros(shape if num_layers is None else (num_layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _need_q4_caches(k_cache, v_cache, kv_heads: int, head_dim: int, dev: int):
+    """Two 4-bit caches of one layer: (pages, page size)."""
+    _need_dims(k_cache, "k_cache", torch.uint8, 4, dev)
+    row = q4_row_bytes(kv_heads, head_dim)
+    if k_cache.shape[2:] != (1, row):
+        raise ValueError(f"k_cache must be [num_blocks, block_size, 1, {row}], got {tuple(k_cache.shape)}")
+    _need_shape(v_cache, "v_cache", torch.uint8, k_cache.shape, dev)
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def spec_q4_attention(q, k_cache, v_cache, block_table, ctx_lens, kv_heads: int, out, window: int = 0, sinks: int = 0,
+                      workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """spec_window_attention over 4-bit caches [num_blocks, block_size, 1, row bytes] (see spec_verify.h); q and out have
+    the 16-bit type that the caches were stored with."""
+    dev = torch.cuda.current_device()
+    _need_queries(q, block_table, dev)
+    B, _, Hq, D = q.shape
+    kv_heads = int(kv_heads)
+    pages, page = _need_q4_caches(k_cache, v_cache, kv_heads, D, dev)
+    return _paged_attention("spec_q4_attention", q, block_table, ctx_lens, out,
+                            _AttnDesc(B, Hq, kv_heads, D, page, block_table.shape[1], pages), window, sinks, workspace,
+                            k_cache, v_cache, dev_err, stream, dev)
+
+
+def _token_stride(t, name: str) -> int:
+    """Elements from one token to the next of a tensor [B, R, H, D] whose tokens are evenly spaced and dense inside."""
+    B, R, H, D = t.shape
+    s = t.stride()
+    step = s[1] if R > 1 else s[0] if B > 1 else H * D
+    if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (B > 1 and R > 1 and s[0] != R * step):
+        raise ValueError(f"{name} must have dense heads and evenly spaced tokens, got strides {s}")
+    return step
+
+
+def spec_cache_store_q4(k, v, block_table, ctx_lens, k_cache, v_cache, dev_err: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None):
+    """Write the newest R tokens of every sequence, k and v [B, R, Hkv, D] bf16 or fp16, into 4-bit caches (see
+    spec_verify.h). k and v may be slices of wider rows."""
+    lib = load_library()
+    dev = torch.cuda.current_device()
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float16) or t.dim() != 4:
+            raise ValueError(f"{name} must be a bfloat16 or float16 tensor [B, R, Hkv, D]")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v differ in shape or type")
+    B, R, H, D = k.shape
+    k_stride, v_stride = _token_stride(k, "k"), _token_stride(v, "v")
+    _need_dims(block_table, "block_table", torch.int32, 2, dev)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    _need_shape(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    pages, page = _need_q4_caches(k_cache, v_cache, H, D, dev)
+    d = _AttnDesc(B, H, H, D, page, block_table.shape[1], pages)
+    rc = lib.spec_cache_store_q4(k.data_ptr(), v.data_ptr(), k_stride, v_stride, block_table.data_ptr(),
+                                 ctx_lens.data_ptr(), R, k_cache.data_ptr(), v_cache.data_ptr(), _DTYPE_CODES[k.dtype],
+                                 ctypes.byref(d), _err_ptr(dev_err), _stream_of(stream, dev))
+    _check("spec_cache_store_q4", rc)
+    return k_cache, v_cache
+
+
+def spec_cache_load_q4(k_cache, v_cache, block_table, ctx_lens, k_out, v_out, dtype: Optional[torch.dtype] = None,
+                       dev_err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Read the newest R tokens of every sequence from 4-bit caches into k_out and v_out [B, R, Hkv, D] (see
+    spec_verify.h). `dtype` is the 16-bit type the caches were stored with, that of k_out without it; k_out and v_out are
+    of that type or fp32."""
+    lib = load_library()
+    dev = torch.cuda.current_device()
+    if not isinstance(k_out, torch.Tensor) or k_out.dim() != 4:
+        raise ValueError("k_out must be a tensor [B, R, Hkv, D]")
+    dtype = k_out.dtype if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype, or the type of k_out without it, must be bfloat16 or float16")
+    if k_out.dtype not in (dtype, torch.float32):
+        raise ValueError(f"k_out must be a float32 or {dtype} tensor")
+    _need_dims(k_out, "k_out", k_out.dtype, 4, dev)
+    _need_shape(v_out, "v_out", k_out.dtype, k_out.shape, dev)
+    B, R, H, D = k_out.shape
+    _need_dims(block_table, "block_table", torch.int32, 2, dev)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    _need_shape(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    pages, page = _need_q4_caches(k_cache, v_cache, H, D, dev)
+    d = _AttnDesc(B, H, H, D, page, block_table.shape[1], pages)
+    rc = lib.spec_cache_load_q4(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), ctx_lens.data_ptr(), R,
+                                k_out.data_ptr(), v_out.data_ptr(), _DTYPE_CODES[dtype], _DTYPE_CODES[k_out.dtype],
+                                ctypes.byref(d), _err_ptr(dev_err), _stream_of(stream, dev))
+    _check("spec_cache_load_q4", rc)
+    return k_out, v_out

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
 SOURCES = ["attention.cu", "accept.cu", "commit.cu", "gdn.cu", "tree_attention.cu", "tree_attention_d64.cu",
-           "tree_attention_d128.cu", "tree_attention_d256.cu", "tree_accept.cu", "cache_pages.cu"]
+           "tree_attention_d128.cu", "tree_attention_d256.cu", "tree_accept.cu", "cache_pages.cu", "cache_q4.cu",
+           "window_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
