@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libspecverify.so")
 SOURCES = ["attention.cu", "accept.cu", "commit.cu", "gdn.cu", "tree_attention.cu", "tree_attention_d64.cu",
            "tree_attention_d128.cu", "tree_attention_d256.cu", "tree_accept.cu", "cache_pages.cu", "cache_q4.cu",
-           "window_attention.cu"]
+           "window_attention.cu", "window_attention_d64.cu", "window_attention_d128.cu", "window_attention_d256.cu",
+           "q4_attention_d64.cu", "q4_attention_d128.cu", "q4_attention_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,17 @@
+// Instances of the attention over a 4-bit cache for head dim 64.
+#include "window_attention_launch.h"
+
+namespace specv {
+namespace wattn {
+
+template <>
+int settings_q4<64>(int packed, int batch, Launch* l) {
+  return with_rows<64, true, true>(packed, [&](auto c) { return settings_of<decltype(c)>(batch, l); });
+}
+template <>
+int launch_q4<64>(int packed, const Launch& l, const Call& call) {
+  return with_rows<64, true, true>(packed, [&](auto c) { return launch_of<decltype(c)>(l, call); });
+}
+
+}  // namespace wattn
+}  // namespace specv

@@ -10,118 +10,11 @@
 // each with a running maximum and sum, and are joined at the end.
 #include <math.h>
 
-#include <type_traits>
-
-#include "attention_device.cuh"
-#include "launch_memo.h"
-#include "q4_device.cuh"
+#include "tensor_map.h"
+#include "window_attention_launch.h"
 
 namespace specv {
 namespace wattn {
-
-constexpr int kMaxBatch = 4096;
-constexpr int kMaxRows = 64;  // packed query rows of a unit
-
-struct Params {
-  const uint8_t* q;
-  const uint8_t* k;
-  const uint8_t* v;
-  uint8_t* out;
-  const int32_t* block_table;
-  const int32_t* ctx_lens;
-  int32_t* dev_err;
-  int64_t num_blocks, row;
-  int rows, heads, kv_heads, gqa, page_shift, max_blocks, window, sinks;
-  float scale_log2;
-};
-
-template <int D, bool FP16, bool Q4>
-__global__ void __launch_bounds__(128) window_attention_kernel(const Params p) {
-  constexpr int E = D / 32;  // elements of a lane
-  __shared__ float s_m[4], s_l[4], s_o[4][D];
-  __shared__ int s_bad;
-  const int h = blockIdx.x % p.heads, i = blockIdx.x / p.heads, b = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = h / p.gqa;
-  const int64_t at = (((int64_t)b * p.rows + i) * p.heads + h) * D + lane * E;
-  const int ctx = p.ctx_lens[b];
-  uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at;
-  if (ctx < p.rows || (int64_t)ctx > ((int64_t)p.max_blocks << p.page_shift)) {
-    if (warp == 0)
-      for (int e = 0; e < E; ++e) out[e] = 0;
-    if (ctx != 0 && threadIdx.x == 0) raise_error(p.dev_err, SPEC_DEVERR_CTX_LEN);
-    return;
-  }
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  const int pos = ctx - p.rows + i, bs = 1 << p.page_shift;
-  const int low = p.window ? max(0, pos - p.window + 1) : 0;
-  // pages are checked for the whole sequence: all its rows are zeros if one of them is bad
-  const int first = p.window ? max(0, ctx - p.rows - p.window + 1) : 0;
-  for (int t = threadIdx.x << p.page_shift; t < ctx; t += 128 << p.page_shift) {
-    if (t + bs <= first && t >= p.sinks) continue;
-    const int page = p.block_table[(int64_t)b * p.max_blocks + (t >> p.page_shift)];
-    if (page < 0 || page >= p.num_blocks) s_bad = 1;
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (warp == 0)
-      for (int e = 0; e < E; ++e) out[e] = 0;
-    if (threadIdx.x == 0) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
-    return;
-  }
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  auto value = [](uint16_t w) { return q4::unpack2<FP16>(w).x; };
-  for (int e = 0; e < E; ++e) {
-    q[e] = value(reinterpret_cast<const uint16_t*>(p.q)[at + e]) * p.scale_log2;
-    o[e] = 0.f;
-  }
-  auto token = [&](const uint8_t* cache, int64_t slot, float (&x)[E]) {
-    if constexpr (Q4) {
-      const uint8_t* row = cache + slot * p.row;
-      const float2 sm = q4::unpack2<FP16>(reinterpret_cast<const uint32_t*>(row + p.kv_heads * (D / 2))[g]);
-      for (int e = 0; e < E; ++e) {
-        const int d = g * D + lane * E + e;
-        x[e] = fmaf((float)((row[d / 2] >> (4 * (d & 1))) & 15), sm.x, sm.y);
-      }
-    } else {
-      const uint16_t* row = reinterpret_cast<const uint16_t*>(cache) + (slot * p.kv_heads + g) * D + lane * E;
-      for (int e = 0; e < E; ++e) x[e] = value(row[e]);
-    }
-  };
-  const int sinks = min(p.sinks, low), total = sinks + pos + 1 - low;
-  for (int j = warp; j < total; j += 4) {
-    const int t = j < sinks ? j : low + j - sinks;
-    const int64_t slot =
-        ((int64_t)p.block_table[(int64_t)b * p.max_blocks + (t >> p.page_shift)] << p.page_shift) + (t & (bs - 1));
-    float x[E], s = 0.f;
-    token(p.k, slot, x);
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], x[e], s);
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (s == -INFINITY) continue;
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), w = exp2f(s - mn);
-    token(p.v, slot, x);
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e] * a);
-    l = l * a + w;
-    m = mn;
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  if (warp != 0) return;
-  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float sum = 0.f;
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    if (s_m[w] == -INFINITY && s_l[w] == 0.f) continue;
-    const float a = exp2f(s_m[w] - top);
-    sum += s_l[w] * a;
-    for (int e = 0; e < E; ++e) o[e] += s_o[w][lane * E + e] * a;
-  }
-  for (int e = 0; e < E; ++e) out[e] = (uint16_t)q4::pack2<FP16>(o[e] / sum, 0.f);
-}
 
 static bool desc_ok(const spec_attn_desc* d, int rows) {
   if (d == nullptr) return false;
@@ -141,6 +34,19 @@ static bool shape_supported(const spec_attn_desc* d, int rows) {
   return (longest / 128 + 2) * d->batch <= INT32_MAX / ((int64_t)d->num_kv_heads * groups);
 }
 
+// How the query rows of a kv head are cut into units.
+struct Rows {
+  int npt, groups, packed;  // query rows of a unit, units, and its packed rows: 8, 16, 32 or 64 at most
+};
+static Rows rows_for(const spec_attn_desc* d, int rows) {
+  const int G = d->num_q_heads / d->num_kv_heads, per = kMaxRows / G;
+  Rows r;
+  r.groups = (rows + per - 1) / per;
+  r.npt = (rows + r.groups - 1) / r.groups;
+  for (r.packed = 8; r.packed < r.npt * G;) r.packed *= 2;
+  return r;
+}
+
 static int call(bool q4, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                 const int32_t* ctx_lens, int32_t num_rows, int32_t window, int32_t sinks, void* out, int32_t dtype,
                 const spec_attn_desc* d, void* workspace, size_t workspace_bytes, int32_t* dev_err,
@@ -156,41 +62,76 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
     return SPEC_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < spec_window_attention_workspace(d, num_rows)) return SPEC_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return SPEC_ERR_INVALID_ARG;
-  Params p;
+  const Rows rows = rows_for(d, num_rows);
+  const bool fp16 = dtype == SPEC_DTYPE_FP16;
+  const int D = d->head_dim, bs = d->block_size;
+  Launch l;
+  int rc;
+  switch (D) {
+    case 64: rc = q4 ? settings_q4<64>(rows.packed, d->batch, &l) : settings_16<64>(rows.packed, fp16, d->batch, &l); break;
+    case 128: rc = q4 ? settings_q4<128>(rows.packed, d->batch, &l) : settings_16<128>(rows.packed, fp16, d->batch, &l); break;
+    default: rc = q4 ? settings_q4<256>(rows.packed, d->batch, &l) : settings_16<256>(rows.packed, fp16, d->batch, &l); break;
+  }
+  if (rc != SPEC_OK) return rc;
+
+  Call c;
+  Params& p = c.p;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const uint8_t*>(q);
-  p.k = static_cast<const uint8_t*>(k_cache);
-  p.v = static_cast<const uint8_t*>(v_cache);
   p.out = static_cast<uint8_t*>(out);
+  p.row = q4::row_bytes(d->num_kv_heads, D);
+  p.kpar = static_cast<const uint8_t*>(k_cache) + d->num_kv_heads * (D / 2);
+  p.vpar = static_cast<const uint8_t*>(v_cache) + d->num_kv_heads * (D / 2);
   p.block_table = block_table;
   p.ctx_lens = ctx_lens;
+  p.counters = reinterpret_cast<int32_t*>(ws);
+  p.lse = reinterpret_cast<float*>(ws + SPEC_ATTN_COUNTER_BYTES);
+  p.opart = p.lse + kMaxPieces * kMaxRows;
   p.dev_err = dev_err;
   p.num_blocks = d->num_blocks;
-  p.row = q4::row_bytes(d->num_kv_heads, d->head_dim);
+  p.batch = d->batch;
   p.rows = num_rows;
   p.heads = d->num_q_heads;
   p.kv_heads = d->num_kv_heads;
   p.gqa = p.heads / p.kv_heads;
-  for (p.page_shift = 0; (1 << p.page_shift) < d->block_size;) ++p.page_shift;
+  p.npt = rows.npt;
+  p.groups = rows.groups;
+  for (p.page_shift = 0; (1 << p.page_shift) < bs;) ++p.page_shift;
   p.max_blocks = d->max_blocks_per_seq;
-  p.window = window;
-  p.sinks = sinks;
-  p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d->head_dim));
-  const dim3 grid((unsigned)(num_rows * p.heads), (unsigned)d->batch);
-  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  auto go = [&](auto D) {
-    constexpr int kD = decltype(D)::value;
-    const bool fp16 = dtype == SPEC_DTYPE_FP16;
-    if (q4 && fp16) window_attention_kernel<kD, true, true><<<grid, 128, 0, stream>>>(p);
-    else if (q4) window_attention_kernel<kD, false, true><<<grid, 128, 0, stream>>>(p);
-    else if (fp16) window_attention_kernel<kD, true, false><<<grid, 128, 0, stream>>>(p);
-    else window_attention_kernel<kD, false, false><<<grid, 128, 0, stream>>>(p);
+  const int longest = p.max_blocks * bs;  // at most 2^30
+  p.window = window >= longest ? 0 : window;
+  p.sinks = sinks > longest ? longest : sinks;
+  p.slots = l.slots;
+  p.fp16 = fp16;
+  p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+  c.stream = reinterpret_cast<cudaStream_t>(stream_);
+
+  EncodeTiledFn encode = encode_fn();
+  if (encode == nullptr) return SPEC_ERR_LAUNCH;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  auto map = [&](CUtensorMap* m, const void* base) {
+    if (q4) {  // one head's codes of a page's tokens; rows as wide as the swizzle
+      const cuuint64_t dims[2] = {(cuuint64_t)p.row, (cuuint64_t)d->num_blocks * bs}, strides[1] = {(cuuint64_t)p.row};
+      const cuuint32_t box[2] = {(cuuint32_t)D / 2, (cuuint32_t)bs};
+      const CUtensorMapSwizzle swizzle =
+          D == 64 ? CU_TENSOR_MAP_SWIZZLE_32B : D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+      return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, ones,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.kv_heads, (cuuint64_t)d->num_blocks * bs};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.kv_heads * D * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)bs};
+    return encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                  dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  switch (d->head_dim) {
-    case 64: go(std::integral_constant<int, 64>{}); break;
-    case 128: go(std::integral_constant<int, 128>{}); break;
-    default: go(std::integral_constant<int, 256>{}); break;
+  if (!map(&c.tk, k_cache) || !map(&c.tv, v_cache)) return SPEC_ERR_LAUNCH;
+  switch (D) {
+    case 64: return q4 ? launch_q4<64>(rows.packed, l, c) : launch_16<64>(rows.packed, fp16, l, c);
+    case 128: return q4 ? launch_q4<128>(rows.packed, l, c) : launch_16<128>(rows.packed, fp16, l, c);
+    default: return q4 ? launch_q4<256>(rows.packed, l, c) : launch_16<256>(rows.packed, fp16, l, c);
   }
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 }  // namespace wattn
@@ -200,7 +141,8 @@ using namespace specv;
 
 extern "C" size_t spec_window_attention_workspace(const spec_attn_desc* d, int32_t num_rows) {
   if (!wattn::desc_ok(d, num_rows) || !wattn::shape_supported(d, num_rows)) return 0;
-  return SPEC_ATTN_COUNTER_BYTES;
+  const int packed = wattn::rows_for(d, num_rows).packed, n = packed < 16 ? 16 : packed;
+  return SPEC_ATTN_COUNTER_BYTES + (size_t)wattn::kMaxPieces * (wattn::kMaxRows + (size_t)n * d->head_dim) * 4;
 }
 
 extern "C" int spec_window_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
