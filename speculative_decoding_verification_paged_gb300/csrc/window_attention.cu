@@ -94,6 +94,7 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   p.heads = d->num_q_heads;
   p.kv_heads = d->num_kv_heads;
   p.gqa = p.heads / p.kv_heads;
+  p.by_gqa = (65535 + p.gqa) / p.gqa;
   p.npt = rows.npt;
   p.groups = rows.groups;
   for (p.page_shift = 0; (1 << p.page_shift) < bs;) ++p.page_shift;

@@ -25,6 +25,7 @@ constexpr int kMaxPieces = 768;    // pieces of cut units in a call
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
 constexpr int kParamSlots = 4;     // tiles of s and m in shared memory
 constexpr int kCandidates = 32;
+constexpr int kMaxTries = 1 << 24;
 constexpr int kBarEpi = 1, kBarGroup0 = 2;  // named barriers: the epilogue's warps, each softmax warpgroup
 constexpr float kUnseen = -3e38f;  // reference of a row that has seen no key
 static_assert(kMaxPieces / 2 * 4 <= SPEC_ATTN_COUNTER_BYTES, "a counter for every cut unit");
@@ -42,6 +43,7 @@ struct Params {
   int32_t* dev_err;
   int64_t num_blocks, row;  // pages; bytes of a 4-bit token row
   int batch, rows, heads, kv_heads, gqa;
+  int by_gqa;       // 2^16 / gqa, rounded up: r / gqa = r * by_gqa >> 16 for r < 64
   int npt, groups;  // query rows of a unit (its npt * gqa packed rows), units per kv head
   int page_shift, max_blocks, window, sinks;
   int slots;  // depth of the ring
@@ -102,7 +104,8 @@ struct Smem {
   static constexpr int STAT_BYTES = 2048 + 256;
   static constexpr int QC = STAT + 2 * STAT_BYTES;                // [QB][2][64] factors of the scores
   static constexpr int PAR = QC + C::QB * 512;                    // [kParamSlots][2][128] s and m of K and V
-  static constexpr int MISC = PAR + (C::Q4 ? kParamSlots * 1024 : 0);  // [64] plan, tensor-memory base, flags
+  static constexpr int EPI = PAR + (C::Q4 ? kParamSlots * 1024 : 0);   // [64] int64 and twice [64] floats of the epilogue
+  static constexpr int MISC = EPI + 1024;  // [64] plan, tensor-memory base, flags
   static constexpr int PREFIX = MISC + 256;
 };
 template <class C>
@@ -216,7 +219,7 @@ struct Task {
 };
 // Tasks are numbered by sequence, piece, kv head and group, so that the blocks of a wave read the same tokens for all
 // heads at about the same time: a line of a 4-bit token row holds several heads.
-__device__ __forceinline__ Task task_at(const Params& p, const int32_t* prefix, const uint16_t* cut, int t) {
+static __device__ __noinline__ Task task_at(const Params& p, const int32_t* prefix, const uint16_t* cut, int t) {
   int lo = 0, hi = p.batch;  // the last b with prefix[b] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -253,8 +256,10 @@ __device__ __forceinline__ void make_plan(const Params& p, int32_t* prefix, uint
   __syncthreads();
   {
     int sum = 0, most = 0;
+#pragma unroll 1
     for (int b = tid; b < B; b += C::kThreads) {
       const int t = tiles_of(p, p.ctx_lens[b]);
+      prefix[b] = t;  // until the prefix sums are made
       sum += t;
       most = max(most, t);
     }
@@ -270,11 +275,13 @@ __device__ __forceinline__ void make_plan(const Params& p, int32_t* prefix, uint
   const float share = (float)misc[0] * (float)units / (float)grid;
   auto length = [&](int c) { return c == 0 ? longest : max(1, min(longest, (int)ceilf(share * (float)c * (1.f / 16.f)))); };
   if (longest > 0) {
+#pragma unroll 1
     for (int c = warp; c < kCandidates; c += C::kWarps) {
       const int len = length(c);
       int tasks = 0, pieces = 0, top = 0, parts = 1;
+#pragma unroll 1
       for (int b = lane; b < B; b += 32) {
-        const int t = tiles_of(p, p.ctx_lens[b]);
+        const int t = prefix[b];
         if (t == 0) continue;
         const int k = (t + len - 1) / len;
         tasks += k;
@@ -295,13 +302,15 @@ __device__ __forceinline__ void make_plan(const Params& p, int32_t* prefix, uint
   __syncthreads();
   if (warp == 0) {
     int best = 0;
+#pragma unroll 1
     for (int c = 1; c < kCandidates && longest > 0; ++c)
       if (cost[c] < cost[best]) best = c;
     const int len = max(1, length(best));
     int tasks = 0, pieces = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int b = b0 + lane;
-      const int t = b < B ? tiles_of(p, p.ctx_lens[b]) : 0;
+      const int t = b < B ? prefix[b] : 0;
       const int k = (t + len - 1) / len, kc = k > 1 ? k : 0;
       int a = k * units, c = kc * units;  // scans
 #pragma unroll
@@ -367,6 +376,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
 
   make_plan<C>(p, prefix, cut, misc);
   // sequences without a task: zeros
+#pragma unroll 1
   for (int b = me; b < p.batch; b += grid) {
     if (prefix[b + 1] != prefix[b]) continue;
     if (tid == 0 && p.ctx_lens[b] != 0) raise_error(p.dev_err, SPEC_DEVERR_CTX_LEN);
@@ -415,6 +425,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     *s_abort = 0;
   }
   // what no one writes and the tensor core reads: weights of rows behind the last one (their sums are not used)
+#pragma unroll 1
   for (int i = tid; i < C::NP * C::BANDS * C::P_BYTES / 16; i += C::kThreads)
     reinterpret_cast<uint4*>(fixed + S::P)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
@@ -425,10 +436,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   const uint32_t ring_u32 = smem_u32(ring), q_u32 = smem_u32(fixed + S::Q), p_u32 = smem_u32(fixed + S::P);
 
   auto wait = [&](uint64_t* bar, int n) {  // until the bar's phase n is complete (n < 0: at once)
-    if (n < 0 || mbar_try_wait(bar, (uint32_t)(n & 1))) return;
-    const long long start = clock64();
-    while (!mbar_try_wait(bar, (uint32_t)(n & 1)) && !*s_abort) {
-      if (clock64() - start > 2000000000LL) {
+    if (n < 0) return;
+    for (int tries = 0; !mbar_try_wait(bar, (uint32_t)(n & 1)); ++tries) {
+      if (*s_abort) break;
+      if (tries == kMaxTries) {  // a second or more
         *s_abort = 1;
         raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
       }
@@ -456,6 +467,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           if (bad) ids = -1;
           if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad[seq & 31] = 1;
         }
+#pragma unroll 1
         for (int w = 0; w < 2; ++w, ++at) {
           const int s = at % NS;
           wait(&empty[s], at / NS - 1);
@@ -464,6 +476,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           __syncwarp();
           const CUtensorMap* map = w == 0 ? &tm_k : &tm_v;
           const uint32_t dst = ring_u32 + s * C::SLOT;
+#pragma unroll 1
           for (int pc = 0; pc < ppt; ++pc) {
             const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
             const int row = id < 0 ? -bs : id << p.page_shift;  // outside of the cache: zeros
@@ -501,10 +514,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       if constexpr (C::Q4) {
         wait(&kd_full[qi % C::KB], qi / C::KB);
         tc_fence_after();
+#pragma unroll 1
+        for (int sl = 0; sl < D / 64; ++sl) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_ts(dst, tmem + C::COL_K + (qi % C::KB) * (D / 2) + ks * 8, kq_lo + qb + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4),
-                  kq_hi, id_qk, ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts(dst, tmem + C::COL_K + (qi % C::KB) * (D / 2) + sl * 32 + ks * 8, kq_lo + qb + ((sl * N * 128 + ks * 32) >> 4),
+                    kq_hi, id_qk, sl + ks > 0 ? 1u : 0u);
+        }
         umma_commit_elect(&s_full[qi & 1]);
         umma_commit_elect(&kd_free[qi % C::KB]);
       } else {
@@ -512,10 +528,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         wait(&full[s], n / NS);
         tc_fence_after();
         const uint32_t kb = (ring_u32 + s * C::SLOT) >> 4;
+#pragma unroll 1
+        for (int sl = 0; sl < D / 64; ++sl) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(dst, kq_lo + kb + (((ks >> 2) * TK * 128 + (ks & 3) * 32) >> 4), kq_hi,
-                 kq_lo + qb + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(dst, kq_lo + kb + ((sl * TK * 128 + ks * 32) >> 4), kq_hi, kq_lo + qb + ((sl * N * 128 + ks * 32) >> 4),
+                   kq_hi, id_qk, sl + ks > 0 ? 1u : 0u);
+        }
         umma_commit_elect(&s_full[qi & 1]);
         umma_commit_elect(&empty[s]);
       }
@@ -526,14 +545,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if (qt < tasks) q_left = task_at(p, prefix, cut, qt).tiles;
       }
     };
-    scores();
-    int i = 0, seq = 0;
-    for (int t = me; t < tasks; t += grid, ++seq) {
-      const int tiles = task_at(p, prefix, cut, t).tiles;
-      const uint32_t o = tmem + C::COL_O + (seq % C::OB) * C::O_COLS;
-      for (int j = 0; j < tiles; ++j, ++i) {
-        if (__any_sync(0xffffffffu, *s_abort)) break;
-        if (qt < tasks) scores();
+    int t = me, seq = 0, tiles = q_left, j = -1;  // tile j of task t is next for the second product; -1: scores first
+    for (int i = -1; t < tasks; ++i) {
+      if (__any_sync(0xffffffffu, *s_abort)) break;
+      if (qt < tasks) scores();
+      if (j >= 0) {
+        const uint32_t o = tmem + C::COL_O + (seq % C::OB) * C::O_COLS;
         if (j == 0) wait(&o_free[seq % C::OB], seq / C::OB - 1);
         wait(&p_full[i & 1], i >> 1);
         const uint32_t pb = (p_u32 + (i % C::NP) * C::BANDS * C::P_BYTES) >> 4;
@@ -542,18 +559,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         else wait(&full[s], n / NS);
         tc_fence_after();
         const uint32_t vb = (ring_u32 + s * C::SLOT) >> 4;
+#pragma unroll 1
+        for (int part = 0; part < C::BANDS * C::HALVES; ++part) {
+          const int band = part / C::HALVES, hh = part % C::HALVES;
+#pragma unroll 1
+          for (int k4 = 0; k4 < TK / 64; ++k4) {
 #pragma unroll
-        for (int band = 0; band < C::BANDS; ++band) {
-#pragma unroll
-          for (int hh = 0; hh < C::HALVES; ++hh) {
-            const uint32_t dst = o + (band * C::HALVES + hh) * N;
-#pragma unroll
-            for (int kk = 0; kk < TK / 16; ++kk) {
-              const uint32_t b = w_lo + pb + ((band * C::P_BYTES + kk * 32 * N) >> 4), acc = j > 0 || kk > 0 ? 1u : 0u;
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t b = w_lo + pb + ((band * C::P_BYTES + (k4 * 4 + kk) * 32 * N) >> 4);
+              const uint32_t acc = j > 0 || k4 + kk > 0 ? 1u : 0u;
               if constexpr (C::Q4)
-                umma_ts(dst, tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + kk * 8, b, w_hi, id_pv, acc);
+                umma_ts(o + part * N, tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + k4 * 32 + kk * 8, b, w_hi,
+                        id_pv, acc);
               else
-                mma_ss(dst, v_lo + vb + ((hh * 2 * TK * 128 + kk * 2048) >> 4), v_hi, b, w_hi, id_pv, acc);
+                mma_ss(o + part * N, v_lo + vb + ((hh * 2 * TK * 128 + (k4 * 4 + kk) * 2048) >> 4), v_hi, b, w_hi, id_pv, acc);
             }
           }
         }
@@ -561,6 +580,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if constexpr (C::Q4) umma_commit_elect(&vd_free[i % C::KB]);
         else umma_commit_elect(&empty[s]);
         if (j == tiles - 1) umma_commit_elect(&o_full[seq % C::OB]);
+      }
+      if (++j == tiles) {
+        j = 0;
+        ++seq;
+        t += grid;
+        if (t < tasks) tiles = task_at(p, prefix, cut, t).tiles;
       }
     }
   } else if (warp == 2) {
@@ -581,7 +606,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           const int s = i % kParamSlots;
           wait(&par_free[s], i / kParamSlots - 1);
           const uint32_t dst = smem_u32(fixed + S::PAR + s * 1024);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < TK / 32; ++c) {
             const int key = c * 32 + lane;
             const int id = __shfl_sync(0xffffffffu, ids, l0 - win + (key >> p.page_shift));
@@ -601,6 +626,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     // =================== epilogue: queries in, results out ===================
     const int et = tid - 32 * C::W_EPI, q4 = warp & 3;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    // packed row r's place among the rows of its sequence
+    auto row_of = [&](const Task& k, int r) {
+      const int i = (r * p.by_gqa) >> 16;
+      return (int64_t)(k.i0 + i) * p.heads + k.g * p.gqa + (r - i * p.gqa);
+    };
     // Query rows of task number seq into its buffer. The buffer's last readers are done: the task QB before has been
     // written out.
     auto load_queries = [&](int t, int seq) {
@@ -609,11 +639,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       constexpr int L = D / 8;  // threads of a row, 8 elements each
       const int c = et % L;
       float* qc = reinterpret_cast<float*>(fixed + S::QC) + (seq % C::QB) * 128;
+#pragma unroll 1
       for (int r = et / L; r < N; r += 128 / L) {
         uint4 x = make_uint4(0, 0, 0, 0);
         if (r < k.nr) {
-          const int i = k.i0 + r / p.gqa, h = k.g * p.gqa + r % p.gqa;
-          x = __ldg(reinterpret_cast<const uint4*>(p.q) + (((int64_t)k.b * p.rows + i) * p.heads + h) * L + c);
+          x = __ldg(reinterpret_cast<const uint4*>(p.q) + ((int64_t)k.b * p.rows * p.heads + row_of(k, r)) * L + c);
         }
         if constexpr (C::Q4) {
           // fp16 times a power of two that brings the row's largest element to [2^14, 2^15); the codes come in the order
@@ -636,8 +666,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
           }
-          int e2 = 0;
-          if (top > 0.f) e2 = max(-100, min(140, 14 - (top < INFINITY ? ilogbf(top) : 127)));
+          const int e2 = max(-100, min(140, 14 + 127 - (__float_as_int(top) >> 23)));
           const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = f[e] * f1 * f2;
@@ -654,65 +683,83 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[seq % C::QB]);
     };
-    for (int s = 0; s < C::QB; ++s)
-      if (me + s * grid < tasks) load_queries(me + s * grid, s);
-    // head dim of this thread's lane
+    // head dim of this thread's lane, and the lane that holds its neighbour
     const int d0 = C::Q4 ? q4 * 32 + 4 * (lane & 7) + (lane >> 3) : q4 * 32 + lane;
-    const float unit = C::Q4 ? ((lane >> 3) & 1 ? 0x1p20f : 0x1p24f) : 1.f;
-    int seq = 0;
-    for (int t = me; t < tasks; t += grid, ++seq) {
+    constexpr int NEXT = C::Q4 ? 8 : 1;
+    const bool odd = lane & NEXT;
+    const float unit = C::Q4 ? (odd ? 0x1p20f : 0x1p24f) : 1.f;
+    int64_t* e_row = reinterpret_cast<int64_t*>(fixed + S::EPI);        // [64] a row's place in the sequence's output
+    float* e_inv = reinterpret_cast<float*>(fixed + S::EPI + 512);      // [64] 1 / its sum
+    float* e_off = e_inv + 64;                                          // [64] what is added to the product
+    int seq = -C::QB;  // the first queries are loaded before the first result
+    for (int t = me - C::QB * grid; t < tasks; t += grid, ++seq) {
+     if (seq >= 0) {
       const Task k = task_at(p, prefix, cut, t);
       const int ob = seq % C::OB;
       wait(&st_full[ob], seq / C::OB);
       wait(&o_full[ob], seq / C::OB);
       tc_fence_after();
-      const float* stat = reinterpret_cast<const float*>(fixed + S::STAT + ob * S::STAT_BYTES);
       const bool bad = s_bad[seq & 31] != 0;
       if (bad && et == 0) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
+      named_sync(kBarEpi, 128);  // the last task's entries have been read
+      if (et < k.nr) {
+        const float* stat = reinterpret_cast<const float*>(fixed + S::STAT + ob * S::STAT_BYTES) + et;
+        const float sum = (stat[0] + stat[64]) + (stat[128] + stat[192]);
+        e_row[et] = row_of(k, et) * D;
+        e_inv[et] = bad ? 0.f : 1.f / sum;
+        if constexpr (C::Q4) e_off[et] = (stat[256] + stat[320]) + (stat[384] + stat[448]);
+        // a piece without a visible key has weight 0
+        if (k.pieces > 1)
+          __stcg(p.lse + (int64_t)k.slot * kMaxRows + et, bad ? INFINITY : sum == 0.f ? -INFINITY : stat[512] + log2f(sum));
+      }
+      named_sync(kBarEpi, 128);
       const uint32_t o = tmem + C::COL_O + ob * C::O_COLS + lane_off;
       float* part = p.opart + (int64_t)k.slot * N * D;
-      constexpr int CH = C::ROWS < 16 ? 8 : 16;
-      for (int c = 0; c < k.nr; c += CH) {
-#pragma unroll
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + (int64_t)k.b * p.rows * p.heads * D;
+#pragma unroll 1
+      for (int c = 0; c < k.nr; c += 8) {
+#pragma unroll 1
         for (int hh = 0; hh < C::HALVES; ++hh) {
-          float v[CH];
-          tmem_load_cols<CH>(o + hh * N + c, v);
+          float v[8];
+          tmem_load_cols<8>(o + hh * N + c, v);
           if constexpr (C::BANDS == 2) {
-            float low[CH];
-            tmem_load_cols<CH>(o + (C::HALVES + hh) * N + c, low);
+            float low[8];
+            tmem_load_cols<8>(o + (C::HALVES + hh) * N + c, low);
 #pragma unroll
-            for (int e = 0; e < CH; ++e) v[e] = fmaf(low[e], 0x1p-18f, v[e]);
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(low[e], 0x1p-18f, v[e]);
           }
+          if (D == 64 && q4 >= 2) continue;
           const int d = hh * 128 + d0;
 #pragma unroll
-          for (int e = 0; e < CH; ++e) {
-            const int r = c + e;
-            if (r >= k.nr) break;
-            const float sum = (stat[r] + stat[64 + r]) + (stat[128 + r] + stat[192 + r]);
-            float x = v[e];
-            if constexpr (C::Q4) x = fmaf(x, unit, (stat[256 + r] + stat[320 + r]) + (stat[384 + r] + stat[448 + r]));
-            x = bad ? 0.f : x / sum;
-            if (D == 64 && q4 >= 2) continue;
-            if (k.pieces == 1) {
-              const int i = k.i0 + r / p.gqa, h = k.g * p.gqa + r % p.gqa;
-              uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + (((int64_t)k.b * p.rows + i) * p.heads + h) * D + d;
-              *out = (uint16_t)(p.fp16 ? q4::pack2<true>(x, 0.f) : q4::pack2<false>(x, 0.f));
-            } else {
-              __stcg(part + r * D + d, x);
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (C::Q4) v[e] = fmaf(v[e], unit, e_off[c + e]);
+            v[e] *= e_inv[c + e];
+          }
+          if (k.pieces == 1) {
+            // pairs of head dims: one thread writes those of the even row, its neighbour those of the odd row
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[e + 1], NEXT);
+              const float lo = odd ? got : v[e], hi = odd ? v[e + 1] : got;
+              const int r = c + e + (odd ? 1 : 0);
+              if (r < k.nr)
+                *reinterpret_cast<uint32_t*>(out + e_row[r] + (d & ~1)) = p.fp16 ? q4::pack2<true>(bad ? 0.f : lo, bad ? 0.f : hi)
+                                                                               : q4::pack2<false>(bad ? 0.f : lo, bad ? 0.f : hi);
             }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + e < k.nr) __stcg(part + (c + e) * D + d, v[e]);
           }
         }
-      }
-      if (k.pieces > 1 && et < k.nr) {
-        const int r = et;
-        const float sum = (stat[r] + stat[64 + r]) + (stat[128 + r] + stat[192 + r]);
-        // a piece without a visible key has weight 0
-        __stcg(p.lse + (int64_t)k.slot * kMaxRows + r, bad ? INFINITY : sum == 0.f ? -INFINITY : stat[512 + r] + log2f(sum));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[ob]);
-      if (me + (seq + C::QB) * grid < tasks) load_queries(me + (seq + C::QB) * grid, seq + C::QB);
+     }
+      if (t + C::QB * grid < tasks) load_queries(t + C::QB * grid, seq + C::QB);
+      if (seq < 0) continue;
+      const Task k = task_at(p, prefix, cut, t);
       if (k.pieces == 1) continue;
       // ---- a cut unit is joined by whoever finishes its last piece
       named_sync(kBarEpi, 128);
@@ -730,12 +777,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       const bool last = *s_last != 0;
       named_sync(kBarEpi, 128);  // s_last is written again
       if (!last) continue;
+#pragma unroll 1
       for (int item = et; item < k.nr * (D / 4); item += 128) {
         const int r = item / (D / 4), c = item - r * (D / 4);
         const float* lse = p.lse + (int64_t)k.first * kMaxRows + r;
         const float4* src = reinterpret_cast<const float4*>(p.opart) + (int64_t)k.first * (N * D / 4) + item;
         float top = -INFINITY;
         bool none = false;
+#pragma unroll 4
         for (int w = 0; w < k.pieces; ++w) {
           const float x = __ldcg(lse + (int64_t)w * kMaxRows);
           none |= x == INFINITY;
@@ -755,11 +804,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           a.w = fmaf(f, y.w, a.w);
         }
         const float inv = 1.f / sum;
-        const int i = k.i0 + r / p.gqa, h = k.g * p.gqa + r % p.gqa;
         uint2 out = p.fp16 ? make_uint2(q4::pack2<true>(a.x * inv, a.y * inv), q4::pack2<true>(a.z * inv, a.w * inv))
                            : make_uint2(q4::pack2<false>(a.x * inv, a.y * inv), q4::pack2<false>(a.z * inv, a.w * inv));
         if (none) out = make_uint2(0, 0);
-        reinterpret_cast<uint2*>(p.out)[(((int64_t)k.b * p.rows + i) * p.heads + h) * (D / 4) + c] = out;
+        reinterpret_cast<uint2*>(p.out)[((int64_t)k.b * p.rows * p.heads + row_of(k, r)) * (D / 4) + c] = out;
       }
     }
   } else if (warp < C::W_K) {
@@ -815,9 +863,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         for (int e = 0; e < CW; ++e) {
           if constexpr (C::Q4) x[e] = fmaf(ks, x[e] * qc[e], km * qc[64 + e]);
           else x[e] *= p.scale_log2;
-          if (masked && (c0 + e < r_lo || c0 + e >= r_hi)) x[e] = -INFINITY;
-          top = fmaxf(top, x[e] - s_ref[c0 + e]);
         }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < CW; ++e)
+            if (c0 + e < r_lo || c0 + e >= r_hi) x[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < CW; ++e) top = fmaxf(top, x[e] - s_ref[c0 + e]);
         grow |= top + lvs > C::LIMIT;
         if (named_sync_or(bar_group, 128, grow)) {
           // ---- new references: 2^SHIFT below the tile's largest weight (4-bit: weight times s) of each row, if that is
@@ -875,27 +928,36 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           }
         }
         // ---- weights
+#pragma unroll
+        for (int e = 0; e < CW; ++e) {
+          x[e] = fast_exp2(x[e] - s_ref[c0 + e]);
+          l[e] += x[e];
+        }
+        if constexpr (C::Q4) {
+          if (masked) {  // s and m of a key may be NaN for the rows that see it
+#pragma unroll
+            for (int e = 0; e < CW; ++e) {
+              const bool see = c0 + e >= r_lo && c0 + e < r_hi;
+              off[e] += see ? x[e] * vm : 0.f;
+              x[e] = see ? x[e] * vs : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < CW; ++e) {
+              off[e] = fmaf(x[e], vm, off[e]);
+              x[e] *= vs;
+            }
+          }
+        }
         uint32_t hi[CW / 2], lo[C::BANDS == 2 ? CW / 2 : 1];
 #pragma unroll
         for (int e = 0; e < CW; e += 2) {
-          float w[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float y = fast_exp2(x[e + u] - s_ref[c0 + e + u]);
-            l[e + u] += y;
-            w[u] = y;
-            if constexpr (C::Q4) {
-              const bool see = !masked || (c0 + e + u >= r_lo && c0 + e + u < r_hi);
-              w[u] = see ? y * vs : 0.f;
-              off[e + u] += see ? y * vm : 0.f;
-            }
-          }
           if constexpr (C::BANDS == 2) {
-            const float a = w[0] >= 0.0625f ? w[0] : 0.f, b = w[1] >= 0.0625f ? w[1] : 0.f;
+            const float a = x[e] >= 0.0625f ? x[e] : 0.f, b = x[e + 1] >= 0.0625f ? x[e + 1] : 0.f;
             hi[e / 2] = q4::pack2<true>(a, b);
-            lo[e / 2] = q4::pack2<true>((w[0] - a) * 0x1p18f, (w[1] - b) * 0x1p18f);
+            lo[e / 2] = q4::pack2<true>((x[e] - a) * 0x1p18f, (x[e + 1] - b) * 0x1p18f);
           } else {
-            hi[e / 2] = q4::pack2<C::FP16>(w[0], w[1]);
+            hi[e / 2] = q4::pack2<C::FP16>(x[e], x[e + 1]);
           }
         }
         if (i >= C::NP) wait(&pv_done[i % C::NP], i / C::NP - 1);
@@ -934,6 +996,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       // fourth 16-fold.
       const int q4 = warp & 3, key = q4 * 32 + lane;
       int total = 0;
+#pragma unroll 1
       for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
       for (int i = 0; i < total; ++i) {
         const int n = 2 * i, s = n % NS;
@@ -943,7 +1006,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         const uint8_t* row = ring + s * C::SLOT + key * (D / 2);
         const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
         const uint32_t dst = tmem + C::COL_K + (i % C::KB) * (D / 2) + ((uint32_t)(q4 * 32) << 16);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; c += 2) {
           uint32_t v[32];
 #pragma unroll
@@ -976,6 +1039,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       // taken from 8, so that a weight's rounding meets at most 8 s.
       const int q4 = warp & 3;
       int total = 0;
+#pragma unroll 1
       for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
       if (q4 >= C::V_WARPS) {  // head dim 64: the upper lanes are not used
 #pragma unroll
@@ -993,10 +1057,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         tc_fence_after();
         if (q4 < C::V_WARPS) {
           const uint32_t base = ring_u32 + s * C::SLOT;
-#pragma unroll
+#pragma unroll 1
           for (int hh = 0; hh < C::HALVES; ++hh) {
             const uint32_t dst = tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + ((uint32_t)(q4 * 32) << 16);
-#pragma unroll
+#pragma unroll 2
             for (int blk = 0; blk < TK / 32; ++blk) {
               const int key = blk * 32 + lane, c = hh * 4 + q4;
               const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
