@@ -107,27 +107,20 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   c.stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  EncodeTiledFn encode = encode_fn();
-  if (encode == nullptr) return SPEC_ERR_LAUNCH;
-  const cuuint32_t ones[3] = {1, 1, 1};
-  auto map = [&](CUtensorMap* m, const void* base) {
-    if (q4) {  // one head's codes of a page's tokens; rows as wide as the swizzle
-      const cuuint64_t dims[2] = {(cuuint64_t)p.row, (cuuint64_t)d->num_blocks * bs}, strides[1] = {(cuuint64_t)p.row};
-      const cuuint32_t box[2] = {(cuuint32_t)D / 2, (cuuint32_t)bs};
-      const CUtensorMapSwizzle swizzle =
-          D == 64 ? CU_TENSOR_MAP_SWIZZLE_32B : D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-      return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, ones,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    }
+  if (!q4) {
+    EncodeTiledFn encode = encode_fn();
+    if (encode == nullptr) return SPEC_ERR_LAUNCH;
+    // K and V [token rows][Hkv][D]: a box holds one head's rows of a page, 64 elements wide
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.kv_heads, (cuuint64_t)d->num_blocks * bs};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.kv_heads * D * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)bs};
-    return encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
-                  dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  if (!map(&c.tk, k_cache) || !map(&c.tv, v_cache)) return SPEC_ERR_LAUNCH;
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)bs}, ones[3] = {1, 1, 1};
+    auto map = [&](CUtensorMap* m, const void* base) {
+      return encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                    dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!map(&c.tk, k_cache) || !map(&c.tv, v_cache)) return SPEC_ERR_LAUNCH;
+  }
   switch (D) {
     case 64: return q4 ? launch_q4<64>(rows.packed, l, c) : launch_16<64>(rows.packed, fp16, l, c);
     case 128: return q4 ? launch_q4<128>(rows.packed, l, c) : launch_16<128>(rows.packed, fp16, l, c);

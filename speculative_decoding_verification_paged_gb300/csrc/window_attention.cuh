@@ -23,9 +23,9 @@ constexpr int kMaxBatch = 4096;
 constexpr int kMaxRows = 64;       // packed query rows of a unit
 constexpr int kMaxPieces = 768;    // pieces of cut units in a call
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
-constexpr int kParamSlots = 4;     // tiles of s and m in shared memory
+constexpr int kParamSlots = 8;     // tiles of s and m in shared memory
 constexpr int kCandidates = 32;
-constexpr int kMaxTries = 1 << 24;
+constexpr long long kMaxCycles = 2000000000LL;  // that a wait lasts at most
 constexpr int kBarEpi = 1, kBarGroup0 = 2;  // named barriers: the epilogue's warps, each softmax warpgroup
 constexpr float kUnseen = -3e38f;  // reference of a row that has seen no key
 static_assert(kMaxPieces / 2 * 4 <= SPEC_ATTN_COUNTER_BYTES, "a counter for every cut unit");
@@ -155,14 +155,6 @@ __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-// 2-D tiled copy into shared memory; c0 is a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int c0, int c1, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
 // 4 bytes from global to shared memory, zeros with bytes = 0; the barrier gets one arrival of this thread once all its
 // copies so far are there.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
@@ -170,6 +162,21 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+// mbarrier.try_wait that may sleep for a millisecond: a warp that asks again and again takes issue slots from those that
+// work (20 of 24 warps wait at any time).
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -399,8 +406,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   if (tid == 0) {
     const uint32_t readers = C::Q4 ? 4 : 1;
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
-      // K and V of a tile alternate in the ring, but not always in the same slots: both have as many readers
+      mbar_init(&full[s], C::Q4 ? 32 : 1);
       mbar_init(&empty[s], readers);
     }
     for (int j = 0; j < 2; ++j) {
@@ -437,53 +443,117 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
 
   auto wait = [&](uint64_t* bar, int n) {  // until the bar's phase n is complete (n < 0: at once)
     if (n < 0) return;
-    for (int tries = 0; !mbar_try_wait(bar, (uint32_t)(n & 1)); ++tries) {
+    for (long long start = 0; !try_wait_long(bar, (uint32_t)(n & 1));) {
+      const long long now = clock64();
+      if (start == 0) start = now;
       if (*s_abort) break;
-      if (tries == kMaxTries) {  // a second or more
+      if (now - start > kMaxCycles) {
         *s_abort = 1;
         raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
       }
     }
   };
 
-  if (warp == 0) {
-    // =================== producer: K and V tiles in turns, NS tiles ahead ===================
+  if (C::Q4 ? warp < C::W_EPI && warp != 1 : warp == 0) {
+    // =================== producers ===================
     const int bs = 1 << p.page_shift, ppt = TK >> p.page_shift;
-    const bool once = p.groups == 1;  // read by this block alone
-    const uint64_t policy = l2_evict_first_policy();
-    int at = 0, seq = 0;  // tiles loaded, tasks
-    for (int t = me; t < tasks; t += grid, ++seq) {
-      const Task k = task_at(p, prefix, cut, t);
-      int win = -1, ids = 0;  // 32 entries of the page list, one a lane
-      if (lane == 0) s_bad[seq & 31] = 0;
-      for (int j = 0; j < k.tiles; ++j) {
-        const int l0 = (k.tile0 + j) * ppt;
-        if (win < 0 || l0 >= win + 32) {
-          win = l0;
-          const int l = l0 + lane;
-          const bool there = l < k.span.pages;
-          ids = there ? __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns)) : -1;
-          const bool bad = there && (ids < 0 || (int64_t)ids >= p.num_blocks) && l < (k.tile0 + k.tiles) * ppt;
-          if (bad) ids = -1;
-          if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad[seq & 31] = 1;
+    // 32 entries of the task's page list from entry l0 on, one a lane; -1 for those behind its end and for bad pages
+    auto page_ids = [&](const Task& k, int l0, int seq) {
+      const int l = l0 + lane;
+      int id = -1;
+      bool bad = false;
+      if (l < min(k.span.pages, (k.tile0 + k.tiles) * ppt)) {
+        id = __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns));
+        bad = id < 0 || (int64_t)id >= p.num_blocks;
+        if (bad) id = -1;
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad[seq & 31] = 1;
+      return id;
+    };
+    if constexpr (C::Q4) {
+      // One warp copies K, one V, with 16-byte cp.async: a tensor copy's rate goes by its rows, whose 64 bytes (head dim
+      // 128) are too few. Rows are swizzled so that both ways of reading a tile are free of bank conflicts. A third warp
+      // copies s and m of the keys.
+      constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte chunks of a row, rows a warp copies at once
+      const int w = warp == 0 ? 0 : 1, H = NS / 2, c = lane % CPR, r0 = lane / CPR;
+      const uint32_t row = (uint32_t)p.row;
+      const uint8_t* src = (w == 0 ? p.kpar : p.vpar) - (int64_t)p.kv_heads * (D / 2) + (uint64_t)r0 * row + c * 16;
+      int i = 0, seq = 0;
+      for (int t = me; t < tasks; t += grid, ++seq) {
+        const Task k = task_at(p, prefix, cut, t);
+        int win = -1, ids = 0;
+        if (lane == 0 && warp == 0) s_bad[seq & 31] = 0;
+        __syncwarp();
+        for (int j = 0; j < k.tiles; ++j, ++i) {
+          const int l0 = (k.tile0 + j) * ppt;
+          if (win < 0 || l0 >= win + 32) {
+            win = l0;
+            ids = page_ids(k, l0, seq);
+          }
+          if (warp == 3) {
+            const int s = i % kParamSlots;
+            wait(&par_free[s], i / kParamSlots - 1);
+            if (__any_sync(0xffffffffu, *s_abort)) break;
+            const uint32_t dst = smem_u32(fixed + S::PAR + s * 1024);
+#pragma unroll 2
+            for (int r = lane; r < TK; r += 32) {
+              const int id = __shfl_sync(0xffffffffu, ids, l0 - win + (r >> p.page_shift));
+              const uint32_t slot = ((uint32_t)max(id, 0) << p.page_shift) + (r & (bs - 1));
+              const uint64_t at = (uint64_t)slot * row + 4 * k.g;
+              cp_async_4(dst + r * 4, p.kpar + at, id < 0 ? 0 : 4);
+              cp_async_4(dst + 512 + r * 4, p.vpar + at, id < 0 ? 0 : 4);
+            }
+            cp_async_arrive(&par_full[s]);
+          } else {
+            const int s = (i % H) * 2 + w;
+            wait(&empty[s], i / H - 1);
+            if (__any_sync(0xffffffffu, *s_abort)) break;
+            for (int pc = 0; pc < ppt; ++pc) {
+              const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
+              const uint32_t dst = ring_u32 + s * C::SLOT + ((pc << p.page_shift) + r0) * (D / 2);
+              const uint8_t* from = src + (uint64_t)((uint32_t)max(id, 0) << p.page_shift) * row + k.g * (D / 2);
+#pragma unroll 4
+              for (int r = 0; r < bs; r += RPI) {
+                const int swz = D == 64 ? (r0 >> 2) & 1 : D == 128 ? (r0 >> 1) & 3 : (r0 + r) & 7;
+                cp_async_16(dst + r * (D / 2) + ((c ^ swz) << 4), from, id < 0 ? 0 : 16);
+                from += RPI * row;
+              }
+            }
+            cp_async_arrive(&full[s]);
+          }
         }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+    } else {
+      const bool once = p.groups == 1;  // read by this block alone
+      const uint64_t policy = l2_evict_first_policy();
+      int at = 0, seq = 0;  // tiles loaded (K and V in turns), tasks
+      for (int t = me; t < tasks; t += grid, ++seq) {
+        const Task k = task_at(p, prefix, cut, t);
+        int win = -1, ids = 0;
+        if (lane == 0) s_bad[seq & 31] = 0;
+        __syncwarp();
+        for (int j = 0; j < k.tiles; ++j) {
+          const int l0 = (k.tile0 + j) * ppt;
+          if (win < 0 || l0 >= win + 32) {
+            win = l0;
+            ids = page_ids(k, l0, seq);
+          }
 #pragma unroll 1
-        for (int w = 0; w < 2; ++w, ++at) {
-          const int s = at % NS;
-          wait(&empty[s], at / NS - 1);
-          if (__any_sync(0xffffffffu, *s_abort)) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)C::SLOT);
-          __syncwarp();
-          const CUtensorMap* map = w == 0 ? &tm_k : &tm_v;
-          const uint32_t dst = ring_u32 + s * C::SLOT;
+          for (int w = 0; w < 2; ++w, ++at) {
+            const int s = at % NS;
+            wait(&empty[s], at / NS - 1);
+            if (__any_sync(0xffffffffu, *s_abort)) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)C::SLOT);
+            __syncwarp();
+            const CUtensorMap* map = w == 0 ? &tm_k : &tm_v;
+            const uint32_t dst = ring_u32 + s * C::SLOT;
 #pragma unroll 1
-          for (int pc = 0; pc < ppt; ++pc) {
-            const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
-            const int row = id < 0 ? -bs : id << p.page_shift;  // outside of the cache: zeros
-            if (lane == 0) {
-              if constexpr (C::Q4) {
-                tma_load_2d(dst + pc * bs * (D / 2), map, k.g * (D / 2), row, &full[s]);
-              } else {
+            for (int pc = 0; pc < ppt; ++pc) {
+              const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
+              const int row = id < 0 ? -bs : id << p.page_shift;  // outside of the cache: zeros
+              if (lane == 0) {
 #pragma unroll
                 for (int sub = 0; sub < D / 64; ++sub) {
                   const uint32_t to = dst + sub * TK * 128 + pc * bs * 128;
@@ -492,13 +562,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
                 }
               }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
+      if (*s_abort)  // copies in flight still write here
+        for (int n = max(0, at - NS); n < at; ++n) mbar_wait_bounded(&full[n % NS], (uint32_t)((n / NS) & 1), 20000000LL);
     }
-    if (*s_abort)  // copies in flight still write here
-      for (int n = max(0, at - NS); n < at; ++n) mbar_wait_bounded(&full[n % NS], (uint32_t)((n / NS) & 1), 20000000LL);
   } else if (warp == 1) {
     // =================== MMA: scores of tile i + 1, then the product of tile i ===================
     const uint32_t id_qk = mma_desc<C::FP16>(N, 0, 0), id_pv = mma_desc<C::FP16>(N, C::Q4 ? 0 : 1, 1);
@@ -588,40 +658,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if (t < tasks) tiles = task_at(p, prefix, cut, t).tiles;
       }
     }
-  } else if (warp == 2) {
-    // =================== 4-bit: s and m of every key ===================
-    if constexpr (C::Q4) {
-      const int bs = 1 << p.page_shift, ppt = TK >> p.page_shift;
-      int i = 0;
-      for (int t = me; t < tasks; t += grid) {
-        const Task k = task_at(p, prefix, cut, t);
-        int win = -1, ids = 0;
-        for (int j = 0; j < k.tiles; ++j, ++i) {
-          const int l0 = (k.tile0 + j) * ppt;
-          if (win < 0 || l0 >= win + 32) {
-            win = l0;
-            const int l = l0 + lane;
-            ids = l < k.span.pages ? __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns)) : -1;
-          }
-          const int s = i % kParamSlots;
-          wait(&par_free[s], i / kParamSlots - 1);
-          const uint32_t dst = smem_u32(fixed + S::PAR + s * 1024);
-#pragma unroll 1
-          for (int c = 0; c < TK / 32; ++c) {
-            const int key = c * 32 + lane;
-            const int id = __shfl_sync(0xffffffffu, ids, l0 - win + (key >> p.page_shift));
-            const bool ok = id >= 0 && (int64_t)id < p.num_blocks;
-            const int64_t off = ok ? (((int64_t)id << p.page_shift) + (key & (bs - 1))) * p.row + 4 * k.g : 0;
-            cp_async_4(dst + key * 4, p.kpar + off, ok ? 4 : 0);
-            cp_async_4(dst + 512 + key * 4, p.vpar + off, ok ? 4 : 0);
-          }
-          cp_async_arrive(&par_full[s]);
-        }
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-    }
-  } else if (warp == 3) {
+  } else if (warp < C::W_EPI) {
   } else if (warp < C::W_SOFT) {
     // =================== epilogue: queries in, results out ===================
     const int et = tid - 32 * C::W_EPI, q4 = warp & 3;
@@ -999,8 +1036,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
 #pragma unroll 1
       for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
       for (int i = 0; i < total; ++i) {
-        const int n = 2 * i, s = n % NS;
-        wait(&full[s], n / NS);
+        const int s = (i % (NS / 2)) * 2;
+        wait(&full[s], i / (NS / 2));
         wait(&kd_free[i % C::KB], i / C::KB - 1);
         tc_fence_after();
         const uint8_t* row = ring + s * C::SLOT + key * (D / 2);
@@ -1051,8 +1088,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         tmem_wait_st();
       }
       for (int i = 0; i < total; ++i) {
-        const int n = 2 * i + 1, s = n % NS;
-        wait(&full[s], n / NS);
+        const int s = (i % (NS / 2)) * 2 + 1;
+        wait(&full[s], i / (NS / 2));
         wait(&vd_free[i % C::KB], i / C::KB - 1);
         tc_fence_after();
         if (q4 < C::V_WARPS) {
