@@ -25,8 +25,8 @@ constexpr int kMaxPieces = 768;    // pieces of cut units in a call
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
 constexpr int kParamSlots = 8;     // tiles of s and m in shared memory
 constexpr int kCandidates = 32;
-constexpr long long kMaxCycles = 2000000000LL;  // that a wait lasts at most
-constexpr int kBarEpi = 1, kBarGroup0 = 2;  // named barriers: the epilogue's warps, each softmax warpgroup
+constexpr uint32_t kMaxTries = 500000;  // of a wait, 2 s
+constexpr int kBarEpi = 1, kBarEnd = 2, kBarGroup0 = 3;  // named barriers: the epilogue's warps, all at the end, each softmax warpgroup
 constexpr float kUnseen = -3e38f;  // reference of a row that has seen no key
 static_assert(kMaxPieces / 2 * 4 <= SPEC_ATTN_COUNTER_BYTES, "a counter for every cut unit");
 
@@ -57,8 +57,12 @@ struct Cfg {
   static constexpr bool Q4 = Q4_;
   static constexpr bool FP16 = FP16_;         // type of the MMA operands (4-bit: always fp16)
   static constexpr int N = ROWS < 16 ? 16 : ROWS;
-  static constexpr int NG = ROWS <= 8 ? 1 : 2;  // softmax warpgroups, each ROWS / NG rows of every tile
+  // Softmax: ST streams, which take the tiles in turns and have an accumulator, references and sums of their own (a tile
+  // is a long chain of steps for its warps), with NG warpgroups each, ROWS / NG rows of a tile.
+  static constexpr int ST = Q4 && ROWS <= 32 ? 2 : 1;
+  static constexpr int NG = ROWS <= 16 ? 1 : ROWS / 16;
   static constexpr int CW = ROWS / NG;
+  static constexpr int CHUNK = CW > 8 && Q4 && ROWS > 16 ? 8 : CW;  // scores that a softmax thread holds at once (registers)
   static constexpr int HALVES = D == 256 ? 2 : 1;  // O^T accumulators of 128 lanes
   // A 16-bit fp16 weight keeps its bits between 2^15 and 2^-14 only: two bands of weights, the lower one times 2^18, with
   // an accumulator each, cover 2^15 to 2^-32. (4-bit: the reference takes the values' scale along, see softmax.)
@@ -67,28 +71,39 @@ struct Cfg {
   static constexpr int NP = D == 256 && N == 64 && BANDS == 2 ? 1 : 2;  // P buffers
   static constexpr int KB = D == 256 ? 1 : 2;                      // 4-bit: unpacked K (and V) tiles in tensor memory
   static constexpr int OPERANDS = Q4 ? KB * (D / 2 + HALVES * (TK / 2)) : 0;
-  static constexpr int O_COLS = BANDS * HALVES * N;
-  static constexpr int OB = OPERANDS + 2 * N + 2 * O_COLS <= 512 ? 2 : 1;  // accumulators
+  static constexpr int O_COLS = BANDS * HALVES * N;                 // of a stream
+  static constexpr int OB = OPERANDS + 2 * N + 2 * ST * O_COLS <= 512 ? 2 : 1;  // tasks whose accumulators there is room for
   static constexpr int COL_K = 0, COL_V = Q4 ? KB * (D / 2) : 0, COL_S = OPERANDS, COL_O = COL_S + 2 * N;
-  static constexpr int COLS = COL_O + OB * O_COLS;
+  static constexpr int COLS = COL_O + OB * ST * O_COLS;
   static constexpr int ALLOC = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
-  static constexpr int SLOT = Q4 ? TK * D / 2 : TK * D * 2;  // one K or V tile
+  // A ring of tiles, K and V in turns; those of head dim 256 in two parts of 128 head dims (16-bit).
+  static constexpr int PARTS = D == 256 && !Q4 ? 2 : 1;
+  static constexpr int SLOT = Q4 ? TK * D / 2 : TK * D * 2 / PARTS;
   static constexpr int Q_BYTES = N * D * 2;
   static constexpr int P_BYTES = N * TK * 2;
   // P is the operand B of the second product, MN-major: the N rows of a key are contiguous and swizzled at that width.
   static constexpr uint32_t P_LAYOUT = N == 16 ? 6u : (N == 32 ? 4u : 2u);
   static constexpr int P_SWZ_SHIFT = N == 16 ? 2 : (N == 32 ? 1 : 0);
   static constexpr int P_SWZ_MASK = N == 16 ? 1 : (N == 32 ? 3 : 7);
-  static constexpr int W_EPI = 4, W_SOFT = 8, W_K = W_SOFT + 4 * NG, W_V = W_K + 4;  // first warps of the roles
+  static constexpr int W_EPI = 4, W_SOFT = 8, W_K = W_SOFT + 4 * NG * ST, W_V = W_K + 4;  // first warps of the roles
   static constexpr int kWarps = Q4 ? W_V + 4 : W_K;
   static constexpr int kThreads = 32 * kWarps;
+  // Registers a thread of the softmax and of the other roles, where they are dealt out anew: 24 warps are launched with
+  // 80, 32 with 64.
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kOtherRegs = kWarps == 24 ? 64 : 48, kSoftRegs = kWarps == 24 ? 112 : 80;
+  static constexpr bool DEAL = Q4 && kWarps >= 24;
+  static_assert(!DEAL || 4 * NG * ST * kSoftRegs + (kWarps - 4 * NG * ST) * kOtherRegs <= kWarps * kLaunchRegs, "registers");
+  static_assert(ST == 1 || NP == 2, "a stream has a P buffer of its own");
   static constexpr int V_WARPS = D / 32 < 4 ? D / 32 : 4;  // 4-bit: warps that unpack V, 32 head dims each (and a half)
   // What a task's start and end, a join, and a piece of it cost, in tiles (us over the us of a tile at the measured copy
   // bandwidth, 45 KB a us for each SM, but 0.35 us at least).
-  static constexpr float TILE_US = 2.f * SLOT / 45000.f > 0.35f ? 2.f * SLOT / 45000.f : 0.35f;
+  static constexpr float TILE_US = 2.f * PARTS * SLOT / 45000.f > 0.35f ? 2.f * PARTS * SLOT / 45000.f : 0.35f;
   static constexpr float TASK_COST = 1.f / TILE_US, JOIN_COST = 2.f / TILE_US, PIECE_COST = 0.15f / TILE_US;
-  static constexpr float SHIFT = 7.f, LIMIT = 15.f;  // weights are 2^SHIFT at the reference's maximum, 2^LIMIT at most
+  // Weights are 2^SHIFT at the largest of the tile that set a row's reference, TOP at most.
+  static constexpr float SHIFT = 7.f, TOP = 32768.f;
+  static constexpr float TINY = 0x1p-60f;  // 4-bit: the smallest s that the reference follows
 };
 
 // Shared memory besides the ring, in order.
@@ -97,15 +112,15 @@ struct Smem {
   static constexpr int Q = 0;
   static constexpr int P = Q + C::QB * C::Q_BYTES;
   static constexpr int BARS = P + C::NP * C::BANDS * C::P_BYTES;  // 96 mbarriers
-  static constexpr int REF = BARS + 96 * 8;                       // [64] reference of each row
-  static constexpr int ALPHA = REF + 256;                         // [64]
-  static constexpr int RED = ALPHA + 256;                         // [4][64]
-  static constexpr int STAT = RED + 1024;                         // per accumulator: [4][64] sums, [4][64] offsets, [64] reference
+  static constexpr int REF = BARS + 96 * 8;                       // [ST][64] minus the reference of each row
+  static constexpr int ALPHA = REF + C::ST * 256;                 // [ST][64]
+  static constexpr int RED = ALPHA + C::ST * 256;                 // [ST][4][64]
+  static constexpr int STAT = RED + C::ST * 1024;                 // [OB][ST]: [4][64] sums, [4][64] offsets, [64] reference
   static constexpr int STAT_BYTES = 2048 + 256;
-  static constexpr int QC = STAT + 2 * STAT_BYTES;                // [QB][2][64] factors of the scores
+  static constexpr int QC = STAT + C::OB * C::ST * STAT_BYTES;    // [QB][2][64] factors of the scores
   static constexpr int PAR = QC + C::QB * 512;                    // [kParamSlots][2][128] s and m of K and V
-  static constexpr int EPI = PAR + (C::Q4 ? kParamSlots * 1024 : 0);   // [64] int64 and twice [64] floats of the epilogue
-  static constexpr int MISC = EPI + 1024;  // [64] plan, tensor-memory base, flags
+  static constexpr int EPI = PAR + (C::Q4 ? kParamSlots * 1024 : 0);   // [64] int64 and three times [64] floats of the epilogue
+  static constexpr int MISC = EPI + 1280;  // [64] plan, tensor-memory base, flags
   static constexpr int PREFIX = MISC + 256;
 };
 template <class C>
@@ -160,23 +175,63 @@ __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
-// mbarrier.try_wait that may sleep for a millisecond: a warp that asks again and again takes issue slots from those that
-// work (20 of 24 warps wait at any time).
-__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
+// K or V rows of a head: box {64 elements, 1 head, rows} at {c0, head, row}; c0 a multiple of 8.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const void* map, int c0, int head, int row, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4}], [%5], %6;\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(head), "r"(row), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t l2_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(pol));
+  return pol;
+}
+// Barriers by their shared-memory address.
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the phase of this parity, `tries` times at most; if they run out, 1 is left of them, which says so and makes
+// later waits short. A try sleeps for up to 4 us (7819 cycles measured; 1942 without the hint). Few instructions: the
+// roles' loops together have to fit the instruction cache.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, uint32_t& tries) {
   asm volatile(
       "{\n"
       ".reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      "selp.u32 %0, 1, 0, p;\n"
+      ".reg .u32 n;\n"
+      "mov.u32 n, %0;\n"
+      "TRY:\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n"
+      "@p bra DONE;\n"
+      "sub.u32 n, n, 1;\n"
+      "setp.ne.u32 p, n, 0;\n"
+      "@p bra TRY;\n"
+      "mov.u32 %0, 1;\n"
+      "DONE:\n"
       "}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "+r"(tries)
+      : "r"(bar), "r"(parity)
       : "memory");
-  return ok != 0;
+}
+// The barrier gets one arrival when all MMAs that this warp issued so far are complete.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "}\n" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -186,6 +241,32 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Pairs of fp32 in one register pair.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
@@ -226,7 +307,7 @@ struct Task {
 };
 // Tasks are numbered by sequence, piece, kv head and group, so that the blocks of a wave read the same tokens for all
 // heads at about the same time: a line of a 4-bit token row holds several heads.
-static __device__ __noinline__ Task task_at(const Params& p, const int32_t* prefix, const uint16_t* cut, int t) {
+__device__ __forceinline__ Task task_at(const Params& p, const int32_t* prefix, const uint16_t* cut, int t) {
   int lo = 0, hi = p.batch;  // the last b with prefix[b] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -343,6 +424,15 @@ __device__ __forceinline__ void make_plan(const Params& p, int32_t* prefix, uint
 // ---------------------------------------------------------------------------
 // Kernel
 // ---------------------------------------------------------------------------
+// A place in a ring of n slots, and how often its end has been passed.
+struct Ring {
+  int slot = 0, round = 0;
+  __device__ __forceinline__ void advance(int by, int n) {
+    slot += by;
+    if (slot >= n) slot -= n, ++round;
+  }
+};
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const __grid_constant__ Params p,
                                                                           const __grid_constant__ CUtensorMap tm_k,
@@ -354,29 +444,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   const int NS = p.slots;
   uint8_t* ring = smem;
   uint8_t* fixed = ring + (size_t)NS * C::SLOT;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(fixed + S::BARS);
-  uint64_t* full = bars;                     // [kMaxSlots] a tile has landed
-  uint64_t* empty = full + kMaxSlots;        // [kMaxSlots] its slot may be filled again
-  uint64_t* q_full = empty + kMaxSlots;      // [QB] queries and their factors written
-  uint64_t* kd_full = q_full + 2;            // [KB] 4-bit: K unpacked
-  uint64_t* kd_free = kd_full + 2;
-  uint64_t* vd_full = kd_free + 2;
-  uint64_t* vd_free = vd_full + 2;
-  uint64_t* s_full = vd_free + 2;            // [2] scores of a tile
-  uint64_t* p_full = s_full + 2;             // [2] weights of a tile written
-  uint64_t* pv_done = p_full + 2;            // [NP] second product of the tile that used the P buffer is complete
-  uint64_t* o_full = pv_done + 2;            // [OB] a task's accumulator is complete
-  uint64_t* o_free = o_full + 2;             // [OB] and has been read, with the statistics
-  uint64_t* st_full = o_free + 2;            // [OB] a task's statistics are written
-  uint64_t* par_full = st_full + 2;          // [kParamSlots] 4-bit: s and m of a tile
-  uint64_t* par_free = par_full + kParamSlots;
-  static_assert(2 * kMaxSlots + 2 * 11 + 2 * kParamSlots <= 96, "barriers fit their area");
-  float* s_ref = reinterpret_cast<float*>(fixed + S::REF);
-  float* s_alpha = reinterpret_cast<float*>(fixed + S::ALPHA);
-  float* s_red = reinterpret_cast<float*>(fixed + S::RED);
+  const uint32_t ring_u32 = smem_u32(ring), fixed_u32 = smem_u32(fixed);
+  const uint32_t q_u32 = fixed_u32 + S::Q, p_u32 = fixed_u32 + S::P;
   int32_t* misc = reinterpret_cast<int32_t*>(fixed + S::MISC);
   int32_t* prefix = reinterpret_cast<int32_t*>(fixed + S::PREFIX);
   uint16_t* cut = reinterpret_cast<uint16_t*>(prefix + p.batch + 1);
+  // mbarriers, 8 bytes each
+  const uint32_t full = fixed_u32 + S::BARS;        // [kMaxSlots] a tile has landed
+  const uint32_t empty = full + 8 * kMaxSlots;      // [kMaxSlots] its slot may be filled again
+  const uint32_t par_full = empty + 8 * kMaxSlots;  // [kParamSlots] 4-bit: s and m of a tile
+  const uint32_t par_free = par_full + 8 * kParamSlots;
+  const uint32_t q_full = par_free + 8 * kParamSlots;  // [QB] queries and their factors written
+  const uint32_t kd_full = q_full + 16, kd_free = kd_full + 16;  // [KB] 4-bit: K unpacked
+  const uint32_t vd_full = kd_free + 16, vd_free = vd_full + 16;  // [KB]
+  const uint32_t s_full = vd_free + 16;    // [2] scores of a tile
+  const uint32_t p_full = s_full + 16;     // [2] weights of a tile written
+  const uint32_t pv_done = p_full + 16;    // [NP] second product of the tile that used the P buffer is complete
+  const uint32_t o_full = pv_done + 16;    // [OB] a task's accumulators are complete
+  const uint32_t o_free = o_full + 16;     // [OB] and have been read, with the statistics
+  const uint32_t st_full = o_free + 16;    // [OB] a task's statistics are written
+  static_assert(2 * kMaxSlots + 2 * kParamSlots + 22 <= 96, "barriers fit their area");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grid = (int)gridDim.x, me = (int)blockIdx.x;
@@ -398,38 +485,38 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   volatile int32_t* s_bad = misc;  // [32] a task (number & 31) met a bad page; the producer is less than 32 tasks ahead
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc) + 32;
   int32_t* s_last = misc + 33;
-  volatile int32_t* s_abort = misc + 34;  // a wait ran out: nothing more is issued, and no one waits any longer
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), C::ALLOC);
     tmem_relinquish();
   }
   if (tid == 0) {
-    const uint32_t readers = C::Q4 ? 4 : 1;
+#pragma unroll 1
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], C::Q4 ? 32 : 1);
-      mbar_init(&empty[s], readers);
+      bar_init(full + 8 * s, C::Q4 ? 32 : 1);
+      bar_init(empty + 8 * s, C::Q4 ? 4 : 1);
     }
-    for (int j = 0; j < 2; ++j) {
-      mbar_init(&q_full[j], 4);
-      mbar_init(&kd_full[j], 4);
-      mbar_init(&kd_free[j], 1);
-      mbar_init(&vd_full[j], 4);
-      mbar_init(&vd_free[j], 1);
-      mbar_init(&s_full[j], 1);
-      mbar_init(&p_full[j], 4 * C::NG);
-      mbar_init(&pv_done[j], 1);
-      mbar_init(&o_full[j], 1);
-      mbar_init(&o_free[j], 4);
-      mbar_init(&st_full[j], 4 * C::NG);
-    }
+#pragma unroll 1
     for (int j = 0; j < kParamSlots; ++j) {
-      mbar_init(&par_full[j], 32);
-      mbar_init(&par_free[j], 4 * C::NG);
+      bar_init(par_full + 8 * j, 32);
+      bar_init(par_free + 8 * j, 4 * C::NG);
+    }
+#pragma unroll 1
+    for (int j = 0; j < 16; j += 8) {
+      bar_init(q_full + j, 4);
+      bar_init(kd_full + j, 4);
+      bar_init(kd_free + j, 1);
+      bar_init(vd_full + j, 4);
+      bar_init(vd_free + j, 1);
+      bar_init(s_full + j, 1);
+      bar_init(p_full + j, 4 * C::NG);
+      bar_init(pv_done + j, 1);
+      bar_init(o_full + j, 1);
+      bar_init(o_free + j, 4);
+      bar_init(st_full + j, 4 * C::NG * C::ST);
     }
     fence_mbar_init();
-    for (int j = 0; j < 32; ++j) s_bad[j] = 0;
-    *s_abort = 0;
   }
+  if (tid < 32) s_bad[tid] = 0;
   // what no one writes and the tensor core reads: weights of rows behind the last one (their sums are not used)
 #pragma unroll 1
   for (int i = tid; i < C::NP * C::BANDS * C::P_BYTES / 16; i += C::kThreads)
@@ -439,23 +526,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const uint32_t ring_u32 = smem_u32(ring), q_u32 = smem_u32(fixed + S::Q), p_u32 = smem_u32(fixed + S::P);
 
-  auto wait = [&](uint64_t* bar, int n) {  // until the bar's phase n is complete (n < 0: at once)
-    if (n < 0) return;
-    for (long long start = 0; !try_wait_long(bar, (uint32_t)(n & 1));) {
-      const long long now = clock64();
-      if (start == 0) start = now;
-      if (*s_abort) break;
-      if (now - start > kMaxCycles) {
-        *s_abort = 1;
-        raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
-      }
-    }
+  uint32_t tries = kMaxTries;
+  auto wait = [&](uint32_t bar, int n) {  // until the bar's phase n is complete (n < 0: at once)
+    if (n >= 0) bar_wait(bar, (uint32_t)(n & 1), tries);
+  };
+  auto leave = [&]() {  // the end of every warp but the one that gives tensor memory back
+    if (tries == 1) raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
+    tc_fence_before();
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;\n" ::"n"(kBarEnd), "n"(C::kThreads) : "memory");
+  };
+  auto other_regs = [&]() {
+    if constexpr (C::DEAL) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
   };
 
+  // Each role has its own instruction for its registers, and its own end: where branches join, the compiler would hold all
+  // that follows to the smaller number.
   if (C::Q4 ? warp < C::W_EPI && warp != 1 : warp == 0) {
     // =================== producers ===================
+    other_regs();
     const int bs = 1 << p.page_shift, ppt = TK >> p.page_shift;
     // 32 entries of the task's page list from entry l0 on, one a lane; -1 for those behind its end and for bad pages
     auto page_ids = [&](const Task& k, int l0, int seq) {
@@ -470,6 +560,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad[seq & 31] = 1;
       return id;
     };
+    Ring at;
+    int i = 0, seq = 0;
     if constexpr (C::Q4) {
       // One warp copies K, one V, with 16-byte cp.async: a tensor copy's rate goes by its rows, whose 64 bytes (head dim
       // 128) are too few. Rows are swizzled so that both ways of reading a tile are free of bank conflicts. A third warp
@@ -478,12 +570,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       const int w = warp == 0 ? 0 : 1, H = NS / 2, c = lane % CPR, r0 = lane / CPR;
       const uint32_t row = (uint32_t)p.row;
       const uint8_t* src = (w == 0 ? p.kpar : p.vpar) - (int64_t)p.kv_heads * (D / 2) + (uint64_t)r0 * row + c * 16;
-      int i = 0, seq = 0;
+#pragma unroll 1
       for (int t = me; t < tasks; t += grid, ++seq) {
         const Task k = task_at(p, prefix, cut, t);
         int win = -1, ids = 0;
         if (lane == 0 && warp == 0) s_bad[seq & 31] = 0;
         __syncwarp();
+#pragma unroll 1
         for (int j = 0; j < k.tiles; ++j, ++i) {
           const int l0 = (k.tile0 + j) * ppt;
           if (win < 0 || l0 >= win + 32) {
@@ -492,48 +585,51 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           }
           if (warp == 3) {
             const int s = i % kParamSlots;
-            wait(&par_free[s], i / kParamSlots - 1);
-            if (__any_sync(0xffffffffu, *s_abort)) break;
-            const uint32_t dst = smem_u32(fixed + S::PAR + s * 1024);
-#pragma unroll 2
+            wait(par_free + 8 * s, i / kParamSlots - 1);
+            if (tries == 1) break;
+            const uint32_t dst = fixed_u32 + S::PAR + s * 1024;
+#pragma unroll 1
             for (int r = lane; r < TK; r += 32) {
               const int id = __shfl_sync(0xffffffffu, ids, l0 - win + (r >> p.page_shift));
               const uint32_t slot = ((uint32_t)max(id, 0) << p.page_shift) + (r & (bs - 1));
-              const uint64_t at = (uint64_t)slot * row + 4 * k.g;
-              cp_async_4(dst + r * 4, p.kpar + at, id < 0 ? 0 : 4);
-              cp_async_4(dst + 512 + r * 4, p.vpar + at, id < 0 ? 0 : 4);
+              const uint64_t off = (uint64_t)slot * row + 4 * k.g;
+              cp_async_4(dst + r * 4, p.kpar + off, id < 0 ? 0 : 4);
+              cp_async_4(dst + 512 + r * 4, p.vpar + off, id < 0 ? 0 : 4);
             }
-            cp_async_arrive(&par_full[s]);
+            cp_async_arrive(par_full + 8 * s);
           } else {
-            const int s = (i % H) * 2 + w;
-            wait(&empty[s], i / H - 1);
-            if (__any_sync(0xffffffffu, *s_abort)) break;
+            const int s = at.slot * 2 + w;
+            wait(empty + 8 * s, at.round - 1);
+            at.advance(1, H);
+            if (tries == 1) break;
+#pragma unroll 1
             for (int pc = 0; pc < ppt; ++pc) {
               const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
               const uint32_t dst = ring_u32 + s * C::SLOT + ((pc << p.page_shift) + r0) * (D / 2);
               const uint8_t* from = src + (uint64_t)((uint32_t)max(id, 0) << p.page_shift) * row + k.g * (D / 2);
-#pragma unroll 4
+#pragma unroll 2
               for (int r = 0; r < bs; r += RPI) {
                 const int swz = D == 64 ? (r0 >> 2) & 1 : D == 128 ? (r0 >> 1) & 3 : (r0 + r) & 7;
                 cp_async_16(dst + r * (D / 2) + ((c ^ swz) << 4), from, id < 0 ? 0 : 16);
                 from += RPI * row;
               }
             }
-            cp_async_arrive(&full[s]);
+            cp_async_arrive(full + 8 * s);
           }
         }
       }
       cp_async_commit();
       cp_async_wait<0>();
     } else {
-      const bool once = p.groups == 1;  // read by this block alone
-      const uint64_t policy = l2_evict_first_policy();
-      int at = 0, seq = 0;  // tiles loaded (K and V in turns), tasks
+      // K and V that no other unit reads again are the first to leave L2
+      const uint64_t policy = p.groups == 1 ? l2_evict_first_policy() : l2_normal_policy();
+#pragma unroll 1
       for (int t = me; t < tasks; t += grid, ++seq) {
         const Task k = task_at(p, prefix, cut, t);
         int win = -1, ids = 0;
         if (lane == 0) s_bad[seq & 31] = 0;
         __syncwarp();
+#pragma unroll 1
         for (int j = 0; j < k.tiles; ++j) {
           const int l0 = (k.tile0 + j) * ppt;
           if (win < 0 || l0 >= win + 32) {
@@ -541,126 +637,160 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             ids = page_ids(k, l0, seq);
           }
 #pragma unroll 1
-          for (int w = 0; w < 2; ++w, ++at) {
-            const int s = at % NS;
-            wait(&empty[s], at / NS - 1);
-            if (__any_sync(0xffffffffu, *s_abort)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)C::SLOT);
+          for (int w = 0; w < 2 * C::PARTS; ++w, ++i) {
+            const int s = at.slot;
+            wait(empty + 8 * s, at.round - 1);
+            if (tries == 1) break;
+            at.advance(1, NS);
+            if (lane == 0) bar_expect(full + 8 * s, (uint32_t)C::SLOT);
             __syncwarp();
-            const CUtensorMap* map = w == 0 ? &tm_k : &tm_v;
-            const uint32_t dst = ring_u32 + s * C::SLOT;
+            const CUtensorMap* map = w < C::PARTS ? &tm_k : &tm_v;
+            const int c0 = w % C::PARTS * 128;
 #pragma unroll 1
             for (int pc = 0; pc < ppt; ++pc) {
               const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
               const int row = id < 0 ? -bs : id << p.page_shift;  // outside of the cache: zeros
               if (lane == 0) {
 #pragma unroll
-                for (int sub = 0; sub < D / 64; ++sub) {
-                  const uint32_t to = dst + sub * TK * 128 + pc * bs * 128;
-                  if (once) tma_load_3d_hint(to, map, sub * 64, k.g, row, &full[s], policy);
-                  else tma_load_3d(to, map, sub * 64, k.g, row, &full[s]);
-                }
+                for (int sub = 0; sub < D / 64 / C::PARTS; ++sub)
+                  tma_rows(ring_u32 + s * C::SLOT + sub * TK * 128 + pc * bs * 128, map, c0 + sub * 64, k.g, row, full + 8 * s,
+                           policy);
               }
             }
             __syncwarp();
           }
         }
       }
-      if (*s_abort)  // copies in flight still write here
-        for (int n = max(0, at - NS); n < at; ++n) mbar_wait_bounded(&full[n % NS], (uint32_t)((n / NS) & 1), 20000000LL);
+      if (tries == 1) {  // copies in flight still write here
+        uint32_t few = 1000;
+        for (int n = max(0, i - NS); n < i; ++n) bar_wait(full + 8 * (n % NS), (uint32_t)((n / NS) & 1), few);
+      }
     }
-  } else if (warp == 1) {
+    leave();
+    return;
+  }
+  if (warp == 1) {
     // =================== MMA: scores of tile i + 1, then the product of tile i ===================
+    other_regs();
     const uint32_t id_qk = mma_desc<C::FP16>(N, 0, 0), id_pv = mma_desc<C::FP16>(N, C::Q4 ? 0 : 1, 1);
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);          // K, Q: K-major
     const uint64_t vmn = smem_desc_sw128(0, TK * 128, 1024);     // V: MN-major
     const uint64_t pmn = smem_desc(0, 16, 16 * N, C::P_LAYOUT);  // P: MN-major, groups of 8 keys
-    const uint32_t kq_lo = (uint32_t)kmaj, kq_hi = (uint32_t)(kmaj >> 32), v_lo = (uint32_t)vmn, v_hi = (uint32_t)(vmn >> 32);
-    const uint32_t w_lo = (uint32_t)pmn, w_hi = (uint32_t)(pmn >> 32);
-    int qt = me, q_left = task_at(p, prefix, cut, me).tiles, q_seq = 0, qi = 0;  // the next tile of scores
-    auto scores = [&]() {
-      wait(&q_full[q_seq % C::QB], q_seq / C::QB);
-      const uint32_t qb = (q_u32 + (q_seq % C::QB) * C::Q_BYTES) >> 4, dst = tmem + C::COL_S + (qi & 1) * N;
-      if constexpr (C::Q4) {
-        wait(&kd_full[qi % C::KB], qi / C::KB);
-        tc_fence_after();
-#pragma unroll 1
-        for (int sl = 0; sl < D / 64; ++sl) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ts(dst, tmem + C::COL_K + (qi % C::KB) * (D / 2) + sl * 32 + ks * 8, kq_lo + qb + ((sl * N * 128 + ks * 32) >> 4),
-                    kq_hi, id_qk, sl + ks > 0 ? 1u : 0u);
-        }
-        umma_commit_elect(&s_full[qi & 1]);
-        umma_commit_elect(&kd_free[qi % C::KB]);
-      } else {
-        const int n = 2 * qi, s = n % NS;
-        wait(&full[s], n / NS);
-        tc_fence_after();
-        const uint32_t kb = (ring_u32 + s * C::SLOT) >> 4;
-#pragma unroll 1
-        for (int sl = 0; sl < D / 64; ++sl) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(dst, kq_lo + kb + ((sl * TK * 128 + ks * 32) >> 4), kq_hi, kq_lo + qb + ((sl * N * 128 + ks * 32) >> 4),
-                   kq_hi, id_qk, sl + ks > 0 ? 1u : 0u);
-        }
-        umma_commit_elect(&s_full[qi & 1]);
-        umma_commit_elect(&empty[s]);
-      }
-      ++qi;
-      if (--q_left == 0) {
-        qt += grid;
-        ++q_seq;
-        if (qt < tasks) q_left = task_at(p, prefix, cut, qt).tiles;
-      }
-    };
+    const uint32_t kq_hi = (uint32_t)(kmaj >> 32), v_hi = (uint32_t)(vmn >> 32), w_hi = (uint32_t)(pmn >> 32);
+    // Values that the compiler knows to be the same in all lanes are operands of the MMAs as they are; others would be
+    // moved to uniform registers for each.
+    auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const uint32_t tm = uniform(tmem);
+    const int n_slots = (int)uniform((uint32_t)NS), all = (int)uniform((uint32_t)tasks);
+    const uint32_t q_lo = uniform((uint32_t)kmaj + (q_u32 >> 4)), k_lo = uniform((uint32_t)kmaj + (ring_u32 >> 4));
+    const uint32_t v_lo = uniform((uint32_t)vmn + (ring_u32 >> 4)), p_lo = uniform((uint32_t)pmn + (p_u32 >> 4));
+    const uint32_t bars = uniform(full);
+    auto bar = [&](uint32_t b) { return bars + (b - full); };
+    auto tiles_at = [&](int t) { return (int)uniform((uint32_t)task_at(p, prefix, cut, t).tiles); };
+    int qt = me, q_left = tiles_at(me), q_seq = 0, qi = 0;  // the next tile of scores
+    Ring k_at, v_at;                                        // 16-bit: slots of its K, and of the next product's V
+    v_at.advance(C::PARTS, n_slots);
     int t = me, seq = 0, tiles = q_left, j = -1;  // tile j of task t is next for the second product; -1: scores first
-    for (int i = -1; t < tasks; ++i) {
-      if (__any_sync(0xffffffffu, *s_abort)) break;
-      if (qt < tasks) scores();
-      if (j >= 0) {
-        const uint32_t o = tmem + C::COL_O + (seq % C::OB) * C::O_COLS;
-        if (j == 0) wait(&o_free[seq % C::OB], seq / C::OB - 1);
-        wait(&p_full[i & 1], i >> 1);
-        const uint32_t pb = (p_u32 + (i % C::NP) * C::BANDS * C::P_BYTES) >> 4;
-        const int n = 2 * i + 1, s = n % NS;
-        if constexpr (C::Q4) wait(&vd_full[i % C::KB], i / C::KB);
-        else wait(&full[s], n / NS);
-        tc_fence_after();
-        const uint32_t vb = (ring_u32 + s * C::SLOT) >> 4;
 #pragma unroll 1
-        for (int part = 0; part < C::BANDS * C::HALVES; ++part) {
-          const int band = part / C::HALVES, hh = part % C::HALVES;
+    for (int i = -1; t < all && tries != 1; ++i) {
+      if (qt < all) {
+        wait(bar(q_full) + 8 * (q_seq % C::QB), q_seq / C::QB);
+        const uint32_t qb = q_lo + (q_seq % C::QB) * (C::Q_BYTES >> 4), dst = tm + C::COL_S + (qi & 1) * N;
+        if constexpr (C::Q4) {
+          wait(bar(kd_full) + 8 * (qi % C::KB), qi / C::KB);
+          tc_fence_after();
+          const uint32_t a = tm + C::COL_K + (qi % C::KB) * (D / 2);
 #pragma unroll 1
-          for (int k4 = 0; k4 < TK / 64; ++k4) {
+          for (int sl = 0; sl < D / 64; ++sl)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t b = w_lo + pb + ((band * C::P_BYTES + (k4 * 4 + kk) * 32 * N) >> 4);
-              const uint32_t acc = j > 0 || k4 + kk > 0 ? 1u : 0u;
-              if constexpr (C::Q4)
-                umma_ts(o + part * N, tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + k4 * 32 + kk * 8, b, w_hi,
-                        id_pv, acc);
-              else
-                mma_ss(o + part * N, v_lo + vb + ((hh * 2 * TK * 128 + (k4 * 4 + kk) * 2048) >> 4), v_hi, b, w_hi, id_pv, acc);
-            }
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ts(dst, a + sl * 32 + ks * 8, qb + sl * (N * 128 >> 4) + ks * 2, kq_hi, id_qk, sl + ks > 0 ? 1u : 0u);
+          mma_commit(bar(s_full) + 8 * (qi & 1));
+          mma_commit(bar(kd_free) + 8 * (qi % C::KB));
+        } else {
+#pragma unroll 1
+          for (int part = 0; part < C::PARTS; ++part) {
+            wait(bar(full) + 8 * k_at.slot, k_at.round);
+            tc_fence_after();
+            const uint32_t kb = k_lo + k_at.slot * (C::SLOT >> 4), qp = qb + part * (N * 256 >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16 / C::PARTS; ++ks)
+              mma_ss(dst, kb + (((ks >> 2) * TK * 128 + (ks & 3) * 32) >> 4), kq_hi,
+                     qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, part + ks > 0 ? 1u : 0u);
+            mma_commit(bar(empty) + 8 * k_at.slot);
+            k_at.advance(1, n_slots);
           }
+          mma_commit(bar(s_full) + 8 * (qi & 1));
+          k_at.advance(C::PARTS, n_slots);
         }
-        umma_commit_elect(&pv_done[i % C::NP]);
-        if constexpr (C::Q4) umma_commit_elect(&vd_free[i % C::KB]);
-        else umma_commit_elect(&empty[s]);
-        if (j == tiles - 1) umma_commit_elect(&o_full[seq % C::OB]);
+        ++qi;
+        if (--q_left == 0) {
+          qt += grid;
+          ++q_seq;
+          if (qt < all) q_left = tiles_at(qt);
+        }
+      }
+      if (j >= 0) {
+        const uint32_t o = tm + C::COL_O + ((seq % C::OB) * C::ST + i % C::ST) * C::O_COLS, more = j >= C::ST ? 1u : 0u;
+        if (j == 0) wait(bar(o_free) + 8 * (seq % C::OB), seq / C::OB - 1);
+        wait(bar(p_full) + 8 * (i & 1), i >> 1);
+        const uint32_t pb = p_lo + (i % C::NP) * (C::BANDS * C::P_BYTES >> 4);
+        if constexpr (C::Q4) {
+          wait(bar(vd_full) + 8 * (i % C::KB), i / C::KB);
+          tc_fence_after();
+#pragma unroll 1
+          for (int hh = 0; hh < C::HALVES; ++hh) {
+            const uint32_t a = tm + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2);
+#pragma unroll 1
+            for (int k4 = 0; k4 < 2; ++k4)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts(o + hh * N, a + k4 * 32 + kk * 8, pb + (k4 * 4 + kk) * (32 * N >> 4), w_hi, id_pv, k4 + kk > 0 ? 1u : more);
+          }
+          mma_commit(bar(pv_done) + 8 * (i % C::NP));
+          mma_commit(bar(vd_free) + 8 * (i % C::KB));
+        } else {
+#pragma unroll 1
+          for (int hh = 0; hh < C::HALVES; ++hh) {
+            wait(bar(full) + 8 * v_at.slot, v_at.round);
+            tc_fence_after();
+            const uint32_t vb = v_lo + v_at.slot * (C::SLOT >> 4);
+#pragma unroll 1
+            for (int band = 0; band < C::BANDS; ++band)
+#pragma unroll
+              for (int kk = 0; kk < TK / 16; ++kk)
+                mma_ss(o + (band * C::HALVES + hh) * N, vb + (kk * 2048 >> 4), v_hi, pb + ((band * C::P_BYTES + kk * 32 * N) >> 4),
+                       w_hi, id_pv, kk > 0 ? 1u : more);
+            mma_commit(bar(empty) + 8 * v_at.slot);
+            v_at.advance(1, n_slots);
+          }
+          mma_commit(bar(pv_done) + 8 * (i % C::NP));
+          v_at.advance(C::PARTS, n_slots);
+        }
+        if (j == tiles - 1) mma_commit(bar(o_full) + 8 * (seq % C::OB));
       }
       if (++j == tiles) {
         j = 0;
         ++seq;
         t += grid;
-        if (t < tasks) tiles = task_at(p, prefix, cut, t).tiles;
+        if (t < all) tiles = tiles_at(t);
       }
     }
-  } else if (warp < C::W_EPI) {
-  } else if (warp < C::W_SOFT) {
+    if (tries == 1) raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
+    __syncwarp();
+    named_sync(kBarEnd, C::kThreads);  // no one uses tensor memory any more
+    tc_fence_after();
+    tmem_dealloc(tmem, C::ALLOC);
+    return;
+  }
+  if (warp < C::W_EPI) {
+    other_regs();
+    leave();
+    return;
+  }
+  if (warp < C::W_SOFT) {
     // =================== epilogue: queries in, results out ===================
+    other_regs();
     const int et = tid - 32 * C::W_EPI, q4 = warp & 3;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     // packed row r's place among the rows of its sequence
@@ -679,12 +809,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
 #pragma unroll 1
       for (int r = et / L; r < N; r += 128 / L) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < k.nr) {
-          x = __ldg(reinterpret_cast<const uint4*>(p.q) + ((int64_t)k.b * p.rows * p.heads + row_of(k, r)) * L + c);
-        }
+        if (r < k.nr) x = __ldg(reinterpret_cast<const uint4*>(p.q) + ((int64_t)k.b * p.rows * p.heads + row_of(k, r)) * L + c);
         if constexpr (C::Q4) {
-          // fp16 times a power of two that brings the row's largest element to [2^14, 2^15); the codes come in the order
-          // and with the factors that the unpacking leaves them in (see there): 0 4 1 5 2 6 3 7, odd ones 16-fold
+          // fp16 times a power of two that brings the row's largest element to [2^14, 2^15); the elements in the order and
+          // with the factors that the unpacking leaves the codes in (see there): 0 4 1 5 2 6 3 7, codes 1 3 5 7 16-fold
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
           float f[8], top = 0.f, sum = 0.f;
 #pragma unroll
@@ -718,82 +846,104 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[seq % C::QB]);
+      if (lane == 0) bar_arrive(q_full + 8 * (seq % C::QB));
     };
     // head dim of this thread's lane, and the lane that holds its neighbour
     const int d0 = C::Q4 ? q4 * 32 + 4 * (lane & 7) + (lane >> 3) : q4 * 32 + lane;
     constexpr int NEXT = C::Q4 ? 8 : 1;
     const bool odd = lane & NEXT;
     const float unit = C::Q4 ? (odd ? 0x1p20f : 0x1p24f) : 1.f;
-    int64_t* e_row = reinterpret_cast<int64_t*>(fixed + S::EPI);        // [64] a row's place in the sequence's output
-    float* e_inv = reinterpret_cast<float*>(fixed + S::EPI + 512);      // [64] 1 / its sum
-    float* e_off = e_inv + 64;                                          // [64] what is added to the product
-    int seq = -C::QB;  // the first queries are loaded before the first result
+    int64_t* e_row = reinterpret_cast<int64_t*>(fixed + S::EPI);    // [64] a row's place in the sequence's output
+    float* e_fac = reinterpret_cast<float*>(fixed + S::EPI + 512);  // [ST][64] a stream's weight over the row's sum
+    float* e_off = e_fac + 128;                                     // [64] what is added to the products
+    int seq = -C::QB, base = 0;  // the first queries are loaded before the first result; tiles of the tasks before
+#pragma unroll 1
     for (int t = me - C::QB * grid; t < tasks; t += grid, ++seq) {
-     if (seq >= 0) {
-      const Task k = task_at(p, prefix, cut, t);
-      const int ob = seq % C::OB;
-      wait(&st_full[ob], seq / C::OB);
-      wait(&o_full[ob], seq / C::OB);
-      tc_fence_after();
-      const bool bad = s_bad[seq & 31] != 0;
-      if (bad && et == 0) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
-      named_sync(kBarEpi, 128);  // the last task's entries have been read
-      if (et < k.nr) {
-        const float* stat = reinterpret_cast<const float*>(fixed + S::STAT + ob * S::STAT_BYTES) + et;
-        const float sum = (stat[0] + stat[64]) + (stat[128] + stat[192]);
-        e_row[et] = row_of(k, et) * D;
-        e_inv[et] = bad ? 0.f : 1.f / sum;
-        if constexpr (C::Q4) e_off[et] = (stat[256] + stat[320]) + (stat[384] + stat[448]);
-        // a piece without a visible key has weight 0
-        if (k.pieces > 1)
-          __stcg(p.lse + (int64_t)k.slot * kMaxRows + et, bad ? INFINITY : sum == 0.f ? -INFINITY : stat[512] + log2f(sum));
-      }
-      named_sync(kBarEpi, 128);
-      const uint32_t o = tmem + C::COL_O + ob * C::O_COLS + lane_off;
-      float* part = p.opart + (int64_t)k.slot * N * D;
-      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + (int64_t)k.b * p.rows * p.heads * D;
-#pragma unroll 1
-      for (int c = 0; c < k.nr; c += 8) {
-#pragma unroll 1
-        for (int hh = 0; hh < C::HALVES; ++hh) {
-          float v[8];
-          tmem_load_cols<8>(o + hh * N + c, v);
-          if constexpr (C::BANDS == 2) {
-            float low[8];
-            tmem_load_cols<8>(o + (C::HALVES + hh) * N + c, low);
+      if (seq >= 0) {
+        const Task k = task_at(p, prefix, cut, t);
+        const int ob = seq % C::OB;
+        wait(st_full + 8 * ob, seq / C::OB);
+        wait(o_full + 8 * ob, seq / C::OB);
+        tc_fence_after();
+        const bool bad = s_bad[seq & 31] != 0;
+        if (bad && et == 0) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
+        const int only = C::ST == 2 && k.tiles == 1 ? base % C::ST : -1;  // the one stream that had a tile
+        base += k.tiles;
+        named_sync(kBarEpi, 128);  // the last task's entries have been read
+        if (et < k.nr) {
+          const float* stat = reinterpret_cast<const float*>(fixed + S::STAT + ob * C::ST * S::STAT_BYTES) + et;
+          float sum[C::ST], ref = -INFINITY, total = 0.f, off = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(low[e], 0x1p-18f, v[e]);
+          for (int st = 0; st < C::ST; ++st) {
+            const float* x = stat + st * (S::STAT_BYTES / 4);
+            sum[st] = (x[0] + x[64]) + (x[128] + x[192]);
+            if (sum[st] != 0.f) ref = fmaxf(ref, x[512]);
           }
-          if (D == 64 && q4 >= 2) continue;
-          const int d = hh * 128 + d0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (C::Q4) v[e] = fmaf(v[e], unit, e_off[c + e]);
-            v[e] *= e_inv[c + e];
+          for (int st = 0; st < C::ST; ++st) {
+            const float* x = stat + st * (S::STAT_BYTES / 4);
+            const float f = sum[st] != 0.f ? exp2f(x[512] - ref) : 0.f;
+            total = fmaf(f, sum[st], total);
+            if (C::Q4 && f != 0.f) off = fmaf(f, (x[256] + x[320]) + (x[384] + x[448]), off);
+            e_fac[64 * st + et] = f;
           }
-          if (k.pieces == 1) {
-            // pairs of head dims: one thread writes those of the even row, its neighbour those of the odd row
+          const float inv = bad ? 0.f : 1.f / total;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[e + 1], NEXT);
-              const float lo = odd ? got : v[e], hi = odd ? v[e + 1] : got;
-              const int r = c + e + (odd ? 1 : 0);
-              if (r < k.nr)
-                *reinterpret_cast<uint32_t*>(out + e_row[r] + (d & ~1)) = p.fp16 ? q4::pack2<true>(bad ? 0.f : lo, bad ? 0.f : hi)
-                                                                               : q4::pack2<false>(bad ? 0.f : lo, bad ? 0.f : hi);
+          for (int st = 0; st < C::ST; ++st) e_fac[64 * st + et] *= inv;
+          e_off[et] = off * inv;
+          e_row[et] = row_of(k, et) * D;
+          // a piece without a visible key has weight 0
+          if (k.pieces > 1)
+            __stcg(p.lse + (int64_t)k.slot * kMaxRows + et, bad ? INFINITY : total == 0.f ? -INFINITY : ref + log2f(total));
+        }
+        named_sync(kBarEpi, 128);
+        const uint32_t o = tmem + C::COL_O + ob * C::ST * C::O_COLS + lane_off;
+        float* part = p.opart + (int64_t)k.slot * N * D;
+        uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + (int64_t)k.b * p.rows * p.heads * D;
+#pragma unroll 1
+        for (int c = 0; c < k.nr; c += 8) {
+#pragma unroll 1
+          for (int hh = 0; hh < C::HALVES; ++hh) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e_off[c + e];
+#pragma unroll 1
+            for (int st = 0; st < C::ST; ++st) {
+              if (C::ST == 2 && only >= 0 && only != st) continue;
+              float x[8];
+              tmem_load_cols<8>(o + st * C::O_COLS + hh * N + c, x);
+              if constexpr (C::BANDS == 2) {
+                float low[8];
+                tmem_load_cols<8>(o + (C::HALVES + hh) * N + c, low);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = fmaf(low[e], 0x1p-18f, x[e]);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = fmaf(x[e] * unit, e_fac[64 * st + c + e], v[e]);
             }
-          } else {
+            if (D == 64 && q4 >= 2) continue;
+            const int d = hh * 128 + d0;
+            if (k.pieces == 1) {
+              // pairs of head dims: one thread writes those of the even row, its neighbour those of the odd row
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + e < k.nr) __stcg(part + (c + e) * D + d, v[e]);
+              for (int e = 0; e < 8; e += 2) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[e + 1], NEXT);
+                const float lo = bad ? 0.f : odd ? got : v[e], hi = bad ? 0.f : odd ? v[e + 1] : got;
+                const int r = c + e + (odd ? 1 : 0);
+                if (r < k.nr)
+                  *reinterpret_cast<uint32_t*>(out + e_row[r] + (d & ~1)) = p.fp16 ? q4::pack2<true>(lo, hi) : q4::pack2<false>(lo, hi);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (c + e < k.nr) __stcg(part + (c + e) * D + d, v[e]);
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(o_free + 8 * ob);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[ob]);
-     }
       if (t + C::QB * grid < tasks) load_queries(t + C::QB * grid, seq + C::QB);
       if (seq < 0) continue;
       const Task k = task_at(p, prefix, cut, t);
@@ -829,11 +979,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         }
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.f;
+#pragma unroll 4
         for (int w = 0; w < k.pieces; ++w) {
           const float x = __ldcg(lse + (int64_t)w * kMaxRows);
-          if (x == -INFINITY) continue;
-          const float4 y = __ldcg(src + (int64_t)w * (N * D / 4));
-          const float f = exp2f(x - top);
+          float4 y = __ldcg(src + (int64_t)w * (N * D / 4));
+          const float f = x == -INFINITY ? 0.f : exp2f(x - top);
+          if (x == -INFINITY) y = make_float4(0.f, 0.f, 0.f, 0.f);
           sum += f;
           a.x = fmaf(f, y.x, a.x);
           a.y = fmaf(f, y.y, a.y);
@@ -847,37 +998,57 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         reinterpret_cast<uint2*>(p.out)[((int64_t)k.b * p.rows * p.heads + row_of(k, r)) * (D / 4) + c] = out;
       }
     }
-  } else if (warp < C::W_K) {
+    leave();
+    return;
+  }
+  if (warp < C::W_K) {
     // =================== softmax ===================
-    const int sw = warp - C::W_SOFT, h = sw >> 2, c0 = h * CW, q4 = warp & 3;
-    const int gt = tid - 32 * C::W_SOFT - h * 128, bar_group = kBarGroup0 + h;
+    if constexpr (C::DEAL) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kSoftRegs));
+    const int group = (warp - C::W_SOFT) >> 2, st = group / C::NG, h = group % C::NG, c0 = h * CW, q4 = warp & 3;
+    const int gt = tid - 32 * C::W_SOFT - group * 128, bar_group = kBarGroup0 + group;
+    float* s_ref = reinterpret_cast<float*>(fixed + S::REF) + st * 64;
+    float* s_alpha = reinterpret_cast<float*>(fixed + S::ALPHA) + st * 64;
+    float* s_red = reinterpret_cast<float*>(fixed + S::RED) + st * 256;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const int key = q4 * 32 + lane;  // the lane of the scores that this thread reads
     const int bs = 1 << p.page_shift, ppt_shift = 7 - p.page_shift;
-    int i = 0, seq = 0;
+    int base = 0, seq = 0;
+#pragma unroll 1
     for (int t = me; t < tasks; t += grid, ++seq) {
       const Task k = task_at(p, prefix, cut, t);
       const int ob = seq % C::OB, first = k.ctx - p.rows + k.i0;  // position of the unit's first row
-      float l[CW], off[C::Q4 ? CW : 1];
+      uint64_t l[CW / 2], off[C::Q4 ? CW / 2 : 1];  // pairs of rows
 #pragma unroll
-      for (int e = 0; e < CW; ++e) l[e] = 0.f;
+      for (int e = 0; e < CW / 2; ++e) l[e] = 0;
 #pragma unroll
-      for (int e = 0; e < (C::Q4 ? CW : 1); ++e) off[e] = 0.f;
-      wait(&q_full[seq % C::QB], seq / C::QB);
+      for (int e = 0; e < (C::Q4 ? CW / 2 : 1); ++e) off[e] = 0;
+      wait(q_full + 8 * (seq % C::QB), seq / C::QB);
       const float* qc = reinterpret_cast<const float*>(fixed + S::QC) + (seq % C::QB) * 128 + c0;
-      for (int j = 0; j < k.tiles; ++j, ++i) {
-        // ---- which rows see this thread's key: [r_lo, r_hi)
-        const int lp = ((k.tile0 + j) << ppt_shift) + (key >> p.page_shift);
-        const int tok = ((lp < k.span.ns ? lp : k.span.wp + lp - k.span.ns) << p.page_shift) + (key & (bs - 1));
-        int r_lo = max(0, tok - first) * p.gqa, r_hi = k.nr;
-        if (p.window != 0 && tok >= p.sinks) r_hi = min(r_hi, (int)min((int64_t)1 << 20, max((int64_t)0, (int64_t)tok - first + p.window)) * p.gqa);
-        if (lp >= k.span.pages || tok >= k.ctx) r_hi = 0;
-        const bool dead = r_lo >= r_hi;
-        const bool masked = __any_sync(0xffffffffu, r_lo > 0 || r_hi < k.nr);
-        float ks = 1.f, km = 0.f, vs = 1.f, vm = 0.f, lvs = 0.f;
+#pragma unroll 1
+      for (int j = C::ST == 2 ? (base ^ st) & 1 : 0; j < k.tiles; j += C::ST) {
+        const int i = base + j;  // of stream i % ST
+        // ---- which rows see this thread's key: [r_lo, r_hi); most tiles are seen whole by all
+        const int l0 = (k.tile0 + j) << ppt_shift;
+        const bool early = l0 < k.span.ns;
+        const int from = (early ? l0 : k.span.wp + l0 - k.span.ns) << p.page_shift;
+        const bool whole = l0 + (1 << ppt_shift) <= (early ? k.span.ns : k.span.pages) && from + TK - 1 <= first &&
+                           (p.window == 0 || from + TK <= p.sinks || from > first + k.nr - 1 - p.window);
+        int r_lo = 0, r_hi = N;  // rows of padding see what all rows see
+        bool dead = false;
+        if (!whole) {
+          const int lp = l0 + (key >> p.page_shift);
+          const int tok = ((lp < k.span.ns ? lp : k.span.wp + lp - k.span.ns) << p.page_shift) + (key & (bs - 1));
+          r_lo = max(0, tok - first) * p.gqa;
+          if (p.window != 0 && tok >= p.sinks)
+            r_hi = min(r_hi, (int)min((int64_t)1 << 20, max((int64_t)0, (int64_t)tok - first + p.window)) * p.gqa);
+          if (lp >= k.span.pages || tok >= k.ctx) r_hi = 0;
+          dead = r_lo >= min(r_hi, k.nr);
+        }
+        auto sees = [&](int e) { return c0 + e >= r_lo && c0 + e < r_hi; };
+        float ks = p.scale_log2, km = 0.f, vs = 1.f, vm = 0.f;
         if constexpr (C::Q4) {
           const int s = i % kParamSlots;
-          wait(&par_full[s], i / kParamSlots);
+          wait(par_full + 8 * s, i / kParamSlots);
           const uint32_t* par = reinterpret_cast<const uint32_t*>(fixed + S::PAR + s * 1024);
           const uint32_t a = dead ? 0u : par[key], b = dead ? 0u : par[128 + key];
           const float2 x = p.fp16 ? q4::unpack2<true>(a) : q4::unpack2<false>(a);
@@ -886,65 +1057,112 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           km = x.y;
           vs = y.x;
           vm = fmaf(8.f, y.x, y.y);  // the codes of V are taken from 8
-          lvs = __log2f(fmaxf(fabsf(vs), 0x1p-60f));
           __syncwarp();
-          if (lane == 0) mbar_arrive(&par_free[s]);
+          if (lane == 0) bar_arrive(par_free + 8 * s);
         }
-        wait(&s_full[i & 1], i >> 1);
+        wait(s_full + 8 * (i & 1), i >> 1);
         tc_fence_after();
-        float x[CW];
-        tmem_load_cols<CW>(tmem + C::COL_S + (i & 1) * N + lane_off + c0, x);
-        bool grow = j == 0;
-        float top = -INFINITY;
+        const uint32_t t_s = tmem + C::COL_S + (i & 1) * N + lane_off + c0;
+        const uint64_t ks2 = pack_f2(ks, ks), km2 = pack_f2(km, km), vs2 = pack_f2(vs, vs);
+        uint64_t y[CW / 2];  // the softmax's weights (4-bit: those that meet V are y times s)
+#pragma unroll 1
+        for (bool settled = false;; settled = true) {
+          if (j >= C::ST || settled) {
+            float x[C::CHUNK], top = 0.f;
 #pragma unroll
-        for (int e = 0; e < CW; ++e) {
-          if constexpr (C::Q4) x[e] = fmaf(ks, x[e] * qc[e], km * qc[64 + e]);
-          else x[e] *= p.scale_log2;
-        }
-        if (masked) {
+            for (int e = 0; e < CW; e += 4) {
+              if (e % C::CHUNK == 0) tmem_load_cols<C::CHUNK>(t_s + e, x);
+              const float4 ref = *reinterpret_cast<const float4*>(s_ref + c0 + e);  // minus the reference
+              const float* xe = x + e % C::CHUNK;
+              uint64_t z[2] = {pack_f2(ref.x, ref.y), pack_f2(ref.z, ref.w)};
+              if constexpr (C::Q4) {
+                const float4 qa = *reinterpret_cast<const float4*>(qc + e), qb = *reinterpret_cast<const float4*>(qc + 64 + e);
+                z[0] = fma_f2(km2, pack_f2(qb.x, qb.y), z[0]);
+                z[1] = fma_f2(km2, pack_f2(qb.z, qb.w), z[1]);
+                z[0] = fma_f2(ks2, mul_f2(pack_f2(xe[0], xe[1]), pack_f2(qa.x, qa.y)), z[0]);
+                z[1] = fma_f2(ks2, mul_f2(pack_f2(xe[2], xe[3]), pack_f2(qa.z, qa.w)), z[1]);
+              } else {
+                z[0] = fma_f2(pack_f2(xe[0], xe[1]), ks2, z[0]);
+                z[1] = fma_f2(pack_f2(xe[2], xe[3]), ks2, z[1]);
+              }
 #pragma unroll
-          for (int e = 0; e < CW; ++e)
-            if (c0 + e < r_lo || c0 + e >= r_hi) x[e] = -INFINITY;
-        }
+              for (int u = 0; u < 2; ++u) {
+                const float2 f = unpack_f2(z[u]);
+                y[e / 2 + u] = pack_f2(fast_exp2(f.x), fast_exp2(f.y));
+              }
+            }
+            if (!whole) {
 #pragma unroll
-        for (int e = 0; e < CW; ++e) top = fmaxf(top, x[e] - s_ref[c0 + e]);
-        grow |= top + lvs > C::LIMIT;
-        if (named_sync_or(bar_group, 128, grow)) {
+              for (int e = 0; e < CW; e += 2) {
+                const float2 f = unpack_f2(y[e / 2]);
+                y[e / 2] = pack_f2(sees(e) ? f.x : 0.f, sees(e + 1) ? f.y : 0.f);
+              }
+            }
+            if (settled) break;
+#pragma unroll
+            for (int e = 0; e < CW / 2; ++e) {
+              const float2 f = unpack_f2(C::Q4 ? mul_f2(y[e], vs2) : y[e]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            bool grow = top > C::TOP;
+            if constexpr (C::Q4) {
+              const bool tiny = fabsf(vs) < C::TINY && !dead;  // s does not bound the softmax's own weights
+              if (__any_sync(0xffffffffu, tiny)) {
+                float most = 0.f;
+#pragma unroll
+                for (int e = 0; e < CW / 2; ++e) {
+                  const float2 f = unpack_f2(y[e]);
+                  most = fmaxf(most, fmaxf(f.x, f.y));
+                }
+                grow |= tiny && most > C::TOP / C::TINY;
+              }
+            }
+            if (!named_sync_or(bar_group, 128, grow)) break;
+          }
           // ---- new references: 2^SHIFT below the tile's largest weight (4-bit: weight times s) of each row, if that is
           // higher; what was summed so far is scaled down
+          const float lvs = C::Q4 ? log2f(fmaxf(fabsf(vs), C::TINY)) : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < CW; c += 8) {
+            float x[8];
+            tmem_load_cols<8>(t_s + c, x);
 #pragma unroll
-          for (int e = 0; e < CW; ++e) {
-            const float m = warp_max(x[e] + lvs);
-            if (lane == 0) s_red[q4 * 64 + c0 + e] = m;
+            for (int e = 0; e < 8; ++e) {
+              float s;  // the score in log2 units, and s
+              if constexpr (C::Q4) s = fmaf(ks, x[e] * qc[c + e], fmaf(km, qc[64 + c + e], lvs));
+              else s = x[e] * ks;
+              const float m = warp_max(sees(c + e) ? s : -INFINITY);
+              if (lane == 0) s_red[q4 * 64 + c0 + c + e] = m;
+            }
           }
           named_sync(bar_group, 128);
           if (gt < CW) {
             const int r = c0 + gt;
             const float m = fmaxf(fmaxf(s_red[r], s_red[64 + r]), fmaxf(s_red[128 + r], s_red[192 + r]));
-            const float old = j == 0 ? kUnseen : s_ref[r], now = fmaxf(old, m - C::SHIFT);
-            s_ref[r] = now;
+            const float old = j < C::ST ? kUnseen : -s_ref[r], now = fmaxf(old, m - C::SHIFT);
+            s_ref[r] = -now;
             s_alpha[r] = fast_exp2(old - now);
           }
           named_sync(bar_group, 128);
-          if (j > 0) {
-            wait(&pv_done[(i - 1) % C::NP], (i - 1) / C::NP);
+          if (j >= C::ST) {
+            wait(pv_done + 8 * ((i - C::ST) % C::NP), (i - C::ST) / C::NP);
             tc_fence_after();
-            constexpr int CH = CW < 16 ? CW : 16;
 #pragma unroll
-            for (int e = 0; e < CW; ++e) {
-              l[e] *= s_alpha[c0 + e];
-              if constexpr (C::Q4) off[e] *= s_alpha[c0 + e];
+            for (int e = 0; e < CW / 2; ++e) {
+              const uint64_t a = pack_f2(s_alpha[c0 + 2 * e], s_alpha[c0 + 2 * e + 1]);
+              l[e] = mul_f2(l[e], a);
+              if constexpr (C::Q4) off[e] = mul_f2(off[e], a);
             }
 #pragma unroll 1
             for (int part = 0; part < C::BANDS * C::HALVES; ++part) {
+#pragma unroll 1
+              for (int c = 0; c < CW; c += 8) {
+                const uint32_t o = tmem + C::COL_O + (ob * C::ST + st) * C::O_COLS + part * N + lane_off + c0 + c;
+                float v[8];
+                tmem_load_cols<8>(o, v);
 #pragma unroll
-              for (int c = 0; c < CW; c += CH) {
-                const uint32_t o = tmem + C::COL_O + ob * C::O_COLS + part * N + lane_off + c0 + c;
-                float v[CH];
-                tmem_load_cols<CH>(o, v);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) v[e] *= s_alpha[c0 + c + e];
-                tmem_store_cols<CH>(o, v);
+                for (int e = 0; e < 8; ++e) v[e] *= s_alpha[c0 + c + e];
+                tmem_store_cols<8>(o, v);
               }
             }
           }
@@ -952,52 +1170,54 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if constexpr (!C::Q4) {
           // slots that no row sees may hold anything: zero their V
           if (__any_sync(0xffffffffu, dead)) {
-            // With two slots, K and V of the tile before may be the last that the V barrier's parity knows of; its product
-            // says that they have landed.
-            if (NS == 2 && i > 0) wait(&pv_done[(i - 1) % C::NP], (i - 1) / C::NP);
-            const int n = 2 * i + 1, s = n % NS;
-            wait(&full[s], n / NS);
-            if (dead) {
-              uint8_t* v = ring + s * C::SLOT + key * 128;
-              for (int c = h; c < D / 8; c += C::NG)
-                *reinterpret_cast<uint4*>(v + (c >> 3) * TK * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            // In a short ring what the tile's V replaces may be the V of the tile before, which may not have landed: the
+            // barrier's parity would then name an earlier phase. That tile's product says that it has.
+            if (NS < 3 * C::PARTS && i > 0) wait(pv_done + 8 * ((i - 1) % C::NP), (i - 1) / C::NP);
+#pragma unroll 1
+            for (int part = 0; part < C::PARTS; ++part) {
+              const int n = (2 * i + 1) * C::PARTS + part, s = n % NS;
+              wait(full + 8 * s, n / NS);
+              if (dead) {
+                uint8_t* v = ring + s * C::SLOT + key * 128;
+                for (int c = h; c < D / 8 / C::PARTS; c += C::NG)
+                  *reinterpret_cast<uint4*>(v + (c >> 3) * TK * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
             }
           }
         }
-        // ---- weights
-#pragma unroll
-        for (int e = 0; e < CW; ++e) {
-          x[e] = fast_exp2(x[e] - s_ref[c0 + e]);
-          l[e] += x[e];
-        }
-        if constexpr (C::Q4) {
-          if (masked) {  // s and m of a key may be NaN for the rows that see it
-#pragma unroll
-            for (int e = 0; e < CW; ++e) {
-              const bool see = c0 + e >= r_lo && c0 + e < r_hi;
-              off[e] += see ? x[e] * vm : 0.f;
-              x[e] = see ? x[e] * vs : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < CW; ++e) {
-              off[e] = fmaf(x[e], vm, off[e]);
-              x[e] *= vs;
-            }
-          }
-        }
+        // ---- sums, and the weights in 16 bits
         uint32_t hi[CW / 2], lo[C::BANDS == 2 ? CW / 2 : 1];
 #pragma unroll
-        for (int e = 0; e < CW; e += 2) {
-          if constexpr (C::BANDS == 2) {
-            const float a = x[e] >= 0.0625f ? x[e] : 0.f, b = x[e + 1] >= 0.0625f ? x[e + 1] : 0.f;
-            hi[e / 2] = q4::pack2<true>(a, b);
-            lo[e / 2] = q4::pack2<true>((x[e] - a) * 0x1p18f, (x[e + 1] - b) * 0x1p18f);
-          } else {
-            hi[e / 2] = q4::pack2<C::FP16>(x[e], x[e + 1]);
+        for (int e = 0; e < CW / 2; ++e) l[e] = add_f2(l[e], y[e]);
+        if constexpr (C::Q4) {
+          if (whole) {
+            const uint64_t vm2 = pack_f2(vm, vm);
+#pragma unroll
+            for (int e = 0; e < CW / 2; ++e) {
+              off[e] = fma_f2(y[e], vm2, off[e]);
+              y[e] = mul_f2(y[e], vs2);
+            }
+          } else {  // s and m may be NaN: a row that does not see the key keeps clear of them
+#pragma unroll
+            for (int e = 0; e < CW; e += 2) {
+              const float2 w = unpack_f2(y[e / 2]), f = unpack_f2(off[e / 2]);
+              off[e / 2] = pack_f2(sees(e) ? fmaf(w.x, vm, f.x) : f.x, sees(e + 1) ? fmaf(w.y, vm, f.y) : f.y);
+              y[e / 2] = pack_f2(sees(e) ? w.x * vs : 0.f, sees(e + 1) ? w.y * vs : 0.f);
+            }
           }
         }
-        if (i >= C::NP) wait(&pv_done[i % C::NP], i / C::NP - 1);
+#pragma unroll
+        for (int e = 0; e < CW / 2; ++e) {
+          const float2 w = unpack_f2(y[e]);
+          if constexpr (C::BANDS == 2) {
+            const float a = w.x >= 0.0625f ? w.x : 0.f, b = w.y >= 0.0625f ? w.y : 0.f;
+            hi[e] = q4::pack2<true>(a, b);
+            lo[e] = q4::pack2<true>((w.x - a) * 0x1p18f, (w.y - b) * 0x1p18f);
+          } else {
+            hi[e] = q4::pack2<C::FP16>(w.x, w.y);
+          }
+        }
+        wait(pv_done + 8 * (i % C::NP), i / C::NP - 1);  // the buffer's last product is done
         uint8_t* pb = fixed + S::P + (i % C::NP) * C::BANDS * C::P_BYTES;
         const int swz = (key >> C::P_SWZ_SHIFT) & C::P_SWZ_MASK;
 #pragma unroll
@@ -1010,39 +1230,60 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         fence_proxy_async_smem();  // weights and zeroed V are read by the tensor core
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[i & 1]);
+        if (lane == 0) bar_arrive(p_full + 8 * (i & 1));
       }
       // ---- the task's statistics
-      wait(&o_free[ob], seq / C::OB - 1);
-      float* stat = reinterpret_cast<float*>(fixed + S::STAT + ob * S::STAT_BYTES);
-      const float sum = reduce_cols<CW, false>(l, lane);
-      if (lane < CW) stat[q4 * 64 + c0 + reduced_col<CW>(lane)] = sum;
-      if constexpr (C::Q4) {
-        const float o = reduce_cols<CW, false>(off, lane);
-        if (lane < CW) stat[256 + q4 * 64 + c0 + reduced_col<CW>(lane)] = o;
+      wait(o_free + 8 * ob, seq / C::OB - 1);
+      base += k.tiles;
+      float* stat = reinterpret_cast<float*>(fixed + S::STAT + (ob * C::ST + st) * S::STAT_BYTES);
+#pragma unroll
+      for (int which = 0; which < (C::Q4 ? 2 : 1); ++which) {
+#pragma unroll 1
+        for (int c = 0; c < CW; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < CW; e += 2) {
+            const float2 f = unpack_f2(which == 0 ? l[e / 2] : off[C::Q4 ? e / 2 : 0]);
+            if (e / 8 * 8 == c) {
+              v[e % 8] = f.x;
+              v[e % 8 + 1] = f.y;
+            }
+          }
+          const float sum = reduce_cols<8, false>(v, lane);
+          if (lane < 8) stat[256 * which + q4 * 64 + c0 + c + reduced_col<8>(lane)] = sum;
+        }
       }
-      if (gt < CW) stat[512 + c0 + gt] = s_ref[c0 + gt];
+      if (gt < CW) stat[512 + c0 + gt] = -s_ref[c0 + gt];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&st_full[ob]);
+      if (lane == 0) bar_arrive(st_full + 8 * ob);
     }
-  } else if (warp < C::W_V) {
-    // =================== 4-bit: K codes into tensor memory, one key a lane ===================
-    if constexpr (C::Q4) {
+    leave();
+    return;
+  }
+  if constexpr (C::Q4) {
+    int total = 0;
+#pragma unroll 1
+    for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
+    const int q4 = warp & 3, H = NS / 2;
+    const uint32_t quarter = (uint32_t)(q4 * 32) << 16;
+    Ring at;
+    if (warp < C::W_V) {
+      // =================== K codes into tensor memory, one key a lane ===================
       // A code c in the low bits of a 16-bit half is the fp16 number c 2^-24, four bits higher c 2^-20: masks are all
       // that it takes. A word of eight codes gives four columns, codes (0, 4), (1, 5), (2, 6), (3, 7), the second and the
       // fourth 16-fold.
-      const int q4 = warp & 3, key = q4 * 32 + lane;
-      int total = 0;
+      other_regs();
+      const int key = q4 * 32 + lane;
+      const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
 #pragma unroll 1
-      for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
       for (int i = 0; i < total; ++i) {
-        const int s = (i % (NS / 2)) * 2;
-        wait(&full[s], i / (NS / 2));
-        wait(&kd_free[i % C::KB], i / C::KB - 1);
+        const int s = at.slot * 2;
+        wait(full + 8 * s, at.round);
+        at.advance(1, H);
+        wait(kd_free + 8 * (i % C::KB), i / C::KB - 1);
         tc_fence_after();
         const uint8_t* row = ring + s * C::SLOT + key * (D / 2);
-        const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
-        const uint32_t dst = tmem + C::COL_K + (i % C::KB) * (D / 2) + ((uint32_t)(q4 * 32) << 16);
+        const uint32_t dst = tmem + C::COL_K + (i % C::KB) * (D / 2) + quarter;
 #pragma unroll 1
         for (int c = 0; c < D / 32; c += 2) {
           uint32_t v[32];
@@ -1052,82 +1293,82 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+              const uint32_t z = w[e] >> 8;
               v[16 * u + 4 * e] = w[e] & 0x000f000fu;
               v[16 * u + 4 * e + 1] = w[e] & 0x00f000f0u;
-              v[16 * u + 4 * e + 2] = (w[e] >> 8) & 0x000f000fu;
-              v[16 * u + 4 * e + 3] = (w[e] >> 8) & 0x00f000f0u;
+              v[16 * u + 4 * e + 2] = z & 0x000f000fu;
+              v[16 * u + 4 * e + 3] = z & 0x00f000f0u;
             }
           }
           tmem_st32(dst + c * 16, v);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) bar_arrive(empty + 8 * s);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&kd_full[i % C::KB]);
+        if (lane == 0) bar_arrive(kd_full + 8 * (i % C::KB));
       }
+      leave();
+      return;
     }
-  } else {
-    // =================== 4-bit: V codes into tensor memory, transposed ===================
-    if constexpr (C::Q4) {
-      // ldmatrix takes 16-bit halves, four codes of neighbouring head dims, and gives a thread those of two keys: the
-      // masks leave a pair of keys for each of four head dims. Head dim 4 g + j of 32 goes to lane 8 j + g. Codes are
-      // taken from 8, so that a weight's rounding meets at most 8 s.
-      const int q4 = warp & 3;
-      int total = 0;
+    // =================== V codes into tensor memory, transposed ===================
+    // ldmatrix takes 16-bit halves, four codes of neighbouring head dims, and gives a thread those of two keys: the
+    // masks leave a pair of keys for each of four head dims. Head dim 4 g + j of 32 goes to lane 8 j + g. Codes are
+    // taken from 8: the sums of the tensor core, which are cut, not rounded, stay near zero, and a weight's rounding
+    // meets at most 8 s.
+    other_regs();
+    if (q4 >= C::V_WARPS) {  // head dim 64: the upper lanes are not used
 #pragma unroll 1
-      for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
-      if (q4 >= C::V_WARPS) {  // head dim 64: the upper lanes are not used
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) {
-          const uint32_t z[32] = {};
-          tmem_st32(tmem + C::COL_V + kb * (TK / 2) + ((uint32_t)(q4 * 32) << 16), z);
-          tmem_st32(tmem + C::COL_V + kb * (TK / 2) + 32 + ((uint32_t)(q4 * 32) << 16), z);
-        }
-        tmem_wait_st();
+      for (int c = 0; c < C::KB * (TK / 2); c += 32) {
+        const uint32_t z[32] = {};
+        tmem_st32(tmem + C::COL_V + c + quarter, z);
       }
-      for (int i = 0; i < total; ++i) {
-        const int s = (i % (NS / 2)) * 2 + 1;
-        wait(&full[s], i / (NS / 2));
-        wait(&vd_free[i % C::KB], i / C::KB - 1);
-        tc_fence_after();
-        if (q4 < C::V_WARPS) {
-          const uint32_t base = ring_u32 + s * C::SLOT;
+      tmem_wait_st();
+    }
 #pragma unroll 1
-          for (int hh = 0; hh < C::HALVES; ++hh) {
-            const uint32_t dst = tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + ((uint32_t)(q4 * 32) << 16);
-#pragma unroll 2
-            for (int blk = 0; blk < TK / 32; ++blk) {
-              const int key = blk * 32 + lane, c = hh * 4 + q4;
-              const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
-              uint32_t r[4], a[8], b[8];
-              ldmatrix_x4_trans(base + key * (D / 2) + ((c ^ swz) << 4), r[0], r[1], r[2], r[3]);
+    for (int i = 0; i < total; ++i) {
+      const int s = at.slot * 2 + 1;
+      wait(full + 8 * s, at.round);
+      at.advance(1, H);
+      wait(vd_free + 8 * (i % C::KB), i / C::KB - 1);
+      tc_fence_after();
+      if (q4 < C::V_WARPS) {
+        const int swz = D == 64 ? (lane >> 2) & 1 : D == 128 ? (lane >> 1) & 3 : lane & 7;
+        const uint32_t from = ring_u32 + s * C::SLOT + lane * (D / 2);
+#pragma unroll 1
+        for (int hh = 0; hh < C::HALVES; ++hh) {
+          const uint32_t dst = tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + quarter;
+          const uint32_t src = from + (((hh * 4 + q4) ^ swz) << 4);
+          uint32_t r[4], next[4];
+          ldmatrix_x4_trans(src, next[0], next[1], next[2], next[3]);
+#pragma unroll 1
+          for (int blk = 0; blk < TK / 32; ++blk) {
+            uint32_t a[8], b[8];
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                a[2 * m] = hadd2(r[m] & 0x000f000fu, 0x80088008u);
-                a[2 * m + 1] = hadd2(r[m] & 0x00f000f0u, 0x80808080u);
-                b[2 * m] = hadd2((r[m] >> 8) & 0x000f000fu, 0x80088008u);
-                b[2 * m + 1] = hadd2((r[m] >> 8) & 0x00f000f0u, 0x80808080u);
-              }
-              tmem_st_16x128_x4(dst + blk * 16, a);
-              tmem_st_16x128_x4(dst + blk * 16 + (16u << 16), b);
+            for (int m = 0; m < 4; ++m) r[m] = next[m];
+            if (blk + 1 < TK / 32) ldmatrix_x4_trans(src + (blk + 1) * 32 * (D / 2), next[0], next[1], next[2], next[3]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t z = r[m] >> 8;
+              a[2 * m] = hadd2(r[m] & 0x000f000fu, 0x80088008u);
+              a[2 * m + 1] = hadd2(r[m] & 0x00f000f0u, 0x80808080u);
+              b[2 * m] = hadd2(z & 0x000f000fu, 0x80088008u);
+              b[2 * m + 1] = hadd2(z & 0x00f000f0u, 0x80808080u);
             }
+            tmem_st_16x128_x4(dst + blk * 16, a);
+            tmem_st_16x128_x4(dst + blk * 16 + (16u << 16), b);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&vd_full[i % C::KB]);
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(empty + 8 * s);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(vd_full + 8 * (i % C::KB));
     }
-  }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, C::ALLOC);
+    leave();
   }
 }
 

@@ -26,6 +26,10 @@ static int settings_of(int batch, Launch* l) {
   std::lock_guard<std::mutex> lock(memo.mu);
   if (memo.grid[dev] == 0) {
     int sms = 0, optin = 0;
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, window_attention_kernel<C>) != cudaSuccess) return SPEC_ERR_LAUNCH;
+    // the registers that are dealt out inside the kernel are those that the launch brings
+    if (C::DEAL && attr.numRegs < C::kLaunchRegs) return SPEC_ERR_LAUNCH;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
       return SPEC_ERR_LAUNCH;
