@@ -23,10 +23,10 @@ constexpr int kMaxBatch = 4096;
 constexpr int kMaxRows = 64;       // packed query rows of a unit
 constexpr int kMaxPieces = 768;    // pieces of cut units in a call
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
-constexpr int kParamSlots = 8;     // tiles of s and m in shared memory
 constexpr int kCandidates = 32;
 constexpr uint32_t kMaxTries = 500000;  // of a wait, 2 s
-constexpr int kBarEpi = 1, kBarEnd = 2, kBarGroup0 = 3;  // named barriers: the epilogue's warps, all at the end, each softmax warpgroup
+constexpr int kBarEpi = 1, kBarEnd = 2, kBarV = 3, kBarGroup0 = 4;  // named barriers: the epilogue's warps, all at the end,
+                                                           // those that unpack V, each softmax warpgroup
 constexpr float kUnseen = -3e38f;  // reference of a row that has seen no key
 static_assert(kMaxPieces / 2 * 4 <= SPEC_ATTN_COUNTER_BYTES, "a counter for every cut unit");
 
@@ -69,18 +69,21 @@ struct Cfg {
   static constexpr int BANDS = FP16 && !Q4 ? 2 : 1;
   static constexpr int QB = D == 256 && N == 64 ? 1 : 2;           // query buffers
   static constexpr int NP = D == 256 && N == 64 && BANDS == 2 ? 1 : 2;  // P buffers
-  static constexpr int KB = D == 256 ? 1 : 2;                      // 4-bit: unpacked K (and V) tiles in tensor memory
-  static constexpr int OPERANDS = Q4 ? KB * (D / 2 + HALVES * (TK / 2)) : 0;
+  static constexpr int VB = D == 256 && N > 16 ? 1 : 2;            // 4-bit: unpacked V tiles in tensor memory (K: 2)
+  static constexpr int OPERANDS = Q4 ? 2 * (D / 4) + VB * HALVES * (TK / 2) : 0;
   static constexpr int O_COLS = BANDS * HALVES * N;                 // of a stream
   static constexpr int OB = OPERANDS + 2 * N + 2 * ST * O_COLS <= 512 ? 2 : 1;  // tasks whose accumulators there is room for
-  static constexpr int COL_K = 0, COL_V = Q4 ? KB * (D / 2) : 0, COL_S = OPERANDS, COL_O = COL_S + 2 * N;
+  static constexpr int COL_K = 0, COL_V = Q4 ? 2 * (D / 4) : 0, COL_S = OPERANDS, COL_O = COL_S + 2 * N;
   static constexpr int COLS = COL_O + OB * ST * O_COLS;
   static constexpr int ALLOC = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
   // A ring of tiles, K and V in turns; those of head dim 256 in two parts of 128 head dims (16-bit).
   static constexpr int PARTS = D == 256 && !Q4 ? 2 : 1;
   static constexpr int SLOT = Q4 ? TK * D / 2 : TK * D * 2 / PARTS;
-  static constexpr int Q_BYTES = N * D * 2;
+  static constexpr int AHEAD = D == 256 ? 3 : 5;  // 4-bit: tiles that are copied ahead; a ring for K and one for V hold one more
+  // Queries: rows of 64 16-bit elements, D / 64 slices. 4-bit: of 128 8-bit ones, in three parts that add up to them.
+  static constexpr int Q_SLICES = D == 256 ? 2 : 1, Q_PART = Q_SLICES * N * 128;
+  static constexpr int Q_BYTES = Q4 ? 3 * Q_PART : N * D * 2;
   static constexpr int P_BYTES = N * TK * 2;
   // P is the operand B of the second product, MN-major: the N rows of a key are contiguous and swizzled at that width.
   static constexpr uint32_t P_LAYOUT = N == 16 ? 6u : (N == 32 ? 4u : 2u);
@@ -111,15 +114,14 @@ template <class C>
 struct Smem {
   static constexpr int Q = 0;
   static constexpr int P = Q + C::QB * C::Q_BYTES;
-  static constexpr int BARS = P + C::NP * C::BANDS * C::P_BYTES;  // 96 mbarriers
-  static constexpr int REF = BARS + 96 * 8;                       // [ST][64] minus the reference of each row
+  static constexpr int BARS = P + C::NP * C::BANDS * C::P_BYTES;  // 64 mbarriers
+  static constexpr int REF = BARS + 64 * 8;                       // [ST][64] minus the reference of each row
   static constexpr int ALPHA = REF + C::ST * 256;                 // [ST][64]
   static constexpr int RED = ALPHA + C::ST * 256;                 // [ST][4][64]
   static constexpr int STAT = RED + C::ST * 1024;                 // [OB][ST]: [4][64] sums, [4][64] offsets, [64] reference
   static constexpr int STAT_BYTES = 2048 + 256;
   static constexpr int QC = STAT + C::OB * C::ST * STAT_BYTES;    // [QB][2][64] factors of the scores
-  static constexpr int PAR = QC + C::QB * 512;                    // [kParamSlots][2][128] s and m of K and V
-  static constexpr int EPI = PAR + (C::Q4 ? kParamSlots * 1024 : 0);   // [64] int64 and three times [64] floats of the epilogue
+  static constexpr int EPI = QC + C::QB * 512;   // [64] int64 and three times [64] floats of the epilogue
   static constexpr int MISC = EPI + 1280;  // [64] plan, tensor-memory base, flags
   static constexpr int PREFIX = MISC + 256;
 };
@@ -148,12 +150,30 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(id), "r"(accumulate)
       : "memory");
 }
-using tattn::umma_ts;
+// The same with A in tensor memory, of 16-bit elements or of e4m3.
+template <bool F8>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t id, uint32_t accumulate) {
+  if constexpr (F8)
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        ".reg .b64 b;\n"
+        "elect.sync _|q, 0xffffffff;\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "mov.b64 b, {%2, %3};\n"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(id), "r"(accumulate)
+        : "memory");
+  else
+    tattn::umma_ts(d, a, b_lo, b_hi, id, accumulate);
+}
 template <bool FP16>
 __device__ __forceinline__ constexpr uint32_t mma_desc(int n, int a_mn, int b_mn) {
   return (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TK >> 4) << 24);
 }
+__device__ __forceinline__ constexpr uint32_t mma_desc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TK >> 4) << 24); }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
@@ -169,14 +189,6 @@ __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
-}
-// 4 bytes from global to shared memory, zeros with bytes = 0; the barrier gets one arrival of this thread once all its
-// copies so far are there.
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 // K or V rows of a head: box {64 elements, 1 head, rows} at {c0, head, row}; c0 a multiple of 8.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const void* map, int c0, int head, int row, uint32_t bar, uint64_t policy) {
@@ -266,6 +278,27 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Four fp32 as e4m3, the first in the low byte; what they lack of the originals is left in x.
+__device__ __forceinline__ uint32_t take_e4m3(float (&x)[4]) {
+  uint32_t r;
+  asm("{\n"
+      ".reg .b16 a, b;\n"
+      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n"
+      "mov.b32 %0, {a, b};\n"
+      "}\n"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f;  // two fp16
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(f) : "h"((uint16_t)(r >> (16 * h))));
+    const float2 v = q4::unpack2<true>(f);
+    x[2 * h] -= v.x;
+    x[2 * h + 1] -= v.y;
+  }
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
@@ -452,9 +485,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   // mbarriers, 8 bytes each
   const uint32_t full = fixed_u32 + S::BARS;        // [kMaxSlots] a tile has landed
   const uint32_t empty = full + 8 * kMaxSlots;      // [kMaxSlots] its slot may be filled again
-  const uint32_t par_full = empty + 8 * kMaxSlots;  // [kParamSlots] 4-bit: s and m of a tile
-  const uint32_t par_free = par_full + 8 * kParamSlots;
-  const uint32_t q_full = par_free + 8 * kParamSlots;  // [QB] queries and their factors written
+  const uint32_t q_full = empty + 8 * kMaxSlots;    // [QB] queries and their factors written
   const uint32_t kd_full = q_full + 16, kd_free = kd_full + 16;  // [KB] 4-bit: K unpacked
   const uint32_t vd_full = kd_free + 16, vd_free = vd_full + 16;  // [KB]
   const uint32_t s_full = vd_free + 16;    // [2] scores of a tile
@@ -463,7 +494,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   const uint32_t o_full = pv_done + 16;    // [OB] a task's accumulators are complete
   const uint32_t o_free = o_full + 16;     // [OB] and have been read, with the statistics
   const uint32_t st_full = o_free + 16;    // [OB] a task's statistics are written
-  static_assert(2 * kMaxSlots + 2 * kParamSlots + 22 <= 96, "barriers fit their area");
+  static_assert(2 * kMaxSlots + 22 <= 64, "barriers fit their area");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grid = (int)gridDim.x, me = (int)blockIdx.x;
@@ -492,13 +523,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   if (tid == 0) {
 #pragma unroll 1
     for (int s = 0; s < NS; ++s) {
-      bar_init(full + 8 * s, C::Q4 ? 32 : 1);
-      bar_init(empty + 8 * s, C::Q4 ? 4 : 1);
-    }
-#pragma unroll 1
-    for (int j = 0; j < kParamSlots; ++j) {
-      bar_init(par_full + 8 * j, 32);
-      bar_init(par_free + 8 * j, 4 * C::NG);
+      bar_init(full + 8 * s, 1);
+      bar_init(empty + 8 * s, 1);
     }
 #pragma unroll 1
     for (int j = 0; j < 16; j += 8) {
@@ -541,130 +567,68 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     if constexpr (C::DEAL) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
   };
 
+  // Page of entry l of the task's page list, -1 behind the task's end and where it is bad, which is noted.
+  const int bs = 1 << p.page_shift, ppt_shift = 7 - p.page_shift;  // pages of a tile: 2^ppt_shift
+  auto page_id = [&](const Task& k, int l, int seq) {
+    int id = -1;
+    if (l < min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift)) {
+      id = __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns));
+      if (id < 0 || (int64_t)id >= p.num_blocks) {
+        id = -1;
+        s_bad[seq & 31] = 1;
+      }
+    }
+    return id;
+  };
+
   // Each role has its own instruction for its registers, and its own end: where branches join, the compiler would hold all
   // that follows to the smaller number.
-  if (C::Q4 ? warp < C::W_EPI && warp != 1 : warp == 0) {
-    // =================== producers ===================
-    other_regs();
-    const int bs = 1 << p.page_shift, ppt = TK >> p.page_shift;
-    // 32 entries of the task's page list from entry l0 on, one a lane; -1 for those behind its end and for bad pages
-    auto page_ids = [&](const Task& k, int l0, int seq) {
-      const int l = l0 + lane;
-      int id = -1;
-      bool bad = false;
-      if (l < min(k.span.pages, (k.tile0 + k.tiles) * ppt)) {
-        id = __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns));
-        bad = id < 0 || (int64_t)id >= p.num_blocks;
-        if (bad) id = -1;
-      }
-      if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad[seq & 31] = 1;
-      return id;
-    };
+  if (!C::Q4 && warp == 0) {
+    // =================== 16-bit: K and V tiles by TMA ===================
+    // K and V that no other unit reads again are the first to leave L2
+    const uint64_t policy = p.groups == 1 ? l2_evict_first_policy() : l2_normal_policy();
     Ring at;
     int i = 0, seq = 0;
-    if constexpr (C::Q4) {
-      // One warp copies K, one V, with 16-byte cp.async: a tensor copy's rate goes by its rows, whose 64 bytes (head dim
-      // 128) are too few. Rows are swizzled so that both ways of reading a tile are free of bank conflicts. A third warp
-      // copies s and m of the keys.
-      constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte chunks of a row, rows a warp copies at once
-      const int w = warp == 0 ? 0 : 1, H = NS / 2, c = lane % CPR, r0 = lane / CPR;
-      const uint32_t row = (uint32_t)p.row;
-      const uint8_t* src = (w == 0 ? p.kpar : p.vpar) - (int64_t)p.kv_heads * (D / 2) + (uint64_t)r0 * row + c * 16;
 #pragma unroll 1
-      for (int t = me; t < tasks; t += grid, ++seq) {
-        const Task k = task_at(p, prefix, cut, t);
-        int win = -1, ids = 0;
-        if (lane == 0 && warp == 0) s_bad[seq & 31] = 0;
-        __syncwarp();
+    for (int t = me; t < tasks; t += grid, ++seq) {
+      const Task k = task_at(p, prefix, cut, t);
+      int win = -1, ids = 0;  // 32 entries of the page list, one a lane
 #pragma unroll 1
-        for (int j = 0; j < k.tiles; ++j, ++i) {
-          const int l0 = (k.tile0 + j) * ppt;
-          if (win < 0 || l0 >= win + 32) {
-            win = l0;
-            ids = page_ids(k, l0, seq);
-          }
-          if (warp == 3) {
-            const int s = i % kParamSlots;
-            wait(par_free + 8 * s, i / kParamSlots - 1);
-            if (tries == 1) break;
-            const uint32_t dst = fixed_u32 + S::PAR + s * 1024;
-#pragma unroll 1
-            for (int r = lane; r < TK; r += 32) {
-              const int id = __shfl_sync(0xffffffffu, ids, l0 - win + (r >> p.page_shift));
-              const uint32_t slot = ((uint32_t)max(id, 0) << p.page_shift) + (r & (bs - 1));
-              const uint64_t off = (uint64_t)slot * row + 4 * k.g;
-              cp_async_4(dst + r * 4, p.kpar + off, id < 0 ? 0 : 4);
-              cp_async_4(dst + 512 + r * 4, p.vpar + off, id < 0 ? 0 : 4);
-            }
-            cp_async_arrive(par_full + 8 * s);
-          } else {
-            const int s = at.slot * 2 + w;
-            wait(empty + 8 * s, at.round - 1);
-            at.advance(1, H);
-            if (tries == 1) break;
-#pragma unroll 1
-            for (int pc = 0; pc < ppt; ++pc) {
-              const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
-              const uint32_t dst = ring_u32 + s * C::SLOT + ((pc << p.page_shift) + r0) * (D / 2);
-              const uint8_t* from = src + (uint64_t)((uint32_t)max(id, 0) << p.page_shift) * row + k.g * (D / 2);
-#pragma unroll 2
-              for (int r = 0; r < bs; r += RPI) {
-                const int swz = D == 64 ? (r0 >> 2) & 1 : D == 128 ? (r0 >> 1) & 3 : (r0 + r) & 7;
-                cp_async_16(dst + r * (D / 2) + ((c ^ swz) << 4), from, id < 0 ? 0 : 16);
-                from += RPI * row;
-              }
-            }
-            cp_async_arrive(full + 8 * s);
-          }
+      for (int j = 0; j < k.tiles; ++j) {
+        const int l0 = (k.tile0 + j) << ppt_shift;
+        if (win < 0 || l0 >= win + 32) {
+          win = l0;
+          ids = page_id(k, l0 + lane, seq);
+          __syncwarp();
         }
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-    } else {
-      // K and V that no other unit reads again are the first to leave L2
-      const uint64_t policy = p.groups == 1 ? l2_evict_first_policy() : l2_normal_policy();
 #pragma unroll 1
-      for (int t = me; t < tasks; t += grid, ++seq) {
-        const Task k = task_at(p, prefix, cut, t);
-        int win = -1, ids = 0;
-        if (lane == 0) s_bad[seq & 31] = 0;
-        __syncwarp();
+        for (int w = 0; w < 2 * C::PARTS; ++w, ++i) {
+          const int s = at.slot;
+          wait(empty + 8 * s, at.round - 1);
+          if (tries == 1) break;
+          at.advance(1, NS);
+          if (lane == 0) bar_expect(full + 8 * s, (uint32_t)C::SLOT);
+          __syncwarp();
+          const CUtensorMap* map = w < C::PARTS ? &tm_k : &tm_v;
+          const int c0 = w % C::PARTS * 128;
 #pragma unroll 1
-        for (int j = 0; j < k.tiles; ++j) {
-          const int l0 = (k.tile0 + j) * ppt;
-          if (win < 0 || l0 >= win + 32) {
-            win = l0;
-            ids = page_ids(k, l0, seq);
-          }
-#pragma unroll 1
-          for (int w = 0; w < 2 * C::PARTS; ++w, ++i) {
-            const int s = at.slot;
-            wait(empty + 8 * s, at.round - 1);
-            if (tries == 1) break;
-            at.advance(1, NS);
-            if (lane == 0) bar_expect(full + 8 * s, (uint32_t)C::SLOT);
-            __syncwarp();
-            const CUtensorMap* map = w < C::PARTS ? &tm_k : &tm_v;
-            const int c0 = w % C::PARTS * 128;
-#pragma unroll 1
-            for (int pc = 0; pc < ppt; ++pc) {
-              const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
-              const int row = id < 0 ? -bs : id << p.page_shift;  // outside of the cache: zeros
-              if (lane == 0) {
+          for (int pc = 0; pc < 1 << ppt_shift; ++pc) {
+            const int id = __shfl_sync(0xffffffffu, ids, l0 - win + pc);
+            const int row = id < 0 ? -bs : id << p.page_shift;  // outside of the cache: zeros
+            if (lane == 0) {
 #pragma unroll
-                for (int sub = 0; sub < D / 64 / C::PARTS; ++sub)
-                  tma_rows(ring_u32 + s * C::SLOT + sub * TK * 128 + pc * bs * 128, map, c0 + sub * 64, k.g, row, full + 8 * s,
-                           policy);
-              }
+              for (int sub = 0; sub < D / 64 / C::PARTS; ++sub)
+                tma_rows(ring_u32 + s * C::SLOT + sub * TK * 128 + pc * bs * 128, map, c0 + sub * 64, k.g, row, full + 8 * s,
+                         policy);
             }
-            __syncwarp();
           }
+          __syncwarp();
         }
       }
-      if (tries == 1) {  // copies in flight still write here
-        uint32_t few = 1000;
-        for (int n = max(0, i - NS); n < i; ++n) bar_wait(full + 8 * (n % NS), (uint32_t)((n / NS) & 1), few);
-      }
+    }
+    if (tries == 1) {  // copies in flight still write here
+      uint32_t few = 1000;
+      for (int n = max(0, i - NS); n < i; ++n) bar_wait(full + 8 * (n % NS), (uint32_t)((n / NS) & 1), few);
     }
     leave();
     return;
@@ -672,7 +636,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   if (warp == 1) {
     // =================== MMA: scores of tile i + 1, then the product of tile i ===================
     other_regs();
-    const uint32_t id_qk = mma_desc<C::FP16>(N, 0, 0), id_pv = mma_desc<C::FP16>(N, C::Q4 ? 0 : 1, 1);
+    const uint32_t id_qk = C::Q4 ? mma_desc_e4m3(N) : mma_desc<C::FP16>(N, 0, 0), id_pv = mma_desc<C::FP16>(N, C::Q4 ? 0 : 1, 1);
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);          // K, Q: K-major
     const uint64_t vmn = smem_desc_sw128(0, TK * 128, 1024);     // V: MN-major
     const uint64_t pmn = smem_desc(0, 16, 16 * N, C::P_LAYOUT);  // P: MN-major, groups of 8 keys
@@ -681,7 +645,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     // moved to uniform registers for each.
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     const uint32_t tm = uniform(tmem);
-    const int n_slots = (int)uniform((uint32_t)NS), all = (int)uniform((uint32_t)tasks);
+    const int n_slots = (int)uniform((uint32_t)NS), all = (int)uniform((uint32_t)tasks), q_parts = p.fp16 ? 3 : 2;
     const uint32_t q_lo = uniform((uint32_t)kmaj + (q_u32 >> 4)), k_lo = uniform((uint32_t)kmaj + (ring_u32 >> 4));
     const uint32_t v_lo = uniform((uint32_t)vmn + (ring_u32 >> 4)), p_lo = uniform((uint32_t)pmn + (p_u32 >> 4));
     const uint32_t bars = uniform(full);
@@ -697,16 +661,19 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         wait(bar(q_full) + 8 * (q_seq % C::QB), q_seq / C::QB);
         const uint32_t qb = q_lo + (q_seq % C::QB) * (C::Q_BYTES >> 4), dst = tm + C::COL_S + (qi & 1) * N;
         if constexpr (C::Q4) {
-          wait(bar(kd_full) + 8 * (qi % C::KB), qi / C::KB);
+          wait(bar(kd_full) + 8 * (qi & 1), qi >> 1);
           tc_fence_after();
-          const uint32_t a = tm + C::COL_K + (qi % C::KB) * (D / 2);
+          const uint32_t a = tm + C::COL_K + (qi & 1) * (D / 4);
+          // bf16 queries are two e4m3 numbers, fp16 ones three; the small parts first
 #pragma unroll 1
-          for (int sl = 0; sl < D / 64; ++sl)
+          for (int part = q_parts - 1; part >= 0; --part) {
+            const uint32_t qp = qb + part * (C::Q_PART >> 4), fresh = part == q_parts - 1 ? 0u : 1u;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_ts(dst, a + sl * 32 + ks * 8, qb + sl * (N * 128 >> 4) + ks * 2, kq_hi, id_qk, sl + ks > 0 ? 1u : 0u);
+            for (int ks = 0; ks < D / 32; ++ks)
+              mma_ts<true>(dst, a + ks * 8, qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, ks > 0 ? 1u : fresh);
+          }
           mma_commit(bar(s_full) + 8 * (qi & 1));
-          mma_commit(bar(kd_free) + 8 * (qi % C::KB));
+          mma_commit(bar(kd_free) + 8 * (qi & 1));
         } else {
 #pragma unroll 1
           for (int part = 0; part < C::PARTS; ++part) {
@@ -736,19 +703,19 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         wait(bar(p_full) + 8 * (i & 1), i >> 1);
         const uint32_t pb = p_lo + (i % C::NP) * (C::BANDS * C::P_BYTES >> 4);
         if constexpr (C::Q4) {
-          wait(bar(vd_full) + 8 * (i % C::KB), i / C::KB);
+          wait(bar(vd_full) + 8 * (i % C::VB), i / C::VB);
           tc_fence_after();
 #pragma unroll 1
           for (int hh = 0; hh < C::HALVES; ++hh) {
-            const uint32_t a = tm + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2);
+            const uint32_t a = tm + C::COL_V + ((i % C::VB) * C::HALVES + hh) * (TK / 2);
 #pragma unroll 1
             for (int k4 = 0; k4 < 2; ++k4)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                umma_ts(o + hh * N, a + k4 * 32 + kk * 8, pb + (k4 * 4 + kk) * (32 * N >> 4), w_hi, id_pv, k4 + kk > 0 ? 1u : more);
+                mma_ts<false>(o + hh * N, a + k4 * 32 + kk * 8, pb + (k4 * 4 + kk) * (32 * N >> 4), w_hi, id_pv, k4 + kk > 0 ? 1u : more);
           }
           mma_commit(bar(pv_done) + 8 * (i % C::NP));
-          mma_commit(bar(vd_free) + 8 * (i % C::KB));
+          mma_commit(bar(vd_free) + 8 * (i % C::VB));
         } else {
 #pragma unroll 1
           for (int hh = 0; hh < C::HALVES; ++hh) {
@@ -811,8 +778,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         uint4 x = make_uint4(0, 0, 0, 0);
         if (r < k.nr) x = __ldg(reinterpret_cast<const uint4*>(p.q) + ((int64_t)k.b * p.rows * p.heads + row_of(k, r)) * L + c);
         if constexpr (C::Q4) {
-          // fp16 times a power of two that brings the row's largest element to [2^14, 2^15); the elements in the order and
-          // with the factors that the unpacking leaves the codes in (see there): 0 4 1 5 2 6 3 7, codes 1 3 5 7 16-fold
+          // The row times a power of two that brings its largest element to [2^7, 2^8), as a sum of e4m3 numbers (8 bits
+          // are two of them, 11 are three; what is below 2^-10 is lost), in the order that the unpacking leaves the codes
+          // in: 0 2 4 6 1 3 5 7.
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
           float f[8], top = 0.f, sum = 0.f;
 #pragma unroll
@@ -831,18 +799,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
           }
-          const int e2 = max(-100, min(140, 14 + 127 - (__float_as_int(top) >> 23)));
+          const int e2 = max(-100, min(133, 7 + 127 - (__float_as_int(top) >> 23)));
           const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
+          float even[4], odd4[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = f[e] * f1 * f2;
-          x = make_uint4(q4::pack2<true>(f[0], f[4]), q4::pack2<true>(f[1] * 0.0625f, f[5] * 0.0625f),
-                         q4::pack2<true>(f[2], f[6]), q4::pack2<true>(f[3] * 0.0625f, f[7] * 0.0625f));
+          for (int e = 0; e < 4; ++e) {
+            even[e] = f[2 * e] * f1 * f2;
+            odd4[e] = f[2 * e + 1] * f1 * f2;
+          }
+          uint8_t* to = dst + (c >> 4) * N * 128 + r * 128 + ((((c & 15) >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint32_t a = take_e4m3(even), b = take_e4m3(odd4);
+            *reinterpret_cast<uint2*>(to + part * C::Q_PART) = make_uint2(a, b);
+          }
           if (c == 0) {
-            qc[r] = pow2(max(-126, min(127, 24 - e2))) * p.scale_log2;
+            qc[r] = pow2(max(-126, min(127, 9 - e2))) * (top < INFINITY ? p.scale_log2 : NAN);
             qc[64 + r] = sum * p.scale_log2;
           }
         }
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * N * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+        if constexpr (!C::Q4) *reinterpret_cast<uint4*>(dst + (c >> 3) * N * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -869,7 +845,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if (bad && et == 0) raise_error(p.dev_err, SPEC_DEVERR_BLOCK_ID);
         const int only = C::ST == 2 && k.tiles == 1 ? base % C::ST : -1;  // the one stream that had a tile
         base += k.tiles;
-        named_sync(kBarEpi, 128);  // the last task's entries have been read
+        named_sync(kBarEpi, 128);  // the last task's entries have been read, and the flag
+        if (et == 0) s_bad[seq & 31] = 0;
         if (et < k.nr) {
           const float* stat = reinterpret_cast<const float*>(fixed + S::STAT + ob * C::ST * S::STAT_BYTES) + et;
           float sum[C::ST], ref = -INFINITY, total = 0.f, off = 0.f;
@@ -1011,7 +988,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     float* s_red = reinterpret_cast<float*>(fixed + S::RED) + st * 256;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const int key = q4 * 32 + lane;  // the lane of the scores that this thread reads
-    const int bs = 1 << p.page_shift, ppt_shift = 7 - p.page_shift;
     int base = 0, seq = 0;
 #pragma unroll 1
     for (int t = me; t < tasks; t += grid, ++seq) {
@@ -1024,8 +1000,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       for (int e = 0; e < (C::Q4 ? CW / 2 : 1); ++e) off[e] = 0;
       wait(q_full + 8 * (seq % C::QB), seq / C::QB);
       const float* qc = reinterpret_cast<const float*>(fixed + S::QC) + (seq % C::QB) * 128 + c0;
+      // 4-bit: s and m of this thread's key, fetched a tile of the stream ahead, and its page another one
+      auto page_of = [&](int j) { return page_id(k, ((k.tile0 + j) << ppt_shift) + (key >> p.page_shift), seq); };
+      auto fetch = [&](int id, uint32_t (&par)[2]) {
+        const uint64_t off = (uint64_t)(((uint32_t)max(id, 0) << p.page_shift) + (key & (bs - 1))) * (uint32_t)p.row + 4 * k.g;
+        par[0] = id < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(p.kpar + off));
+        par[1] = id < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(p.vpar + off));
+      };
+      const int j0 = C::ST == 2 ? (base ^ st) & 1 : 0;
+      int id = -1;
+      uint32_t par[2];
+      if constexpr (C::Q4) {
+        fetch(page_of(j0), par);
+        id = page_of(j0 + C::ST);
+      }
 #pragma unroll 1
-      for (int j = C::ST == 2 ? (base ^ st) & 1 : 0; j < k.tiles; j += C::ST) {
+      for (int j = j0; j < k.tiles; j += C::ST) {
         const int i = base + j;  // of stream i % ST
         // ---- which rows see this thread's key: [r_lo, r_hi); most tiles are seen whole by all
         const int l0 = (k.tile0 + j) << ppt_shift;
@@ -1047,18 +1037,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         auto sees = [&](int e) { return c0 + e >= r_lo && c0 + e < r_hi; };
         float ks = p.scale_log2, km = 0.f, vs = 1.f, vm = 0.f;
         if constexpr (C::Q4) {
-          const int s = i % kParamSlots;
-          wait(par_full + 8 * s, i / kParamSlots);
-          const uint32_t* par = reinterpret_cast<const uint32_t*>(fixed + S::PAR + s * 1024);
-          const uint32_t a = dead ? 0u : par[key], b = dead ? 0u : par[128 + key];
+          const uint32_t a = dead ? 0u : par[0], b = dead ? 0u : par[1];
           const float2 x = p.fp16 ? q4::unpack2<true>(a) : q4::unpack2<false>(a);
           const float2 y = p.fp16 ? q4::unpack2<true>(b) : q4::unpack2<false>(b);
           ks = x.x;
           km = x.y;
           vs = y.x;
           vm = fmaf(8.f, y.x, y.y);  // the codes of V are taken from 8
-          __syncwarp();
-          if (lane == 0) bar_arrive(par_free + 8 * s);
+          fetch(id, par);
+          id = page_of(j + 2 * C::ST);
         }
         wait(s_full + 8 * (i & 1), i >> 1);
         tc_fence_after();
@@ -1261,113 +1248,167 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     return;
   }
   if constexpr (C::Q4) {
-    int total = 0;
-#pragma unroll 1
-    for (int t = me; t < tasks; t += grid) total += task_at(p, prefix, cut, t).tiles;
-    const int q4 = warp & 3, H = NS / 2;
+    // =================== 4-bit: codes from the cache into tensor memory ===================
+    // Each warp copies the rows of 32 keys with 16-byte cp.async, H tiles ahead (a tensor copy's rate goes by its rows,
+    // whose 64 bytes at head dim 128 are too few). Rows are swizzled so that both ways of reading a tile are free of bank
+    // conflicts.
+    other_regs();
+    constexpr int H = C::AHEAD + 1;
+    const int q4 = warp & 3;
+    const bool is_k = warp < C::W_V;
     const uint32_t quarter = (uint32_t)(q4 * 32) << 16;
-    Ring at;
-    if (warp < C::W_V) {
-      // =================== K codes into tensor memory, one key a lane ===================
-      // A code c in the low bits of a 16-bit half is the fp16 number c 2^-24, four bits higher c 2^-20: masks are all
-      // that it takes. A word of eight codes gives four columns, codes (0, 4), (1, 5), (2, 6), (3, 7), the second and the
-      // fourth 16-fold.
-      other_regs();
+    constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte chunks of a row, rows a warp copies at once
+    const int c = lane % CPR, r0 = lane / CPR;
+    const uint32_t row = (uint32_t)p.row;
+    const uint8_t* src = (is_k ? p.kpar : p.vpar) - (int64_t)p.kv_heads * (D / 2) + c * 16;
+    const uint32_t mine = ring_u32 + (is_k ? 0 : H * C::SLOT);
+    const uint8_t* mine_ptr = ring + (is_k ? 0 : H * C::SLOT);
+    // The tile that is copied next: entries [l, end) of the task's page list are left, which are those of `table`, from
+    // entry ns on `skip` further on.
+    int t = me, seq = -1, to = 0, l = 0, end = 0, ns = 0, skip = 0, id = -1;
+    const int32_t* table = nullptr;
+    const uint8_t* head = src;
+    const int mine_l = bs < 32 ? 2 * q4 + (lane >> 4) : (q4 * 32) >> p.page_shift;  // this lane's page in a tile
+    auto next = [&]() {  // its page
+      if (l >= end && t < tasks) {
+        const Task k = task_at(p, prefix, cut, t);
+        table = p.block_table + (int64_t)k.b * p.max_blocks;
+        head = src + k.g * (D / 2);
+        l = k.tile0 << ppt_shift;
+        end = min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift);
+        ns = k.span.ns;
+        skip = k.span.wp - ns;
+        t += grid;
+        ++seq;
+      }
+      id = -1;
+      const int e = l + mine_l;
+      if (e < end) {
+        id = __ldg(table + (e < ns ? e : e + skip));
+        if (id < 0 || (int64_t)id >= p.num_blocks) {
+          id = -1;
+          s_bad[seq & 31] = 1;
+        }
+      }
+    };
+    auto copy = [&]() {
+      if (l < end) {
+        const uint32_t dst = mine + to * C::SLOT + (q4 * 32 + r0) * (D / 2);
+        const int page[2] = {__shfl_sync(0xffffffffu, id, 0), __shfl_sync(0xffffffffu, id, 16)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // 16 rows
+          const uint32_t slot = ((uint32_t)max(page[half], 0) << p.page_shift) + ((q4 * 32 + half * 16 + r0) & (bs - 1));
+          const uint8_t* from = head + (uint64_t)slot * row;
+#pragma unroll
+          for (int r = 0; r < 16; r += RPI) {
+            const int swz = D == 64 ? (r0 >> 2) & 1 : D == 128 ? (r0 >> 1) & 3 : (r0 + r) & 7;
+            cp_async_16(dst + (half * 16 + r) * (D / 2) + ((c ^ swz) << 4), from + r * row, page[half] < 0 ? 0 : 16);
+          }
+        }
+        if (++to == H) to = 0;
+        l += 1 << ppt_shift;
+        next();
+      }
+      cp_async_commit();
+    };
+    next();
+    int total = 0, at = 0;
+#pragma unroll 1
+    for (int x = me; x < tasks; x += grid) total += task_at(p, prefix, cut, x).tiles;
+#pragma unroll 1
+    for (int x = 0; x < C::AHEAD; ++x) copy();
+    if (is_k) {
+      // ---- K, one key a lane. A code c in a byte is the e4m3 number c 2^-9, the subnormal ones and those above alike: a
+      // word of eight codes gives two columns, codes 0 2 4 6 and 1 3 5 7, for a mask each. The queries are split instead
+      // of K being made wider.
       const int key = q4 * 32 + lane;
       const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
 #pragma unroll 1
       for (int i = 0; i < total; ++i) {
-        const int s = at.slot * 2;
-        wait(full + 8 * s, at.round);
-        at.advance(1, H);
-        wait(kd_free + 8 * (i % C::KB), i / C::KB - 1);
+        cp_async_wait<C::AHEAD - 1>();
+        __syncwarp();
+        wait(kd_free + 8 * (i & 1), (i >> 1) - 1);
         tc_fence_after();
-        const uint8_t* row = ring + s * C::SLOT + key * (D / 2);
-        const uint32_t dst = tmem + C::COL_K + (i % C::KB) * (D / 2) + quarter;
+        const uint8_t* from = mine_ptr + at * C::SLOT + key * (D / 2);
+        const uint32_t dst = tmem + C::COL_K + (i & 1) * (D / 4) + quarter;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; c += 2) {
-          uint32_t v[32];
+        for (int x = 0; x < D / 32; x += 2) {
+          uint32_t v[16];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row + (((c + u) ^ swz) << 4));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint4 q = *reinterpret_cast<const uint4*>(from + (((x + u) ^ swz) << 4));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t z = w[e] >> 8;
-              v[16 * u + 4 * e] = w[e] & 0x000f000fu;
-              v[16 * u + 4 * e + 1] = w[e] & 0x00f000f0u;
-              v[16 * u + 4 * e + 2] = z & 0x000f000fu;
-              v[16 * u + 4 * e + 3] = z & 0x00f000f0u;
+              v[8 * u + 2 * e] = w[e] & 0x0f0f0f0fu;
+              v[8 * u + 2 * e + 1] = (w[e] >> 4) & 0x0f0f0f0fu;
             }
           }
-          tmem_st32(dst + c * 16, v);
+          tattn::tmem_st16u(dst + x * 8, v);
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(empty + 8 * s);
+        if (++at == H) at = 0;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(kd_full + 8 * (i % C::KB));
+        if (lane == 0) bar_arrive(kd_full + 8 * (i & 1));
+        copy();
       }
-      leave();
-      return;
-    }
-    // =================== V codes into tensor memory, transposed ===================
-    // ldmatrix takes 16-bit halves, four codes of neighbouring head dims, and gives a thread those of two keys: the
-    // masks leave a pair of keys for each of four head dims. Head dim 4 g + j of 32 goes to lane 8 j + g. Codes are
-    // taken from 8: the sums of the tensor core, which are cut, not rounded, stay near zero, and a weight's rounding
-    // meets at most 8 s.
-    other_regs();
-    if (q4 >= C::V_WARPS) {  // head dim 64: the upper lanes are not used
+    } else {
+      // ---- V, transposed. ldmatrix takes 16-bit halves, four codes of neighbouring head dims, and gives a thread those of
+      // two keys: the masks leave a pair of keys for each of four head dims. Head dim 4 g + j of 32 goes to lane 8 j + g.
+      // Codes are taken from 8: the sums of the tensor core, which are cut, not rounded, stay near zero, and a weight's
+      // rounding meets at most 8 s.
+      if (q4 >= C::V_WARPS) {  // head dim 64: the upper lanes are not used
 #pragma unroll 1
-      for (int c = 0; c < C::KB * (TK / 2); c += 32) {
-        const uint32_t z[32] = {};
-        tmem_st32(tmem + C::COL_V + c + quarter, z);
+        for (int x = 0; x < C::VB * (TK / 2); x += 32) {
+          const uint32_t z[32] = {};
+          tmem_st32(tmem + C::COL_V + x + quarter, z);
+        }
+        tmem_wait_st();
       }
-      tmem_wait_st();
-    }
+      const int swz = D == 64 ? (lane >> 2) & 1 : D == 128 ? (lane >> 1) & 3 : lane & 7;
 #pragma unroll 1
-    for (int i = 0; i < total; ++i) {
-      const int s = at.slot * 2 + 1;
-      wait(full + 8 * s, at.round);
-      at.advance(1, H);
-      wait(vd_free + 8 * (i % C::KB), i / C::KB - 1);
-      tc_fence_after();
-      if (q4 < C::V_WARPS) {
-        const int swz = D == 64 ? (lane >> 2) & 1 : D == 128 ? (lane >> 1) & 3 : lane & 7;
-        const uint32_t from = ring_u32 + s * C::SLOT + lane * (D / 2);
+      for (int i = 0; i < total; ++i) {
+        cp_async_wait<C::AHEAD - 1>();
+        named_sync(kBarV, 128);  // all four warps' rows are there, and the last tile has been read
+        copy();
+        wait(vd_free + 8 * (i % C::VB), i / C::VB - 1);
+        tc_fence_after();
+        if (q4 < C::V_WARPS) {
+          const uint32_t from = mine + at * C::SLOT + lane * (D / 2);
 #pragma unroll 1
-        for (int hh = 0; hh < C::HALVES; ++hh) {
-          const uint32_t dst = tmem + C::COL_V + ((i % C::KB) * C::HALVES + hh) * (TK / 2) + quarter;
-          const uint32_t src = from + (((hh * 4 + q4) ^ swz) << 4);
-          uint32_t r[4], next[4];
-          ldmatrix_x4_trans(src, next[0], next[1], next[2], next[3]);
+          for (int hh = 0; hh < C::HALVES; ++hh) {
+            const uint32_t dst = tmem + C::COL_V + ((i % C::VB) * C::HALVES + hh) * (TK / 2) + quarter;
+            const uint32_t m0 = from + (((hh * 4 + q4) ^ swz) << 4);
+            uint32_t r[4], next[4];
+            ldmatrix_x4_trans(m0, next[0], next[1], next[2], next[3]);
 #pragma unroll 1
-          for (int blk = 0; blk < TK / 32; ++blk) {
-            uint32_t a[8], b[8];
+            for (int blk = 0; blk < TK / 32; ++blk) {
+              uint32_t a[8], b[8];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) r[m] = next[m];
-            if (blk + 1 < TK / 32) ldmatrix_x4_trans(src + (blk + 1) * 32 * (D / 2), next[0], next[1], next[2], next[3]);
+              for (int m = 0; m < 4; ++m) r[m] = next[m];
+              if (blk + 1 < TK / 32) ldmatrix_x4_trans(m0 + (blk + 1) * 32 * (D / 2), next[0], next[1], next[2], next[3]);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const uint32_t z = r[m] >> 8;
-              a[2 * m] = hadd2(r[m] & 0x000f000fu, 0x80088008u);
-              a[2 * m + 1] = hadd2(r[m] & 0x00f000f0u, 0x80808080u);
-              b[2 * m] = hadd2(z & 0x000f000fu, 0x80088008u);
-              b[2 * m + 1] = hadd2(z & 0x00f000f0u, 0x80808080u);
+              for (int m = 0; m < 4; ++m) {
+                const uint32_t z = r[m] >> 8;
+                a[2 * m] = hadd2(r[m] & 0x000f000fu, 0x80088008u);
+                a[2 * m + 1] = hadd2(r[m] & 0x00f000f0u, 0x80808080u);
+                b[2 * m] = hadd2(z & 0x000f000fu, 0x80088008u);
+                b[2 * m + 1] = hadd2(z & 0x00f000f0u, 0x80808080u);
+              }
+              tmem_st_16x128_x4(dst + blk * 16, a);
+              tmem_st_16x128_x4(dst + blk * 16 + (16u << 16), b);
             }
-            tmem_st_16x128_x4(dst + blk * 16, a);
-            tmem_st_16x128_x4(dst + blk * 16 + (16u << 16), b);
           }
         }
+        if (++at == H) at = 0;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(vd_full + 8 * (i % C::VB));
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(empty + 8 * s);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(vd_full + 8 * (i % C::KB));
     }
+    cp_async_wait<0>();
     leave();
   }
 }
