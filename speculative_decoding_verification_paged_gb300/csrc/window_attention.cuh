@@ -25,7 +25,7 @@ constexpr int kMaxPieces = 768;    // pieces of cut units in a call
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
 constexpr int kCandidates = 32;
 constexpr uint32_t kMaxTries = 500000;  // of a wait, 2 s
-constexpr int kBarEpi = 1, kBarEnd = 2, kBarV = 3, kBarGroup0 = 4;  // named barriers: the epilogue's warps, all at the end,
+constexpr int kBarEpi = 1, kBarEnd = 2, kBarV = 3, kBarGroup0 = 5;  // named barriers: the epilogue's warps, all at the end,
                                                            // those that unpack V, each softmax warpgroup
 constexpr float kUnseen = -3e38f;  // reference of a row that has seen no key
 static_assert(kMaxPieces / 2 * 4 <= SPEC_ATTN_COUNTER_BYTES, "a counter for every cut unit");
@@ -46,7 +46,7 @@ struct Params {
   int by_gqa;       // 2^16 / gqa, rounded up: r / gqa = r * by_gqa >> 16 for r < 64
   int npt, groups;  // query rows of a unit (its npt * gqa packed rows), units per kv head
   int page_shift, max_blocks, window, sinks;
-  int slots;  // depth of the ring
+  int slots;  // tiles (or parts of one) that fit the ring
   int fp16;   // type of q and out (4-bit: and of s and m)
   float scale_log2;
 };
@@ -59,7 +59,8 @@ struct Cfg {
   static constexpr int N = ROWS < 16 ? 16 : ROWS;
   // Softmax: ST streams, which take the tiles in turns and have an accumulator, references and sums of their own (a tile
   // is a long chain of steps for its warps), with NG warpgroups each, ROWS / NG rows of a tile.
-  static constexpr int ST = Q4 && ROWS <= 32 ? 2 : 1;
+  static constexpr int UG = ROWS <= 32 ? 2 : 1;  // 4-bit: groups of four warps that unpack K (and V), taking the tiles in turns
+  static constexpr int ST = Q4 && ROWS <= 16 ? 2 : 1;
   static constexpr int NG = ROWS <= 16 ? 1 : ROWS / 16;
   static constexpr int CW = ROWS / NG;
   static constexpr int CHUNK = CW > 8 && Q4 && ROWS > 16 ? 8 : CW;  // scores that a softmax thread holds at once (registers)
@@ -69,7 +70,7 @@ struct Cfg {
   static constexpr int BANDS = FP16 && !Q4 ? 2 : 1;
   static constexpr int QB = D == 256 && N == 64 ? 1 : 2;           // query buffers
   static constexpr int NP = D == 256 && N == 64 && BANDS == 2 ? 1 : 2;  // P buffers
-  static constexpr int VB = D == 256 && N > 16 ? 1 : 2;            // 4-bit: unpacked V tiles in tensor memory (K: 2)
+  static constexpr int VB = D == 256 && N == 64 ? 1 : 2;           // 4-bit: unpacked V tiles in tensor memory (K: 2)
   static constexpr int OPERANDS = Q4 ? 2 * (D / 4) + VB * HALVES * (TK / 2) : 0;
   static constexpr int O_COLS = BANDS * HALVES * N;                 // of a stream
   static constexpr int OB = OPERANDS + 2 * N + 2 * ST * O_COLS <= 512 ? 2 : 1;  // tasks whose accumulators there is room for
@@ -77,10 +78,12 @@ struct Cfg {
   static constexpr int COLS = COL_O + OB * ST * O_COLS;
   static constexpr int ALLOC = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
-  // A ring of tiles, K and V in turns; those of head dim 256 in two parts of 128 head dims (16-bit).
+  // Tiles in shared memory; those of head dim 256 in two parts of 128 head dims (16-bit).
   static constexpr int PARTS = D == 256 && !Q4 ? 2 : 1;
   static constexpr int SLOT = Q4 ? TK * D / 2 : TK * D * 2 / PARTS;
-  static constexpr int AHEAD = D == 256 ? 3 : 5;  // 4-bit: tiles that are copied ahead; a ring for K and one for V hold one more
+  // 4-bit: tiles that a group copies ahead; its ring holds one more.
+  static constexpr int AHEAD = D == 256 ? 3 / UG : UG == 2 ? 3 : 5;
+  static constexpr int RINGS = 2 * UG * (AHEAD + 1);
   // Queries: rows of 64 16-bit elements, D / 64 slices. 4-bit: of 128 8-bit ones, in three parts that add up to them.
   static constexpr int Q_SLICES = D == 256 ? 2 : 1, Q_PART = Q_SLICES * N * 128;
   static constexpr int Q_BYTES = Q4 ? 3 * Q_PART : N * D * 2;
@@ -89,15 +92,15 @@ struct Cfg {
   static constexpr uint32_t P_LAYOUT = N == 16 ? 6u : (N == 32 ? 4u : 2u);
   static constexpr int P_SWZ_SHIFT = N == 16 ? 2 : (N == 32 ? 1 : 0);
   static constexpr int P_SWZ_MASK = N == 16 ? 1 : (N == 32 ? 3 : 7);
-  static constexpr int W_EPI = 4, W_SOFT = 8, W_K = W_SOFT + 4 * NG * ST, W_V = W_K + 4;  // first warps of the roles
-  static constexpr int kWarps = Q4 ? W_V + 4 : W_K;
+  static constexpr int W_EPI = 4, W_SOFT = 8, W_K = W_SOFT + 4 * NG * ST, W_V = W_K + 4 * UG;  // first warps of the roles
+  static constexpr int kWarps = Q4 ? W_V + 4 * UG : W_K;
   static constexpr int kThreads = 32 * kWarps;
-  // Registers a thread of the softmax and of the other roles, where they are dealt out anew: 24 warps are launched with
-  // 80, 32 with 64.
+  // Registers a thread of the softmax and of the other roles, where they are dealt out anew: 32 warps are launched with 64.
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kOtherRegs = kWarps == 24 ? 64 : 48, kSoftRegs = kWarps == 24 ? 112 : 80;
-  static constexpr bool DEAL = Q4 && kWarps >= 24;
+  static constexpr int kOtherRegs = 48, kSoftRegs = NG * ST == 4 ? 80 : NG * ST == 2 ? 112 : 160;
+  static constexpr bool DEAL = Q4;
   static_assert(!DEAL || 4 * NG * ST * kSoftRegs + (kWarps - 4 * NG * ST) * kOtherRegs <= kWarps * kLaunchRegs, "registers");
+  static_assert(!Q4 || kWarps == 32, "");
   static_assert(ST == 1 || NP == 2, "a stream has a P buffer of its own");
   static constexpr int V_WARPS = D / 32 < 4 ? D / 32 : 4;  // 4-bit: warps that unpack V, 32 head dims each (and a half)
   // What a task's start and end, a join, and a piece of it cost, in tiles (us over the us of a tile at the measured copy
@@ -474,7 +477,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   using S = Smem<C>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int NS = p.slots;
+  // 16-bit: KS slots for K, the others for V, so that a barrier's phases are all waited for by one warp, in turn (the
+  // parity of a phase says nothing to a warp that has not seen the phase before)
+  const int NS = p.slots, KS = NS - NS / 2;
   uint8_t* ring = smem;
   uint8_t* fixed = ring + (size_t)NS * C::SLOT;
   const uint32_t ring_u32 = smem_u32(ring), fixed_u32 = smem_u32(fixed);
@@ -567,18 +572,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     if constexpr (C::DEAL) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
   };
 
-  // Page of entry l of the task's page list, -1 behind the task's end and where it is bad, which is noted.
+  // Entry l of a task's page list, -1 behind the task's end; and whether it is a page, noted where it is not. A call of its
+  // own, so that the entry can be on its way while other work is done.
   const int bs = 1 << p.page_shift, ppt_shift = 7 - p.page_shift;  // pages of a tile: 2^ppt_shift
-  auto page_id = [&](const Task& k, int l, int seq) {
-    int id = -1;
-    if (l < min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift)) {
-      id = __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns));
-      if (id < 0 || (int64_t)id >= p.num_blocks) {
-        id = -1;
-        s_bad[seq & 31] = 1;
-      }
-    }
-    return id;
+  auto entry = [&](const Task& k, int l) {
+    return l < min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift)
+               ? __ldg(p.block_table + (int64_t)k.b * p.max_blocks + (l < k.span.ns ? l : k.span.wp + l - k.span.ns))
+               : -1;
+  };
+  auto checked = [&](int id, bool there, int seq) {
+    const bool ok = id >= 0 && (int64_t)id < p.num_blocks;
+    if (there && !ok) s_bad[seq & 31] = 1;
+    return ok ? id : -1;
   };
 
   // Each role has its own instruction for its registers, and its own end: where branches join, the compiler would hold all
@@ -587,8 +592,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     // =================== 16-bit: K and V tiles by TMA ===================
     // K and V that no other unit reads again are the first to leave L2
     const uint64_t policy = p.groups == 1 ? l2_evict_first_policy() : l2_normal_policy();
-    Ring at;
-    int i = 0, seq = 0;
+    Ring at[2];  // K's and V's
+    int seq = 0;
 #pragma unroll 1
     for (int t = me; t < tasks; t += grid, ++seq) {
       const Task k = task_at(p, prefix, cut, t);
@@ -598,18 +603,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         const int l0 = (k.tile0 + j) << ppt_shift;
         if (win < 0 || l0 >= win + 32) {
           win = l0;
-          ids = page_id(k, l0 + lane, seq);
+          ids = checked(entry(k, l0 + lane), l0 + lane < min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift), seq);
           __syncwarp();
         }
 #pragma unroll 1
-        for (int w = 0; w < 2 * C::PARTS; ++w, ++i) {
-          const int s = at.slot;
-          wait(empty + 8 * s, at.round - 1);
+        for (int w = 0; w < 2 * C::PARTS; ++w) {
+          const bool v = w >= C::PARTS;
+          const int s = v ? KS + at[1].slot : at[0].slot;
+          wait(empty + 8 * s, (v ? at[1].round : at[0].round) - 1);
           if (tries == 1) break;
-          at.advance(1, NS);
+          if (v) at[1].advance(1, NS - KS);
+          else at[0].advance(1, KS);
           if (lane == 0) bar_expect(full + 8 * s, (uint32_t)C::SLOT);
           __syncwarp();
-          const CUtensorMap* map = w < C::PARTS ? &tm_k : &tm_v;
+          const CUtensorMap* map = v ? &tm_v : &tm_k;
           const int c0 = w % C::PARTS * 128;
 #pragma unroll 1
           for (int pc = 0; pc < 1 << ppt_shift; ++pc) {
@@ -628,13 +635,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     }
     if (tries == 1) {  // copies in flight still write here
       uint32_t few = 1000;
-      for (int n = max(0, i - NS); n < i; ++n) bar_wait(full + 8 * (n % NS), (uint32_t)((n / NS) & 1), few);
+      for (int s = 0; s < NS; ++s) {
+        const Ring& x = at[s < KS ? 0 : 1];
+        const int copied = x.round + ((s < KS ? s : s - KS) < x.slot ? 1 : 0);
+        if (copied > 0) bar_wait(full + 8 * s, (uint32_t)((copied - 1) & 1), few);
+      }
     }
     leave();
     return;
   }
-  if (warp == 1) {
-    // =================== MMA: scores of tile i + 1, then the product of tile i ===================
+  if (warp == 1 || warp == 2) {
+    // =================== MMA: one warp issues the scores, one the products ===================
     other_regs();
     const uint32_t id_qk = C::Q4 ? mma_desc_e4m3(N) : mma_desc<C::FP16>(N, 0, 0), id_pv = mma_desc<C::FP16>(N, C::Q4 ? 0 : 1, 1);
     const uint64_t kmaj = smem_desc_sw128(0, 16, 1024);          // K, Q: K-major
@@ -645,103 +656,96 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     // moved to uniform registers for each.
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     const uint32_t tm = uniform(tmem);
-    const int n_slots = (int)uniform((uint32_t)NS), all = (int)uniform((uint32_t)tasks), q_parts = p.fp16 ? 3 : 2;
+    const int n_slots = (int)uniform((uint32_t)(warp == 2 ? NS - KS : KS)), all = (int)uniform((uint32_t)tasks), q_parts = p.fp16 ? 3 : 2;
     const uint32_t q_lo = uniform((uint32_t)kmaj + (q_u32 >> 4)), k_lo = uniform((uint32_t)kmaj + (ring_u32 >> 4));
     const uint32_t v_lo = uniform((uint32_t)vmn + (ring_u32 >> 4)), p_lo = uniform((uint32_t)pmn + (p_u32 >> 4));
     const uint32_t bars = uniform(full);
     auto bar = [&](uint32_t b) { return bars + (b - full); };
     auto tiles_at = [&](int t) { return (int)uniform((uint32_t)task_at(p, prefix, cut, t).tiles); };
-    int qt = me, q_left = tiles_at(me), q_seq = 0, qi = 0;  // the next tile of scores
-    Ring k_at, v_at;                                        // 16-bit: slots of its K, and of the next product's V
-    v_at.advance(C::PARTS, n_slots);
-    int t = me, seq = 0, tiles = q_left, j = -1;  // tile j of task t is next for the second product; -1: scores first
+    Ring at;  // 16-bit: the slot of the next K (V)
+    const int first_slot = warp == 2 ? (int)uniform((uint32_t)KS) : 0;
+    int i = 0, seq = 0;
 #pragma unroll 1
-    for (int i = -1; t < all && tries != 1; ++i) {
-      if (qt < all) {
-        wait(bar(q_full) + 8 * (q_seq % C::QB), q_seq / C::QB);
-        const uint32_t qb = q_lo + (q_seq % C::QB) * (C::Q_BYTES >> 4), dst = tm + C::COL_S + (qi & 1) * N;
-        if constexpr (C::Q4) {
-          wait(bar(kd_full) + 8 * (qi & 1), qi >> 1);
-          tc_fence_after();
-          const uint32_t a = tm + C::COL_K + (qi & 1) * (D / 4);
-          // bf16 queries are two e4m3 numbers, fp16 ones three; the small parts first
+    for (int t = me; t < all; t += grid, ++seq) {
+      const int tiles = tiles_at(t);
 #pragma unroll 1
-          for (int part = q_parts - 1; part >= 0; --part) {
-            const uint32_t qp = qb + part * (C::Q_PART >> 4), fresh = part == q_parts - 1 ? 0u : 1u;
-#pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-              mma_ts<true>(dst, a + ks * 8, qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, ks > 0 ? 1u : fresh);
-          }
-          mma_commit(bar(s_full) + 8 * (qi & 1));
-          mma_commit(bar(kd_free) + 8 * (qi & 1));
-        } else {
-#pragma unroll 1
-          for (int part = 0; part < C::PARTS; ++part) {
-            wait(bar(full) + 8 * k_at.slot, k_at.round);
+      for (int j = 0; j < tiles && tries != 1; ++j, ++i) {
+        if (warp == 1) {
+          wait(bar(p_full) + 8 * (i & 1), (i >> 1) - 1);  // the scores of tile i - 2 have been read
+          wait(bar(q_full) + 8 * (seq % C::QB), seq / C::QB);
+          const uint32_t qb = q_lo + (seq % C::QB) * (C::Q_BYTES >> 4), dst = tm + C::COL_S + (i & 1) * N;
+          if constexpr (C::Q4) {
+            wait(bar(kd_full) + 8 * (i & 1), i >> 1);
             tc_fence_after();
-            const uint32_t kb = k_lo + k_at.slot * (C::SLOT >> 4), qp = qb + part * (N * 256 >> 4);
-#pragma unroll
-            for (int ks = 0; ks < D / 16 / C::PARTS; ++ks)
-              mma_ss(dst, kb + (((ks >> 2) * TK * 128 + (ks & 3) * 32) >> 4), kq_hi,
-                     qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, part + ks > 0 ? 1u : 0u);
-            mma_commit(bar(empty) + 8 * k_at.slot);
-            k_at.advance(1, n_slots);
-          }
-          mma_commit(bar(s_full) + 8 * (qi & 1));
-          k_at.advance(C::PARTS, n_slots);
-        }
-        ++qi;
-        if (--q_left == 0) {
-          qt += grid;
-          ++q_seq;
-          if (qt < all) q_left = tiles_at(qt);
-        }
-      }
-      if (j >= 0) {
-        const uint32_t o = tm + C::COL_O + ((seq % C::OB) * C::ST + i % C::ST) * C::O_COLS, more = j >= C::ST ? 1u : 0u;
-        if (j == 0) wait(bar(o_free) + 8 * (seq % C::OB), seq / C::OB - 1);
-        wait(bar(p_full) + 8 * (i & 1), i >> 1);
-        const uint32_t pb = p_lo + (i % C::NP) * (C::BANDS * C::P_BYTES >> 4);
-        if constexpr (C::Q4) {
-          wait(bar(vd_full) + 8 * (i % C::VB), i / C::VB);
-          tc_fence_after();
+            const uint32_t a = tm + C::COL_K + (i & 1) * (D / 4);
+            // bf16 queries are two e4m3 numbers, fp16 ones three; the small parts first
 #pragma unroll 1
-          for (int hh = 0; hh < C::HALVES; ++hh) {
-            const uint32_t a = tm + C::COL_V + ((i % C::VB) * C::HALVES + hh) * (TK / 2);
-#pragma unroll 1
-            for (int k4 = 0; k4 < 2; ++k4)
+            for (int part = q_parts - 1; part >= 0; --part) {
+              const uint32_t qp = qb + part * (C::Q_PART >> 4), fresh = part == q_parts - 1 ? 0u : 1u;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts<false>(o + hh * N, a + k4 * 32 + kk * 8, pb + (k4 * 4 + kk) * (32 * N >> 4), w_hi, id_pv, k4 + kk > 0 ? 1u : more);
+              for (int ks = 0; ks < D / 32; ++ks)
+                mma_ts<true>(dst, a + ks * 8, qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, ks > 0 ? 1u : fresh);
+            }
+            mma_commit(bar(s_full) + 8 * (i & 1));
+            mma_commit(bar(kd_free) + 8 * (i & 1));
+          } else {
+#pragma unroll 1
+            for (int part = 0; part < C::PARTS; ++part) {
+              wait(bar(full) + 8 * (first_slot + at.slot), at.round);
+              tc_fence_after();
+              const uint32_t kb = k_lo + (first_slot + at.slot) * (C::SLOT >> 4), qp = qb + part * (N * 256 >> 4);
+#pragma unroll
+              for (int ks = 0; ks < D / 16 / C::PARTS; ++ks)
+                mma_ss(dst, kb + (((ks >> 2) * TK * 128 + (ks & 3) * 32) >> 4), kq_hi,
+                       qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, part + ks > 0 ? 1u : 0u);
+              mma_commit(bar(empty) + 8 * (first_slot + at.slot));
+              at.advance(1, n_slots);
+            }
+            mma_commit(bar(s_full) + 8 * (i & 1));
           }
-          mma_commit(bar(pv_done) + 8 * (i % C::NP));
-          mma_commit(bar(vd_free) + 8 * (i % C::VB));
         } else {
-#pragma unroll 1
-          for (int hh = 0; hh < C::HALVES; ++hh) {
-            wait(bar(full) + 8 * v_at.slot, v_at.round);
+          const uint32_t o = tm + C::COL_O + ((seq % C::OB) * C::ST + i % C::ST) * C::O_COLS, more = j >= C::ST ? 1u : 0u;
+          if (j == 0) wait(bar(o_free) + 8 * (seq % C::OB), seq / C::OB - 1);
+          wait(bar(p_full) + 8 * (i & 1), i >> 1);
+          const uint32_t pb = p_lo + (i % C::NP) * (C::BANDS * C::P_BYTES >> 4);
+          if constexpr (C::Q4) {
+            wait(bar(vd_full) + 8 * (i % C::VB), i / C::VB);
             tc_fence_after();
-            const uint32_t vb = v_lo + v_at.slot * (C::SLOT >> 4);
 #pragma unroll 1
-            for (int band = 0; band < C::BANDS; ++band)
+            for (int hh = 0; hh < C::HALVES; ++hh) {
+              const uint32_t a = tm + C::COL_V + ((i % C::VB) * C::HALVES + hh) * (TK / 2);
+#pragma unroll 1
+              for (int k4 = 0; k4 < 2; ++k4)
 #pragma unroll
-              for (int kk = 0; kk < TK / 16; ++kk)
-                mma_ss(o + (band * C::HALVES + hh) * N, vb + (kk * 2048 >> 4), v_hi, pb + ((band * C::P_BYTES + kk * 32 * N) >> 4),
-                       w_hi, id_pv, kk > 0 ? 1u : more);
-            mma_commit(bar(empty) + 8 * v_at.slot);
-            v_at.advance(1, n_slots);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ts<false>(o + hh * N, a + k4 * 32 + kk * 8, pb + (k4 * 4 + kk) * (32 * N >> 4), w_hi, id_pv, k4 + kk > 0 ? 1u : more);
+            }
+            mma_commit(bar(pv_done) + 8 * (i % C::NP));
+            mma_commit(bar(vd_free) + 8 * (i % C::VB));
+          } else {
+#pragma unroll 1
+            for (int hh = 0; hh < C::HALVES; ++hh) {
+              wait(bar(full) + 8 * (first_slot + at.slot), at.round);
+              tc_fence_after();
+              const uint32_t vb = v_lo + (first_slot + at.slot) * (C::SLOT >> 4);
+#pragma unroll 1
+              for (int band = 0; band < C::BANDS; ++band)
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                  mma_ss(o + (band * C::HALVES + hh) * N, vb + (kk * 2048 >> 4), v_hi, pb + ((band * C::P_BYTES + kk * 32 * N) >> 4),
+                         w_hi, id_pv, kk > 0 ? 1u : more);
+              mma_commit(bar(empty) + 8 * (first_slot + at.slot));
+              at.advance(1, n_slots);
+            }
+            mma_commit(bar(pv_done) + 8 * (i % C::NP));
           }
-          mma_commit(bar(pv_done) + 8 * (i % C::NP));
-          v_at.advance(C::PARTS, n_slots);
+          if (j == tiles - 1) mma_commit(bar(o_full) + 8 * (seq % C::OB));
         }
-        if (j == tiles - 1) mma_commit(bar(o_full) + 8 * (seq % C::OB));
       }
-      if (++j == tiles) {
-        j = 0;
-        ++seq;
-        t += grid;
-        if (t < all) tiles = tiles_at(t);
-      }
+    }
+    if (warp == 2) {
+      leave();
+      return;
     }
     if (tries == 1) raise_error(p.dev_err, SPEC_DEVERR_TIMEOUT);
     __syncwarp();
@@ -1001,11 +1005,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       wait(q_full + 8 * (seq % C::QB), seq / C::QB);
       const float* qc = reinterpret_cast<const float*>(fixed + S::QC) + (seq % C::QB) * 128 + c0;
       // 4-bit: s and m of this thread's key, fetched a tile of the stream ahead, and its page another one
-      auto page_of = [&](int j) { return page_id(k, ((k.tile0 + j) << ppt_shift) + (key >> p.page_shift), seq); };
-      auto fetch = [&](int id, uint32_t (&par)[2]) {
-        const uint64_t off = (uint64_t)(((uint32_t)max(id, 0) << p.page_shift) + (key & (bs - 1))) * (uint32_t)p.row + 4 * k.g;
-        par[0] = id < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(p.kpar + off));
-        par[1] = id < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(p.vpar + off));
+      auto page_of = [&](int j) { return entry(k, ((k.tile0 + j) << ppt_shift) + (key >> p.page_shift)); };
+      auto fetch = [&](int id, uint32_t (&par)[2]) {  // bad pages are noted by those who copy the codes
+        const bool ok = id >= 0 && (int64_t)id < p.num_blocks;
+        const uint64_t off = (uint64_t)(((uint32_t)(ok ? id : 0) << p.page_shift) + (key & (bs - 1))) * (uint32_t)p.row + 4 * k.g;
+        par[0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(p.kpar + off)) : 0u;
+        par[1] = ok ? __ldg(reinterpret_cast<const uint32_t*>(p.vpar + off)) : 0u;
       };
       const int j0 = C::ST == 2 ? (base ^ st) & 1 : 0;
       int id = -1;
@@ -1157,13 +1162,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if constexpr (!C::Q4) {
           // slots that no row sees may hold anything: zero their V
           if (__any_sync(0xffffffffu, dead)) {
-            // In a short ring what the tile's V replaces may be the V of the tile before, which may not have landed: the
-            // barrier's parity would then name an earlier phase. That tile's product says that it has.
-            if (NS < 3 * C::PARTS && i > 0) wait(pv_done + 8 * ((i - 1) % C::NP), (i - 1) / C::NP);
+            // What the tile's V replaces in the ring may not have landed yet: the barrier's parity would then name an
+            // earlier phase. The product of the tile before says that it has.
+            if (i > 0) wait(pv_done + 8 * ((i - 1) % C::NP), (i - 1) / C::NP);
 #pragma unroll 1
             for (int part = 0; part < C::PARTS; ++part) {
-              const int n = (2 * i + 1) * C::PARTS + part, s = n % NS;
-              wait(full + 8 * s, n / NS);
+              const int n = i * C::PARTS + part, s = KS + n % (NS - KS);
+              wait(full + 8 * s, n / (NS - KS));
               if (dead) {
                 uint8_t* v = ring + s * C::SLOT + key * 128;
                 for (int c = h; c < D / 8 / C::PARTS; c += C::NG)
@@ -1253,48 +1258,48 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     // whose 64 bytes at head dim 128 are too few). Rows are swizzled so that both ways of reading a tile are free of bank
     // conflicts.
     other_regs();
-    constexpr int H = C::AHEAD + 1;
-    const int q4 = warp & 3;
+    constexpr int H = C::AHEAD + 1, UG = C::UG;
+    const int q4 = warp & 3, group = ((warp - C::W_K) >> 2) % UG;  // tiles i with i % UG == group
     const bool is_k = warp < C::W_V;
     const uint32_t quarter = (uint32_t)(q4 * 32) << 16;
     constexpr int CPR = D / 32, RPI = 32 / CPR;  // 16-byte chunks of a row, rows a warp copies at once
     const int c = lane % CPR, r0 = lane / CPR;
     const uint32_t row = (uint32_t)p.row;
     const uint8_t* src = (is_k ? p.kpar : p.vpar) - (int64_t)p.kv_heads * (D / 2) + c * 16;
-    const uint32_t mine = ring_u32 + (is_k ? 0 : H * C::SLOT);
-    const uint8_t* mine_ptr = ring + (is_k ? 0 : H * C::SLOT);
-    // The tile that is copied next: entries [l, end) of the task's page list are left, which are those of `table`, from
-    // entry ns on `skip` further on.
-    int t = me, seq = -1, to = 0, l = 0, end = 0, ns = 0, skip = 0, id = -1;
+    const uint32_t my_ring = ((is_k ? 0 : UG) + group) * H * C::SLOT, mine = ring_u32 + my_ring;
+    const uint8_t* mine_ptr = ring + my_ring;
+    // The tile that is copied next: tile j of a task whose page list is that of `table`, up to entry `end`, entries ns and
+    // on `skip` further on.
+    int t = me - grid, seq = -1, to = 0, j = group, tiles = 0, l0 = 0, end = 0, ns = 0, skip = 0, id = -1;
+    bool there = false;
     const int32_t* table = nullptr;
     const uint8_t* head = src;
     const int mine_l = bs < 32 ? 2 * q4 + (lane >> 4) : (q4 * 32) >> p.page_shift;  // this lane's page in a tile
     auto next = [&]() {  // its page
-      if (l >= end && t < tasks) {
+      while (j >= tiles && t < tasks) {
+        j -= tiles;
+        t += grid;
+        ++seq;
+        tiles = 0;
+        if (t >= tasks) break;
         const Task k = task_at(p, prefix, cut, t);
         table = p.block_table + (int64_t)k.b * p.max_blocks;
         head = src + k.g * (D / 2);
-        l = k.tile0 << ppt_shift;
+        tiles = k.tiles;
+        l0 = k.tile0 << ppt_shift;
         end = min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift);
         ns = k.span.ns;
         skip = k.span.wp - ns;
-        t += grid;
-        ++seq;
       }
-      id = -1;
-      const int e = l + mine_l;
-      if (e < end) {
-        id = __ldg(table + (e < ns ? e : e + skip));
-        if (id < 0 || (int64_t)id >= p.num_blocks) {
-          id = -1;
-          s_bad[seq & 31] = 1;
-        }
-      }
+      const int e = l0 + (j << ppt_shift) + mine_l;
+      there = t < tasks && e < end;
+      id = there ? __ldg(table + (e < ns ? e : e + skip)) : -1;
     };
     auto copy = [&]() {
-      if (l < end) {
+      if (t < tasks) {
         const uint32_t dst = mine + to * C::SLOT + (q4 * 32 + r0) * (D / 2);
-        const int page[2] = {__shfl_sync(0xffffffffu, id, 0), __shfl_sync(0xffffffffu, id, 16)};
+        const int good = checked(id, there, seq);
+        const int page[2] = {__shfl_sync(0xffffffffu, good, 0), __shfl_sync(0xffffffffu, good, 16)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // 16 rows
           const uint32_t slot = ((uint32_t)max(page[half], 0) << p.page_shift) + ((q4 * 32 + half * 16 + r0) & (bs - 1));
@@ -1306,7 +1311,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           }
         }
         if (++to == H) to = 0;
-        l += 1 << ppt_shift;
+        j += UG;
         next();
       }
       cp_async_commit();
@@ -1324,7 +1329,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       const int key = q4 * 32 + lane;
       const int swz = D == 64 ? (key >> 2) & 1 : D == 128 ? (key >> 1) & 3 : key & 7;
 #pragma unroll 1
-      for (int i = 0; i < total; ++i) {
+      for (int i = group; i < total; i += UG) {
         cp_async_wait<C::AHEAD - 1>();
         __syncwarp();
         wait(kd_free + 8 * (i & 1), (i >> 1) - 1);
@@ -1358,23 +1363,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       // two keys: the masks leave a pair of keys for each of four head dims. Head dim 4 g + j of 32 goes to lane 8 j + g.
       // Codes are taken from 8: the sums of the tensor core, which are cut, not rounded, stay near zero, and a weight's
       // rounding meets at most 8 s.
-      if (q4 >= C::V_WARPS) {  // head dim 64: the upper lanes are not used
-#pragma unroll 1
-        for (int x = 0; x < C::VB * (TK / 2); x += 32) {
-          const uint32_t z[32] = {};
-          tmem_st32(tmem + C::COL_V + x + quarter, z);
-        }
-        tmem_wait_st();
-      }
       const int swz = D == 64 ? (lane >> 2) & 1 : D == 128 ? (lane >> 1) & 3 : lane & 7;
 #pragma unroll 1
-      for (int i = 0; i < total; ++i) {
+      for (int i = group; i < total; i += UG) {
         cp_async_wait<C::AHEAD - 1>();
-        named_sync(kBarV, 128);  // all four warps' rows are there, and the last tile has been read
+        named_sync(kBarV + group, 128);  // all four warps' rows are there, and the last tile has been read
         copy();
         wait(vd_free + 8 * (i % C::VB), i / C::VB - 1);
         tc_fence_after();
-        if (q4 < C::V_WARPS) {
+        if (q4 < C::V_WARPS) {  // head dim 64: the upper lanes hold anything, and so do those of the results
           const uint32_t from = mine + at * C::SLOT + lane * (D / 2);
 #pragma unroll 1
           for (int hh = 0; hh < C::HALVES; ++hh) {

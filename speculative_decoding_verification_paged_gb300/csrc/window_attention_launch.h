@@ -38,7 +38,7 @@ static int settings_of(int batch, Launch* l) {
   }
   const size_t fixed = smem_fixed<C>(batch), room = memo.granted[dev];
   const size_t fit = fixed < room ? (room - fixed) / C::SLOT : 0;
-  const int least = C::Q4 ? 2 * (C::AHEAD + 1) : 2 * C::PARTS, most = C::Q4 ? least : kMaxSlots;
+  const int least = C::Q4 ? C::RINGS : 2 * C::PARTS, most = C::Q4 ? least : kMaxSlots;
   if (fit < (size_t)least) return SPEC_ERR_UNSUPPORTED;
   l->slots = fit > (size_t)most ? most : (int)fit;
   l->smem = fixed + (size_t)l->slots * C::SLOT;
