@@ -24,6 +24,7 @@ constexpr int kMaxRows = 64;       // packed query rows of a unit
 constexpr int kMaxPieces = 768;    // pieces of cut units in a call
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
 constexpr int kCandidates = 32;
+constexpr int kPageSlots = 8;      // 4-bit: tiles whose pages, s and m are in shared memory
 constexpr uint32_t kMaxTries = 500000;  // of a wait, 2 s
 constexpr int kBarEpi = 1, kBarEnd = 2, kBarV = 3, kBarGroup0 = 5;  // named barriers: the epilogue's warps, all at the end,
                                                            // those that unpack V, each softmax warpgroup
@@ -73,8 +74,9 @@ struct Cfg {
   static constexpr int VB = D == 256 && N == 64 ? 1 : 2;           // 4-bit: unpacked V tiles in tensor memory (K: 2)
   static constexpr int OPERANDS = Q4 ? 2 * (D / 4) + VB * HALVES * (TK / 2) : 0;
   static constexpr int O_COLS = BANDS * HALVES * N;                 // of a stream
-  static constexpr int OB = OPERANDS + 2 * N + 2 * ST * O_COLS <= 512 ? 2 : 1;  // tasks whose accumulators there is room for
-  static constexpr int COL_K = 0, COL_V = Q4 ? 2 * (D / 4) : 0, COL_S = OPERANDS, COL_O = COL_S + 2 * N;
+  static constexpr int SB = 2 * ST;                                // scores of tiles
+  static constexpr int OB = OPERANDS + SB * N + 2 * ST * O_COLS <= 512 ? 2 : 1;  // tasks whose accumulators there is room for
+  static constexpr int COL_K = 0, COL_V = Q4 ? 2 * (D / 4) : 0, COL_S = OPERANDS, COL_O = COL_S + SB * N;
   static constexpr int COLS = COL_O + OB * ST * O_COLS;
   static constexpr int ALLOC = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
@@ -117,14 +119,16 @@ template <class C>
 struct Smem {
   static constexpr int Q = 0;
   static constexpr int P = Q + C::QB * C::Q_BYTES;
-  static constexpr int BARS = P + C::NP * C::BANDS * C::P_BYTES;  // 64 mbarriers
-  static constexpr int REF = BARS + 64 * 8;                       // [ST][64] minus the reference of each row
+  static constexpr int BARS = P + C::NP * C::BANDS * C::P_BYTES;  // 96 mbarriers
+  static constexpr int REF = BARS + 96 * 8;                       // [ST][64] minus the reference of each row
   static constexpr int ALPHA = REF + C::ST * 256;                 // [ST][64]
   static constexpr int RED = ALPHA + C::ST * 256;                 // [ST][4][64]
   static constexpr int STAT = RED + C::ST * 1024;                 // [OB][ST]: [4][64] sums, [4][64] offsets, [64] reference
   static constexpr int STAT_BYTES = 2048 + 256;
   static constexpr int QC = STAT + C::OB * C::ST * STAT_BYTES;    // [QB][2][64] factors of the scores
-  static constexpr int EPI = QC + C::QB * 512;   // [64] int64 and three times [64] floats of the epilogue
+  static constexpr int PAGES = QC + C::QB * 512;                  // [kPageSlots]: [8] pages of a tile, kv head
+  static constexpr int PAR = PAGES + (C::Q4 ? kPageSlots * 48 : 0);    // [kPageSlots][2][128] s and m of K and V
+  static constexpr int EPI = PAR + (C::Q4 ? kPageSlots * 1024 : 0);   // [64] int64 and three times [64] floats of the epilogue
   static constexpr int MISC = EPI + 1280;  // [64] plan, tensor-memory base, flags
   static constexpr int PREFIX = MISC + 256;
 };
@@ -192,6 +196,14 @@ __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t taddr, const uint32_t
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+// 4 bytes from global to shared memory, zeros with bytes = 0; the barrier gets one arrival of this thread once all its
+// copies so far are there.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 // K or V rows of a head: box {64 elements, 1 head, rows} at {c0, head, row}; c0 a multiple of 8.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const void* map, int c0, int head, int row, uint32_t bar, uint64_t policy) {
@@ -493,13 +505,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   const uint32_t q_full = empty + 8 * kMaxSlots;    // [QB] queries and their factors written
   const uint32_t kd_full = q_full + 16, kd_free = kd_full + 16;  // [KB] 4-bit: K unpacked
   const uint32_t vd_full = kd_free + 16, vd_free = vd_full + 16;  // [KB]
-  const uint32_t s_full = vd_free + 16;    // [2] scores of a tile
-  const uint32_t p_full = s_full + 16;     // [2] weights of a tile written
+  const uint32_t s_full = vd_free + 16;    // [SB] scores of a tile
+  const uint32_t s_free = s_full + 32;     // [SB] and their buffer may be written again
+  const uint32_t p_full = s_free + 32;     // [2] weights of a tile written
   const uint32_t pv_done = p_full + 16;    // [NP] second product of the tile that used the P buffer is complete
   const uint32_t o_full = pv_done + 16;    // [OB] a task's accumulators are complete
   const uint32_t o_free = o_full + 16;     // [OB] and have been read, with the statistics
   const uint32_t st_full = o_free + 16;    // [OB] a task's statistics are written
-  static_assert(2 * kMaxSlots + 22 <= 64, "barriers fit their area");
+  const uint32_t pg_full = st_full + 16;   // [kPageSlots] 4-bit: pages of a tile are there
+  const uint32_t par_full = pg_full + 8 * kPageSlots;   // [kPageSlots] its s and m
+  const uint32_t par_free = par_full + 8 * kPageSlots;  // [kPageSlots] they (and the pages) have been read
+  static_assert(2 * kMaxSlots + 28 + 3 * kPageSlots <= 96, "barriers fit their area");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grid = (int)gridDim.x, me = (int)blockIdx.x;
@@ -532,13 +548,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       bar_init(empty + 8 * s, 1);
     }
 #pragma unroll 1
+    for (int j = 0; j < kPageSlots; ++j) {
+      bar_init(pg_full + 8 * j, 1);
+      bar_init(par_full + 8 * j, 32);
+      bar_init(par_free + 8 * j, 4 * C::NG);
+    }
+#pragma unroll 1
     for (int j = 0; j < 16; j += 8) {
       bar_init(q_full + j, 4);
       bar_init(kd_full + j, 4);
       bar_init(kd_free + j, 1);
       bar_init(vd_full + j, 4);
       bar_init(vd_free + j, 1);
-      bar_init(s_full + j, 1);
+      bar_init(s_full + 2 * j, 1);
+      bar_init(s_full + 2 * j + 8, 1);
+      bar_init(s_free + 2 * j, 4 * C::NG);
+      bar_init(s_free + 2 * j + 8, 4 * C::NG);
       bar_init(p_full + j, 4 * C::NG);
       bar_init(pv_done + j, 1);
       bar_init(o_full + j, 1);
@@ -671,9 +696,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
 #pragma unroll 1
       for (int j = 0; j < tiles && tries != 1; ++j, ++i) {
         if (warp == 1) {
-          wait(bar(p_full) + 8 * (i & 1), (i >> 1) - 1);  // the scores of tile i - 2 have been read
+          wait(bar(s_free) + 8 * (i % C::SB), i / C::SB - 1);
           wait(bar(q_full) + 8 * (seq % C::QB), seq / C::QB);
-          const uint32_t qb = q_lo + (seq % C::QB) * (C::Q_BYTES >> 4), dst = tm + C::COL_S + (i & 1) * N;
+          const uint32_t qb = q_lo + (seq % C::QB) * (C::Q_BYTES >> 4), dst = tm + C::COL_S + (i % C::SB) * N;
           if constexpr (C::Q4) {
             wait(bar(kd_full) + 8 * (i & 1), i >> 1);
             tc_fence_after();
@@ -686,7 +711,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
               for (int ks = 0; ks < D / 32; ++ks)
                 mma_ts<true>(dst, a + ks * 8, qp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), kq_hi, id_qk, ks > 0 ? 1u : fresh);
             }
-            mma_commit(bar(s_full) + 8 * (i & 1));
+            mma_commit(bar(s_full) + 8 * (i % C::SB));
             mma_commit(bar(kd_free) + 8 * (i & 1));
           } else {
 #pragma unroll 1
@@ -701,7 +726,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
               mma_commit(bar(empty) + 8 * (first_slot + at.slot));
               at.advance(1, n_slots);
             }
-            mma_commit(bar(s_full) + 8 * (i & 1));
+            mma_commit(bar(s_full) + 8 * (i % C::SB));
           }
         } else {
           const uint32_t o = tm + C::COL_O + ((seq % C::OB) * C::ST + i % C::ST) * C::O_COLS, more = j >= C::ST ? 1u : 0u;
@@ -756,6 +781,44 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
   }
   if (warp < C::W_EPI) {
     other_regs();
+    if (C::Q4 && warp == 3) {
+      // =================== 4-bit: the tiles' pages, and s and m of their keys ===================
+      // That s and m of a tile have been read says that its codes have been copied, by its pages: the unpacking comes first.
+      const uint32_t row = (uint32_t)p.row;
+      int n = 0, seq = 0;
+#pragma unroll 1
+      for (int t = me; t < tasks; t += grid, ++seq) {
+        const Task k = task_at(p, prefix, cut, t);
+        int win = -1, ids = 0;  // 32 entries of the page list, one a lane
+#pragma unroll 1
+        for (int j = 0; j < k.tiles && tries != 1; ++j, ++n) {
+          const int l0 = (k.tile0 + j) << ppt_shift, s = n % kPageSlots;
+          if (win < 0 || l0 >= win + 32) {
+            win = l0;
+            ids = checked(entry(k, l0 + lane), l0 + lane < min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift), seq);
+          }
+          wait(par_free + 8 * s, n / kPageSlots - 1);
+          int32_t* pages = reinterpret_cast<int32_t*>(fixed + S::PAGES + s * 48);
+          const int id = __shfl_sync(0xffffffffu, ids, l0 - win + (lane & ((1 << ppt_shift) - 1)));
+          if (lane < 8) pages[lane] = id;
+          if (lane == 8) pages[8] = k.g;
+          __syncwarp();
+          if (lane == 0) bar_arrive(pg_full + 8 * s);
+          const uint32_t dst = fixed_u32 + S::PAR + s * 1024;
+#pragma unroll 2
+          for (int r = lane; r < TK; r += 32) {
+            const int page = __shfl_sync(0xffffffffu, ids, l0 - win + (r >> p.page_shift));
+            const uint32_t slot = ((uint32_t)max(page, 0) << p.page_shift) + (r & (bs - 1));
+            const uint64_t off = (uint64_t)slot * row + 4 * k.g;
+            cp_async_4(dst + r * 4, p.kpar + off, page < 0 ? 0 : 4);
+            cp_async_4(dst + 512 + r * 4, p.vpar + off, page < 0 ? 0 : 4);
+          }
+          cp_async_arrive(par_full + 8 * s);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+    }
     leave();
     return;
   }
@@ -1004,21 +1067,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
       for (int e = 0; e < (C::Q4 ? CW / 2 : 1); ++e) off[e] = 0;
       wait(q_full + 8 * (seq % C::QB), seq / C::QB);
       const float* qc = reinterpret_cast<const float*>(fixed + S::QC) + (seq % C::QB) * 128 + c0;
-      // 4-bit: s and m of this thread's key, fetched a tile of the stream ahead, and its page another one
-      auto page_of = [&](int j) { return entry(k, ((k.tile0 + j) << ppt_shift) + (key >> p.page_shift)); };
-      auto fetch = [&](int id, uint32_t (&par)[2]) {  // bad pages are noted by those who copy the codes
-        const bool ok = id >= 0 && (int64_t)id < p.num_blocks;
-        const uint64_t off = (uint64_t)(((uint32_t)(ok ? id : 0) << p.page_shift) + (key & (bs - 1))) * (uint32_t)p.row + 4 * k.g;
-        par[0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(p.kpar + off)) : 0u;
-        par[1] = ok ? __ldg(reinterpret_cast<const uint32_t*>(p.vpar + off)) : 0u;
-      };
       const int j0 = C::ST == 2 ? (base ^ st) & 1 : 0;
-      int id = -1;
-      uint32_t par[2];
-      if constexpr (C::Q4) {
-        fetch(page_of(j0), par);
-        id = page_of(j0 + C::ST);
-      }
 #pragma unroll 1
       for (int j = j0; j < k.tiles; j += C::ST) {
         const int i = base + j;  // of stream i % ST
@@ -1042,19 +1091,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         auto sees = [&](int e) { return c0 + e >= r_lo && c0 + e < r_hi; };
         float ks = p.scale_log2, km = 0.f, vs = 1.f, vm = 0.f;
         if constexpr (C::Q4) {
-          const uint32_t a = dead ? 0u : par[0], b = dead ? 0u : par[1];
+          const int s = i % kPageSlots;
+          wait(par_full + 8 * s, i / kPageSlots);
+          const uint32_t* par = reinterpret_cast<const uint32_t*>(fixed + S::PAR + s * 1024) + key;
+          const uint32_t a = dead ? 0u : par[0], b = dead ? 0u : par[128];
+          __syncwarp();
+          if (lane == 0) bar_arrive(par_free + 8 * s);
           const float2 x = p.fp16 ? q4::unpack2<true>(a) : q4::unpack2<false>(a);
           const float2 y = p.fp16 ? q4::unpack2<true>(b) : q4::unpack2<false>(b);
           ks = x.x;
           km = x.y;
           vs = y.x;
           vm = fmaf(8.f, y.x, y.y);  // the codes of V are taken from 8
-          fetch(id, par);
-          id = page_of(j + 2 * C::ST);
         }
-        wait(s_full + 8 * (i & 1), i >> 1);
+        wait(s_full + 8 * (i % C::SB), i / C::SB);
         tc_fence_after();
-        const uint32_t t_s = tmem + C::COL_S + (i & 1) * N + lane_off + c0;
+        const uint32_t t_s = tmem + C::COL_S + (i % C::SB) * N + lane_off + c0;
         const uint64_t ks2 = pack_f2(ks, ks), km2 = pack_f2(km, km), vs2 = pack_f2(vs, vs);
         uint64_t y[CW / 2];  // the softmax's weights (4-bit: those that meet V are y times s)
 #pragma unroll 1
@@ -1159,6 +1211,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(s_free + 8 * (i % C::SB));
         if constexpr (!C::Q4) {
           // slots that no row sees may hold anything: zero their V
           if (__any_sync(0xffffffffu, dead)) {
@@ -1268,58 +1323,32 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
     const uint8_t* src = (is_k ? p.kpar : p.vpar) - (int64_t)p.kv_heads * (D / 2) + c * 16;
     const uint32_t my_ring = ((is_k ? 0 : UG) + group) * H * C::SLOT, mine = ring_u32 + my_ring;
     const uint8_t* mine_ptr = ring + my_ring;
-    // The tile that is copied next: tile j of a task whose page list is that of `table`, up to entry `end`, entries ns and
-    // on `skip` further on.
-    int t = me - grid, seq = -1, to = 0, j = group, tiles = 0, l0 = 0, end = 0, ns = 0, skip = 0, id = -1;
-    bool there = false;
-    const int32_t* table = nullptr;
-    const uint8_t* head = src;
-    const int mine_l = bs < 32 ? 2 * q4 + (lane >> 4) : (q4 * 32) >> p.page_shift;  // this lane's page in a tile
-    auto next = [&]() {  // its page
-      while (j >= tiles && t < tasks) {
-        j -= tiles;
-        t += grid;
-        ++seq;
-        tiles = 0;
-        if (t >= tasks) break;
-        const Task k = task_at(p, prefix, cut, t);
-        table = p.block_table + (int64_t)k.b * p.max_blocks;
-        head = src + k.g * (D / 2);
-        tiles = k.tiles;
-        l0 = k.tile0 << ppt_shift;
-        end = min(k.span.pages, (k.tile0 + k.tiles) << ppt_shift);
-        ns = k.span.ns;
-        skip = k.span.wp - ns;
-      }
-      const int e = l0 + (j << ppt_shift) + mine_l;
-      there = t < tasks && e < end;
-      id = there ? __ldg(table + (e < ns ? e : e + skip)) : -1;
-    };
+    int total = 0, at = 0, to = 0, n = group;  // slots of the next tile to unpack and to copy, and the latter's number
+#pragma unroll 1
+    for (int x = me; x < tasks; x += grid) total += task_at(p, prefix, cut, x).tiles;
     auto copy = [&]() {
-      if (t < tasks) {
+      if (n < total) {
+        const int s = n % kPageSlots;
+        wait(pg_full + 8 * s, n / kPageSlots);
+        const int32_t* pages = reinterpret_cast<const int32_t*>(fixed + S::PAGES + s * 48);
         const uint32_t dst = mine + to * C::SLOT + (q4 * 32 + r0) * (D / 2);
-        const int good = checked(id, there, seq);
-        const int page[2] = {__shfl_sync(0xffffffffu, good, 0), __shfl_sync(0xffffffffu, good, 16)};
+        const uint8_t* head = src + pages[8] * (D / 2);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // 16 rows
-          const uint32_t slot = ((uint32_t)max(page[half], 0) << p.page_shift) + ((q4 * 32 + half * 16 + r0) & (bs - 1));
+          const int key = q4 * 32 + half * 16, page = pages[key >> p.page_shift];
+          const uint32_t slot = ((uint32_t)max(page, 0) << p.page_shift) + ((key + r0) & (bs - 1));
           const uint8_t* from = head + (uint64_t)slot * row;
 #pragma unroll
           for (int r = 0; r < 16; r += RPI) {
             const int swz = D == 64 ? (r0 >> 2) & 1 : D == 128 ? (r0 >> 1) & 3 : (r0 + r) & 7;
-            cp_async_16(dst + (half * 16 + r) * (D / 2) + ((c ^ swz) << 4), from + r * row, page[half] < 0 ? 0 : 16);
+            cp_async_16(dst + (half * 16 + r) * (D / 2) + ((c ^ swz) << 4), from + r * row, page < 0 ? 0 : 16);
           }
         }
         if (++to == H) to = 0;
-        j += UG;
-        next();
+        n += UG;
       }
       cp_async_commit();
     };
-    next();
-    int total = 0, at = 0;
-#pragma unroll 1
-    for (int x = me; x < tasks; x += grid) total += task_at(p, prefix, cut, x).tiles;
 #pragma unroll 1
     for (int x = 0; x < C::AHEAD; ++x) copy();
     if (is_k) {
