@@ -1,17 +1,17 @@
 // Instances of the attention over a 4-bit cache for head dim 128.
-#include "window_attention_launch.h"
+#include "q4_attention_launch.h"
 
 namespace specv {
-namespace wattn {
+namespace qattn {
 
 template <>
-int settings_q4<128>(int packed, int batch, Launch* l) {
-  return with_rows<128, true, true>(packed, [&](auto c) { return settings_of<decltype(c)>(batch, l); });
+int launch<128>(const spec_attn_desc* d, int all, const Params& p, cudaStream_t stream) {
+  return with_rows<128>(all, [&](auto c) { return launch_of<decltype(c)>(d, p, stream); });
 }
 template <>
-int launch_q4<128>(int packed, const Launch& l, const Call& call) {
-  return with_rows<128, true, true>(packed, [&](auto c) { return launch_of<decltype(c)>(l, call); });
+size_t workspace<128>(const spec_attn_desc* d, int rows, int all) {
+  return with_rows<128>(all, [&](auto c) { return workspace_of<decltype(c)>(d, rows); });
 }
 
-}  // namespace wattn
+}  // namespace qattn
 }  // namespace specv

@@ -10,6 +10,7 @@
 // each with a running maximum and sum, and are joined at the end.
 #include <math.h>
 
+#include "q4_attention_launch.h"
 #include "tensor_map.h"
 #include "window_attention_launch.h"
 
@@ -30,21 +31,32 @@ static bool shape_supported(const spec_attn_desc* d, int rows) {
   if (rows > 64 || G > kMaxRows || d->batch > kMaxBatch) return false;
   const int64_t longest = (int64_t)d->max_blocks_per_seq * bs;
   if (longest > (1 << 30) || d->num_blocks > INT32_MAX / bs) return false;
-  const int per = kMaxRows / G, groups = (rows + per - 1) / per;
+  const int groups = (rows * G + 15) / 16;  // at most
   return (longest / 128 + 2) * d->batch <= INT32_MAX / ((int64_t)d->num_kv_heads * groups);
 }
 
 // How the query rows of a kv head are cut into units.
 struct Rows {
-  int npt, groups, packed;  // query rows of a unit, units, and its packed rows: 8, 16, 32 or 64 at most
+  int per, groups, packed;  // packed rows of a unit, units, and what its kernel has room for: 8, 16, 32 or 64
 };
-static Rows rows_for(const spec_attn_desc* d, int rows) {
+static Rows rows_for(const spec_attn_desc* d, int rows) {  // whole query rows
   const int G = d->num_q_heads / d->num_kv_heads, per = kMaxRows / G;
   Rows r;
   r.groups = (rows + per - 1) / per;
-  r.npt = (rows + r.groups - 1) / r.groups;
-  for (r.packed = 8; r.packed < r.npt * G;) r.packed *= 2;
+  r.per = (rows + r.groups - 1) / r.groups * G;
+  for (r.packed = 8; r.packed < r.per;) r.packed *= 2;
   return r;
+}
+static size_t workspace_16(const spec_attn_desc* d, int rows) {
+  return SPEC_ATTN_COUNTER_BYTES + kCutBytes + (size_t)kMaxPieces * rows_for(d, rows).per * (1 + d->head_dim) * 4;
+}
+static size_t workspace_q4(const spec_attn_desc* d, int rows) {
+  const int all = rows * (d->num_q_heads / d->num_kv_heads);
+  switch (d->head_dim) {
+    case 64: return qattn::workspace<64>(d, rows, all);
+    case 128: return qattn::workspace<128>(d, rows, all);
+    default: return qattn::workspace<256>(d, rows, all);
+  }
 }
 
 static int call(bool q4, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -65,14 +77,6 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   const Rows rows = rows_for(d, num_rows);
   const bool fp16 = dtype == SPEC_DTYPE_FP16;
   const int D = d->head_dim, bs = d->block_size;
-  Launch l;
-  int rc;
-  switch (D) {
-    case 64: rc = q4 ? settings_q4<64>(rows.packed, d->batch, &l) : settings_16<64>(rows.packed, fp16, d->batch, &l); break;
-    case 128: rc = q4 ? settings_q4<128>(rows.packed, d->batch, &l) : settings_16<128>(rows.packed, fp16, d->batch, &l); break;
-    default: rc = q4 ? settings_q4<256>(rows.packed, d->batch, &l) : settings_16<256>(rows.packed, fp16, d->batch, &l); break;
-  }
-  if (rc != SPEC_OK) return rc;
 
   Call c;
   Params& p = c.p;
@@ -80,13 +84,14 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   p.q = static_cast<const uint8_t*>(q);
   p.out = static_cast<uint8_t*>(out);
   p.row = q4::row_bytes(d->num_kv_heads, D);
-  p.kpar = static_cast<const uint8_t*>(k_cache) + d->num_kv_heads * (D / 2);
-  p.vpar = static_cast<const uint8_t*>(v_cache) + d->num_kv_heads * (D / 2);
+  p.k = static_cast<const uint8_t*>(k_cache);
+  p.v = static_cast<const uint8_t*>(v_cache);
   p.block_table = block_table;
   p.ctx_lens = ctx_lens;
-  p.counters = reinterpret_cast<int32_t*>(ws);
-  p.lse = reinterpret_cast<float*>(ws + SPEC_ATTN_COUNTER_BYTES);
-  p.opart = p.lse + kMaxPieces * kMaxRows;
+  // the first bytes are other kernels' counters, which stay zero
+  p.cut_units = reinterpret_cast<CutUnit*>(ws + SPEC_ATTN_COUNTER_BYTES);
+  p.lse = reinterpret_cast<float*>(ws + SPEC_ATTN_COUNTER_BYTES + kCutBytes);
+  p.opart = p.lse + (size_t)kMaxPieces * rows.per;
   p.dev_err = dev_err;
   p.num_blocks = d->num_blocks;
   p.batch = d->batch;
@@ -94,37 +99,55 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   p.heads = d->num_q_heads;
   p.kv_heads = d->num_kv_heads;
   p.gqa = p.heads / p.kv_heads;
-  p.by_gqa = (65535 + p.gqa) / p.gqa;
-  p.npt = rows.npt;
+  p.by_gqa = ((1 << 20) + p.gqa - 1) / p.gqa;
+  p.per = p.sub = rows.per;
+  p.unit_heads = p.parts = p.pairs = 1;
+  p.by_sub = ((1 << 16) + p.sub - 1) / p.sub;
+  p.by_parts = 1 << 8;
   p.groups = rows.groups;
+  p.head_units = p.kv_heads;
   for (p.page_shift = 0; (1 << p.page_shift) < bs;) ++p.page_shift;
   p.max_blocks = d->max_blocks_per_seq;
   const int longest = p.max_blocks * bs;  // at most 2^30
   p.window = window >= longest ? 0 : window;
   p.sinks = sinks > longest ? longest : sinks;
-  p.slots = l.slots;
+  p.slots = 0;
   p.fp16 = fp16;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   c.stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  if (!q4) {
-    EncodeTiledFn encode = encode_fn();
-    if (encode == nullptr) return SPEC_ERR_LAUNCH;
-    // K and V [token rows][Hkv][D]: a box holds one head's rows of a page, 64 elements wide
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.kv_heads, (cuuint64_t)d->num_blocks * bs};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.kv_heads * D * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)bs}, ones[3] = {1, 1, 1};
-    auto map = [&](CUtensorMap* m, const void* base) {
-      return encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
-                    dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    if (!map(&c.tk, k_cache) || !map(&c.tv, v_cache)) return SPEC_ERR_LAUNCH;
+  if (q4) {
+    switch (D) {
+      case 64: return qattn::launch<64>(d, num_rows * p.gqa, p, c.stream);
+      case 128: return qattn::launch<128>(d, num_rows * p.gqa, p, c.stream);
+      default: return qattn::launch<256>(d, num_rows * p.gqa, p, c.stream);
+    }
   }
+  Launch l;
+  int rc;
   switch (D) {
-    case 64: return q4 ? launch_q4<64>(rows.packed, l, c) : launch_16<64>(rows.packed, fp16, l, c);
-    case 128: return q4 ? launch_q4<128>(rows.packed, l, c) : launch_16<128>(rows.packed, fp16, l, c);
-    default: return q4 ? launch_q4<256>(rows.packed, l, c) : launch_16<256>(rows.packed, fp16, l, c);
+    case 64: rc = settings_16<64>(rows.packed, fp16, d->batch, &l); break;
+    case 128: rc = settings_16<128>(rows.packed, fp16, d->batch, &l); break;
+    default: rc = settings_16<256>(rows.packed, fp16, d->batch, &l); break;
+  }
+  if (rc != SPEC_OK) return rc;
+  p.slots = l.slots;
+  EncodeTiledFn encode = encode_fn();
+  if (encode == nullptr) return SPEC_ERR_LAUNCH;
+  // K and V [token rows][Hkv][D]: a box holds one head's rows of a page, 64 elements wide
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.kv_heads, (cuuint64_t)d->num_blocks * bs};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.kv_heads * D * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)bs}, ones[3] = {1, 1, 1};
+  auto map = [&](CUtensorMap* m, const void* base) {
+    return encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                  dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!map(&c.tk, k_cache) || !map(&c.tv, v_cache)) return SPEC_ERR_LAUNCH;
+  switch (D) {
+    case 64: return launch_16<64>(rows.packed, fp16, l, c);
+    case 128: return launch_16<128>(rows.packed, fp16, l, c);
+    default: return launch_16<256>(rows.packed, fp16, l, c);
   }
 }
 
@@ -135,8 +158,8 @@ using namespace specv;
 
 extern "C" size_t spec_window_attention_workspace(const spec_attn_desc* d, int32_t num_rows) {
   if (!wattn::desc_ok(d, num_rows) || !wattn::shape_supported(d, num_rows)) return 0;
-  const int packed = wattn::rows_for(d, num_rows).packed, n = packed < 16 ? 16 : packed;
-  return SPEC_ATTN_COUNTER_BYTES + (size_t)wattn::kMaxPieces * (wattn::kMaxRows + (size_t)n * d->head_dim) * 4;
+  const size_t a = wattn::workspace_16(d, num_rows), b = wattn::workspace_q4(d, num_rows);
+  return a > b ? a : b;
 }
 
 extern "C" int spec_window_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

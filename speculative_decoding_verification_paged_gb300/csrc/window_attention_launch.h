@@ -1,9 +1,10 @@
 // Launch settings and launches of the windowed attention's kernels: one
-// translation unit for each head dim and kind of cache.
+// translation unit for each head dim.
 #pragma once
 
 #include "launch_memo.h"
 #include "window_attention.cuh"
+#include "window_join.cuh"
 
 namespace specv {
 namespace wattn {
@@ -26,10 +27,6 @@ static int settings_of(int batch, Launch* l) {
   std::lock_guard<std::mutex> lock(memo.mu);
   if (memo.grid[dev] == 0) {
     int sms = 0, optin = 0;
-    cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, window_attention_kernel<C>) != cudaSuccess) return SPEC_ERR_LAUNCH;
-    // the registers that are dealt out inside the kernel are those that the launch brings
-    if (C::DEAL && attr.numRegs < C::kLaunchRegs) return SPEC_ERR_LAUNCH;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
       return SPEC_ERR_LAUNCH;
@@ -38,27 +35,30 @@ static int settings_of(int batch, Launch* l) {
   }
   const size_t fixed = smem_fixed<C>(batch), room = memo.granted[dev];
   const size_t fit = fixed < room ? (room - fixed) / C::SLOT : 0;
-  const int least = C::Q4 ? C::RINGS : 2 * C::PARTS, most = C::Q4 ? least : kMaxSlots;
-  if (fit < (size_t)least) return SPEC_ERR_UNSUPPORTED;
-  l->slots = fit > (size_t)most ? most : (int)fit;
+  if (fit < (size_t)2 * C::PARTS) return SPEC_ERR_UNSUPPORTED;
+  l->slots = fit > (size_t)kMaxSlots ? kMaxSlots : (int)fit;
   l->smem = fixed + (size_t)l->slots * C::SLOT;
   l->grid = memo.grid[dev];
   return SPEC_OK;
 }
 template <class C>
-static int launch_of(const Launch& l, const Call& c) {
+static int launch_of(const Launch& l, Call c) {
+  c.p.task_cost = C::TASK_COST;
+  c.p.join_cost = C::JOIN_COST;
+  c.p.piece_cost = C::PIECE_COST;
   window_attention_kernel<C><<<l.grid, C::kThreads, l.smem, c.stream>>>(c.p, c.tk, c.tv);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_LAUNCH;
+  return launch_join<C::D>(c.p, kMaxPieces, c.stream);
 }
 
 // fn(configuration) for a unit of at most `packed` rows.
-template <int D, bool Q4, bool FP16, class F>
+template <int D, bool FP16, class F>
 static int with_rows(int packed, F fn) {
   switch (packed) {
-    case 8: return fn(Cfg<D, 8, Q4, FP16>{});
-    case 16: return fn(Cfg<D, 16, Q4, FP16>{});
-    case 32: return fn(Cfg<D, 32, Q4, FP16>{});
-    default: return fn(Cfg<D, 64, Q4, FP16>{});
+    case 8: return fn(Cfg<D, 8, FP16>{});
+    case 16: return fn(Cfg<D, 16, FP16>{});
+    case 32: return fn(Cfg<D, 32, FP16>{});
+    default: return fn(Cfg<D, 64, FP16>{});
   }
 }
 
@@ -66,10 +66,6 @@ template <int D>
 int settings_16(int packed, bool fp16, int batch, Launch* l);
 template <int D>
 int launch_16(int packed, bool fp16, const Launch& l, const Call& c);
-template <int D>
-int settings_q4(int packed, int batch, Launch* l);
-template <int D>
-int launch_q4(int packed, const Launch& l, const Call& c);
 
 }  // namespace wattn
 }  // namespace specv
