@@ -132,7 +132,7 @@ __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8
       got = __ldg(reinterpret_cast<const uint4*>(p.q) + wattn::out_row(p, k.b, head0 + h, R) * L + c);
     return got;
   };
-  uint4 next = row(tid / L), second = row(tid / L + STEP);
+  uint4 next[2] = {row(tid / L), row(tid / L + STEP)};
   // rows behind a pair's
 #pragma unroll 1
   for (int x = tid; p.sub < ROWS && x < p.pairs * C::Q_BYTES / 16; x += C::kThreads)
@@ -141,47 +141,52 @@ __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8
   for (int x = tid; x < p.pairs * 2 * ROWS; x += C::kThreads) qc[x] = 0.f;
   __syncthreads();
 #pragma unroll 1
-  for (int rr = tid / L; rr - lane / L < rows; rr += STEP) {
-    const uint4 x = next;
-    next = second;
-    second = row(rr + 2 * STEP);
-    const int of_pair = rr * p.by_sub >> 16, r = rr - of_pair * p.sub;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float f[8], top = 0.f, sum = 0.f;
+  for (int rr0 = tid / L; rr0 - lane / L < rows; rr0 += 2 * STEP) {
+    const uint4 now[2] = {next[0], next[1]};
+    next[0] = row(rr0 + 2 * STEP);
+    next[1] = row(rr0 + 3 * STEP);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 v = p.fp16 ? q4::unpack2<true>(w[e]) : q4::unpack2<false>(w[e]);
-      f[2 * e] = v.x;
-      f[2 * e + 1] = v.y;
-    }
+    for (int y = 0; y < 2; ++y) {
+      const uint4 x = now[y];
+      const int rr = rr0 + y * STEP, of_pair = rr * p.by_sub >> 16, r = rr - of_pair * p.sub;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float f[8], top = 0.f, sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      top = fmaxf(top, fabsf(f[e]));
-      sum += f[e];
-    }
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = p.fp16 ? q4::unpack2<true>(w[e]) : q4::unpack2<false>(w[e]);
+        f[2 * e] = v.x;
+        f[2 * e + 1] = v.y;
+      }
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const int e2 = max(-100, min(140, 14 + 127 - (__float_as_int(top) >> 23)));
-    const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
+      for (int e = 0; e < 8; ++e) {
+        top = fmaxf(top, fabsf(f[e]));
+        sum += f[e];
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = f[e] * f1 * f2 * (e & 1 ? 0.0625f : 1.f);
-    if (rr >= rows) continue;
-    if (c == 0) {
-      qc[of_pair * 2 * ROWS + r] = pow2(max(-126, min(127, 24 - e2))) * p.scale_log2;
-      qc[of_pair * 2 * ROWS + ROWS + r] = sum * p.scale_log2;
+      for (int o = 1; o < L; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      }
+      const int e2 = max(-100, min(140, 14 + 127 - (__float_as_int(top) >> 23)));
+      const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * f1 * f2 * (e & 1 ? 0.0625f : 1.f);
+      if (rr < rows && c == 0) {
+        qc[of_pair * 2 * ROWS + r] = pow2(max(-126, min(127, 24 - e2))) * p.scale_log2;
+        qc[of_pair * 2 * ROWS + ROWS + r] = sum * p.scale_log2;
+      }
+      // word c of the row is word `at` of lane `of`'s codes, and the operands of two steps
+      constexpr int WORDS = D / 32 < 4 ? D / 32 : 4;  // words of a lane in a row of up to 64 bytes
+      const int of = (c / WORDS) & 3, at = c % WORDS + (c / (4 * WORDS)) * WORDS;
+      const int mt = r / 16, up = (r / 8) & 1;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(queries + of_pair * C::Q_BYTES) + (mt * C::STEPS + 2 * at) * 128 + ((r & 7) * 4 + of) * 4 + up;
+      if (rr < rows) {
+        dst[0] = q4::pack2<true>(f[0], f[4]);
+        dst[2] = q4::pack2<true>(f[1], f[5]);
+        dst[128] = q4::pack2<true>(f[2], f[6]);
+        dst[130] = q4::pack2<true>(f[3], f[7]);
+      }
     }
-    // word c of the row is word `at` of lane `of`'s codes, and the operands of two steps
-    constexpr int WORDS = D / 32 < 4 ? D / 32 : 4;  // words of a lane in a row of up to 64 bytes
-    const int of = (c / WORDS) & 3, at = c % WORDS + (c / (4 * WORDS)) * WORDS;
-    const int mt = r / 16, up = (r / 8) & 1;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(queries + of_pair * C::Q_BYTES) + (mt * C::STEPS + 2 * at) * 128 + ((r & 7) * 4 + of) * 4 + up;
-    dst[0] = q4::pack2<true>(f[0], f[4]);
-    dst[2] = q4::pack2<true>(f[1], f[5]);
-    dst[128] = q4::pack2<true>(f[2], f[6]);
-    dst[130] = q4::pack2<true>(f[3], f[7]);
   }
 }
 
@@ -201,6 +206,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), g = lane >> 2, t4 = lane & 3;
   const int grid = (int)gridDim.x, me = (int)blockIdx.x;
 
+  // the queries are on their way to L2 while the plan is made
+  {
+    const int64_t bytes = (int64_t)p.batch * p.rows * p.heads * D * 2;
+    for (int64_t at = ((int64_t)me * C::kThreads + tid) * 128; at < bytes; at += (int64_t)grid * C::kThreads * 128)
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.q + at));
+  }
   // The calls read the parameters here: by a reference to the kernel's own they take a memory access each.
   Params* shared = reinterpret_cast<Params*>(fixed + S::PARAMS);
   if (tid == 0) *shared = p;
