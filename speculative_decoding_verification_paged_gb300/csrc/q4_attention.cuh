@@ -10,11 +10,6 @@
 namespace specv {
 namespace qattn {
 
-using wattn::pack_f2;
-using wattn::unpack_f2;
-using wattn::fma_f2;
-using wattn::mul_f2;
-using wattn::add_f2;
 using wattn::Params;
 using wattn::Task;
 using wattn::bar_init;
