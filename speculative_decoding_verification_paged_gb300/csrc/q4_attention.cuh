@@ -118,6 +118,7 @@ __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8
   constexpr int D = C::D, ROWS = C::ROWS;
   const Task k = *task;
   const int tid = threadIdx.x, lane = tid & 31;
+  const bool fp16 = p.fp16;
   constexpr int L = D / 8, STEP = C::kThreads / L;  // threads of a row, 8 elements each; rows in a step
   const int c = tid % L, head0 = k.g * p.unit_heads, rows = p.pairs * p.sub;
   auto row = [&](int x) {  // row x, zeros if there is none
@@ -146,11 +147,12 @@ __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8
       const int rr = rr0 + y * STEP, of_pair = rr * p.by_sub >> 16, r = rr - of_pair * p.sub;
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       float f[8], top = 0.f, sum = 0.f;
+      if (fp16) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 v = p.fp16 ? q4::unpack2<true>(w[e]) : q4::unpack2<false>(w[e]);
-        f[2 * e] = v.x;
-        f[2 * e + 1] = v.y;
+        for (int e = 0; e < 4; ++e) reinterpret_cast<float2*>(f)[e] = q4::unpack2<true>(w[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) reinterpret_cast<float2*>(f)[e] = q4::unpack2<false>(w[e]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -162,12 +164,12 @@ __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
-      const int e2 = max(-100, min(140, 14 + 127 - (__float_as_int(top) >> 23)));
-      const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
+      const int e2 = max(-100, min(126, 14 + 127 - (__float_as_int(top) >> 23)));
+      const float f1 = pow2(e2), f2 = pow2(e2 - 4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * f1 * f2 * (e & 1 ? 0.0625f : 1.f);
+      for (int e = 0; e < 8; ++e) f[e] *= e & 1 ? f2 : f1;
       if (rr < rows && c == 0) {
-        qc[of_pair * 2 * ROWS + r] = pow2(max(-126, min(127, 24 - e2))) * p.scale_log2;
+        qc[of_pair * 2 * ROWS + r] = pow2(24 - e2) * p.scale_log2;
         qc[of_pair * 2 * ROWS + ROWS + r] = sum * p.scale_log2;
       }
       // word c of the row is word `at` of lane `of`'s codes, and the operands of two steps
