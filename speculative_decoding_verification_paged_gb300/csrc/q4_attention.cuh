@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
     k.tiles = uniform(k.tiles), k.ctx = uniform(k.ctx), k.span.ns = uniform(k.span.ns), k.span.wp = uniform(k.span.wp);
     k.span.pages = uniform(k.span.pages);
     const int head0 = k.g * p.unit_heads, kv_head = head0 + head;
-    // keys of the unit's page list, and the tokens that it leaves out behind the first ones
+    // keys of the unit's page list, and the tokens that it leaves out behind the first extra
     const int entries = k.span.pages << p.page_shift, first_keys = k.span.ns << p.page_shift;
     const int skipped = (k.span.wp - k.span.ns) << p.page_shift, key0 = k.tile0 * C::KEYS;
     const int tiles = (min(k.tiles * C::KEYS, entries - key0) + TK - 1) / TK;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
 
     // ---- state of this lane's rows: g + 8 u of tile mt
     const int r0 = k.r0 + part * p.sub, nr = kv_head < p.kv_heads ? min(p.sub, k.r0 + k.nr - r0) : 0;
-    float o[MT][C::TILES][4], ones[MT][4];  // ones: sums of the weights that the products use
+    float o[MT][C::TILES][4], extra[MT][4];  // extra: what the products have too much
     float sum[MT][2], offset[MT][2], nref[MT][2], fc[MT][2], fd[MT][2];  // nref: minus the reference; factors of the scores
     int pos[MT][2];
 #pragma unroll
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ones[mt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) extra[mt][e] = 0.f;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int r = mt * 16 + u * 8 + g;
@@ -394,8 +394,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             if (!(tok <= high_pos && (p.window == 0 || tok < p.sinks || tok > low_pos - p.window))) x = make_float2(0.f, 0.f);
           }
           if (lane >= 16) x.y = fmaf(8.f, x.x, x.y);  // the codes of V are taken from 8
+          if (lane >= 24) x.x = -x.x;                 // and the last 8 keys' weights are negative (see the product)
           float* to_par = par + ((lane & 15) >> 1) * 8 + (lane >> 4) * 4 + (lane & 1);
-          __syncwarp();  // the last ones have been read
+          __syncwarp();  // the last extra have been read
           to_par[0] = x.x;
           to_par[2] = x.y;
           __syncwarp();
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
               nref[mt][u] = -now;
               sum[mt][u] *= alpha;
               offset[mt][u] *= alpha;
-              ones[mt][2 * u] *= alpha;
+              extra[mt][2 * u] *= alpha;
 #pragma unroll
               for (int x = 0; x < C::TILES; ++x) {
                 o[mt][x][2 * u] *= alpha;
@@ -538,13 +539,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             offset[mt][u] += b.x + b.y;
           }
         // ---- product with V, 32 head dims at a time. ldmatrix takes 16-bit halves, four codes of neighbouring head dims,
-        // and gives a lane those of two keys: the masks leave a pair of keys, operand B, for each of four head dims. Eight
-        // times the sum of the operands A is taken off in the end, so that a weight's rounding meets at most 8 s.
+        // and gives a lane those of two keys: the masks leave a pair of keys, operand B, for each of four head dims. The
+        // last 8 of 16 keys come as 15 - n with negative weights, -w (15 - n) = w n - 15 w: the sums of the tensor core, which
+        // are cut, not rounded, stay near zero. `extra`, 8 w of the first and -7 w of the last keys, is taken off in the end;
+        // that leaves the codes taken from 8, so that a weight's rounding meets at most 8 s.
 #pragma unroll
         for (int step = 0; step < NB / 2; ++step)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            mma_f16(ones[mt], pa[mt][step][0], pa[mt][step][1], pa[mt][step][2], pa[mt][step][3], 0x3c003c00u, 0x3c003c00u);
+            mma_f16(extra[mt], pa[mt][step][0], pa[mt][step][1], pa[mt][step][2], pa[mt][step][3], 0x48004800u, 0x47004700u);
         fresh = false;
         constexpr int CH = 4 / NB;  // 16-byte chunks of a row that a load takes, of 8 NB keys
         const uint32_t v_u32 = at + v_of;
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
 #pragma unroll
               for (int m = 0; m < NB; ++m) {
                 const uint32_t z = j & 2 ? r[ch * NB + m] >> 8 : r[ch * NB + m];
-                b[m] = j & 1 ? z & 0x00f000f0u : z & 0x000f000fu;
+                b[m] = (m & 1 ? ~z : z) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
               }
 #pragma unroll
               for (int step = 0; step < NB / 2; ++step)
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
       for (int x = 0; x < C::TILES; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          o[mt][x][e] = fmaf(o[mt][x][e], x & 1 ? 0x1p20f : 0x1p24f, -8.f * ones[mt][e & 2]);
+          o[mt][x][e] = fmaf(o[mt][x][e], x & 1 ? 0x1p20f : 0x1p24f, -extra[mt][e & 2]);
     if (p.splits > 1) {  // the other splits' results, by way of the ring, to the first one's warps
       float* box = reinterpret_cast<float*>(smem) + lane;
       if (works && split > 0) {
