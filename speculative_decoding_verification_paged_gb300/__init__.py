@@ -31,6 +31,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -704,6 +705,7 @@ def spec_window_attention(q, k_cache, v_cache, block_table, ctx_lens, out, windo
                             window, sinks, workspace, k_cache, v_cache, dev_err, stream, dev)
 
 
+@functools.lru_cache(maxsize=64)
 def q4_row_bytes(kv_heads: int, head_dim: int) -> int:
     """Bytes of a token's row in a 4-bit cache."""
     size = int(load_library().spec_q4_row_bytes(_int32(kv_heads, "kv_heads"), _int32(head_dim, "head_dim")))
