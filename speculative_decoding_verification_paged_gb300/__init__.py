@@ -750,6 +750,8 @@ def spec_q4_attention(q, k_cache, v_cache, block_table, ctx_lens, kv_heads: int,
 def _token_stride(t, name: str) -> int:
     """Elements from one token to the next of a tensor [B, R, H, D] whose tokens are evenly spaced and dense inside."""
     B, R, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
     s = t.stride()
     step = s[1] if R > 1 else s[0] if B > 1 else H * D
     if (D > 1 and s[3] != 1) or (H > 1 and s[2] != D) or (B > 1 and R > 1 and s[0] != R * step):

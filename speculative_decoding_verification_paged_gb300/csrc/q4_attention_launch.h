@@ -42,11 +42,6 @@ static bool cut_up(const spec_attn_desc* d, int rows, Params* p) {
     // the ring holds a split's tile at work and the next ones, and in the end the other splits' results
     if (p->slots < 2 * p->splits || (size_t)(p->splits - 1) * p->pairs * C::STATE * 128 > p->slots * tile) continue;
     p->ahead = p->slots / p->splits - (p->splits == 1 && p->slots > 2 ? 2 : 1);
-    // A block takes about 2.4 us for 32 keys of 8 pairs (2.2 to 2.7 measured at head dims 128 and 256, 16 and 32 rows)
-    const float tile_us = (C::D == 64 ? 0.2f : 0.3f) * p->pairs;
-    p->task_cost = 8.f / tile_us;
-    p->join_cost = 3.f / tile_us;
-    p->piece_cost = 0.05f / tile_us;
     return true;
   }
   return false;
@@ -59,6 +54,12 @@ static int launch_of(const spec_attn_desc* d, Params p, cudaStream_t stream) {
   if (dev < 0) return SPEC_ERR_LAUNCH;
   if (!cut_up<C>(d, p.rows, &p)) return SPEC_ERR_UNSUPPORTED;
   p.opart = p.lse + (size_t)kMaxPieces * p.pairs * p.sub;
+  // A block takes about 2.4 us for 32 keys of 8 pairs (2.2 to 2.7 measured at head dims 128 and 256, 16 and 32 rows)
+  const float tile_us = (C::D == 64 ? 0.2f : 0.3f) * p.pairs;
+  p.cuts = wattn::may_cut(p, C::KEYS, tile_us);
+  p.task_cost = 8.f / tile_us;
+  p.join_cost = 3.f / tile_us;
+  p.piece_cost = 0.05f / tile_us;
   const size_t smem = p.slots * (2 * (size_t)TK * p.seg) + Smem<C>::bytes(p.pairs, p.batch);
   int grid;
   {
@@ -73,7 +74,7 @@ static int launch_of(const spec_attn_desc* d, Params p, cudaStream_t stream) {
   }
   q4_attention_kernel<C><<<grid, C::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_LAUNCH;
-  return wattn::launch_join<C::D>(p, kMaxPieces, stream);
+  return p.cuts ? wattn::launch_join<C::D>(p, kMaxPieces, stream) : SPEC_OK;
 }
 template <class C>
 static size_t workspace_of(const spec_attn_desc* d, int rows) {

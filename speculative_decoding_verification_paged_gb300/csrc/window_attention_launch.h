@@ -43,12 +43,13 @@ static int settings_of(int batch, Launch* l) {
 }
 template <class C>
 static int launch_of(const Launch& l, Call c) {
+  c.p.cuts = may_cut(c.p, C::KEYS, C::TILE_US);
   c.p.task_cost = C::TASK_COST;
   c.p.join_cost = C::JOIN_COST;
   c.p.piece_cost = C::PIECE_COST;
   window_attention_kernel<C><<<l.grid, C::kThreads, l.smem, c.stream>>>(c.p, c.tk, c.tv);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_LAUNCH;
-  return launch_join<C::D>(c.p, kMaxPieces, c.stream);
+  return c.p.cuts ? launch_join<C::D>(c.p, kMaxPieces, c.stream) : SPEC_OK;
 }
 
 // fn(configuration) for a unit of at most `packed` rows.

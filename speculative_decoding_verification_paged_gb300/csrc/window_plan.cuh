@@ -42,6 +42,7 @@ struct Params {
   // 4-bit: splits that take the tiles in turns, own tiles that one is ahead of its work; bytes of a token in shared memory,
   // and where s and m begin
   int splits, ahead, seg, seg_par;
+  int cuts;  // whether units may be cut, see may_cut
   float task_cost, join_cost, piece_cost;  // what a task's start and end, a join, and a piece of it cost, in tiles
   int fp16;   // type of q and out (4-bit: and of s and m)
   float scale_log2;
@@ -147,6 +148,16 @@ __device__ __forceinline__ Task task_at(const Params& p, const int32_t* prefix, 
   return k;
 }
 
+// Whether a unit can be so long, in tiles that take `tile_us`, that cutting it pays: where not, the launch of the join (2 to
+// 3 us) is left out with the cuts.
+static inline bool may_cut(const Params& p, int keys, float tile_us) {
+  const int64_t page = int64_t(1) << p.page_shift, table = (int64_t)p.max_blocks << p.page_shift;
+  int64_t tokens = table;
+  if (p.window != 0) tokens = (p.sinks + page - 1) / page * page + ((int64_t)p.window + p.rows + 2 * page) / page * page;
+  if (tokens > table) tokens = table;
+  return (float)((tokens + keys - 1) / keys) * tile_us > 3.f;
+}
+
 // Length of the pieces. A block does ceil(tasks / blocks) tasks, one after the other; a task costs its tiles and
 // something for its start and end, and cut units have to be joined. 32 lengths (no cut at all, and sixteenths of an even
 // share) are tried, and the cheapest is taken.
@@ -179,7 +190,7 @@ __device__ __forceinline__ void make_plan(const Params& p, int32_t* prefix, uint
   auto length = [&](int c) { return c == 0 ? longest : max(1, min(longest, (int)ceilf(share * (float)c * (1.f / 16.f)))); };
   // of t tiles, by the reciprocal of a piece's length: 1 to t
   auto pieces_of = [](int t, float by_len) { return max(1, (int)ceilf((float)t * by_len - 1e-3f)); };
-  if (longest > 0) {
+  if (longest > 0 && p.cuts) {
 #pragma unroll 1
     for (int c = warp; c < kCandidates; c += C::kWarps) {
       const float by_len = 1.f / (float)length(c);
@@ -206,8 +217,8 @@ __device__ __forceinline__ void make_plan(const Params& p, int32_t* prefix, uint
   __syncthreads();
   if (warp == 0) {
     static_assert(kCandidates == 32, "one a lane");
-    const float least = longest > 0 ? -warp_max(-cost[lane]) : 0.f;
-    const int best = longest > 0 ? __ffs(__ballot_sync(0xffffffffu, cost[lane] == least)) - 1 : 0;
+    const float least = longest > 0 && p.cuts ? -warp_max(-cost[lane]) : 0.f;
+    const int best = longest > 0 && p.cuts ? __ffs(__ballot_sync(0xffffffffu, cost[lane] == least)) - 1 : 0;
     const float by_len = 1.f / (float)max(1, length(best));
     int tasks = 0, pieces = 0;
 #pragma unroll 1
@@ -262,7 +273,7 @@ struct CutUnit {
 static_assert(sizeof(CutUnit) == 24, "");
 template <class C>
 __device__ __forceinline__ void list_cut(const Params& p, const int32_t* prefix, const uint16_t* cut, int32_t* misc) {
-  if (blockIdx.x != 0) return;
+  if (blockIdx.x != 0 || !p.cuts) return;
   const int units = p.head_units * p.groups;
   if (threadIdx.x == 0) misc[0] = 0;
   __syncthreads();
