@@ -656,7 +656,7 @@ int spec_cache_update(int32_t* block_table, int32_t* page_refs, const int32_t* c
  *              may hold anything, NaN included, and pages that hold only such
  *              slots are not looked at (their block_table entry may be anything).
  *              A NaN or +inf among the scores that a row sees makes that row NaN,
- *              a score of -inf is a weight of 0; a NaN or infinity in the V of a
+ *              a score of -inf is a weight of 0 (NaN where a row has no other); a NaN or infinity in the V of a
  *              slot that only other rows of the sequence see may reach the row.
  *  block_table [B, max_blocks_per_seq] int32
  *  ctx_lens    [B] int32, tokens in the cache, the rows' own included: 0 (an empty
@@ -676,9 +676,10 @@ int spec_cache_update(int32_t* block_table, int32_t* page_refs, const int32_t* c
  * id outside the cache among the pages that it sees (SPEC_DEVERR_BLOCK_ID) gets out
  * rows of zeros. Device pointers 16-byte aligned.
  * Supported: D in {64,128,256}; bs in {16,32,64,128}; num_rows <= 64; G <= 64;
- * B <= 4096; with groups = ceil(num_rows / floor(64 / G)), at most 2^31 - 1 key
- * tiles: (max_blocks_per_seq * bs / 128 + 2) * B * Hkv * groups;
- * max_blocks_per_seq * bs at most 2^30; num_blocks * bs at most 2^31 - 1.
+ * B <= 4096; max_blocks_per_seq * bs at most 2^30; num_blocks * bs,
+ * (max_blocks_per_seq * bs / 32 + 2) * B and
+ * (max_blocks_per_seq * bs / 128 + 2) * B * Hkv * ceil(num_rows * G / 16) at most
+ * 2^31 - 1.
  */
 size_t spec_window_attention_workspace(const spec_attn_desc* d, int32_t num_rows);
 
@@ -750,7 +751,8 @@ int spec_cache_load_q4(const void* k_cache, const void* v_cache, const int32_t* 
  * workspace, errors and limits are those of spec_window_attention; there is no
  * exception for V: what a row does not see cannot reach it.
  * q is held as fp16 times a power of two of its row (elements below 2^-24 of the row's
- * largest lose bits), the weights times s as fp16 times a power of two of the row.
+ * largest lose bits; a row with an element of 2^115 or more may come out as NaN), the
+ * weights times s as fp16 times a power of two of the row.
  */
 int spec_q4_attention(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_table, const int32_t* ctx_lens, int32_t num_rows,

@@ -3,10 +3,16 @@
 // Per token and kv head, over its D elements x_e:
 //   m = min x,  s = round16((max x - min x) / 15),  n_e = round((x_e - m) / s).
 //
-// Both directions are bound by HBM: a store reads 2 bytes and writes 1/2 + 4/D
-// bytes an element, a load the reverse. A thread holds 8 elements (16 bytes of
-// 16-bit values, one word of codes), so that every access of a warp is a run of
-// consecutive bytes; the D / 8 lanes of a head find its range by shuffles.
+// A store reads 2 bytes and writes 1/2 + 4/D bytes an element, a load the reverse. A
+// thread holds 8 elements (16 bytes of 16-bit values, one word of codes), so that
+// every access of a warp is a run of consecutive bytes; the D / 8 lanes of a head find
+// its range by shuffles, least and negated greatest in the halves of one word.
+//
+// A load is bound by HBM: 65,536 tokens of 8 heads of 128 in 60 to 66 us, 340 MB, 76 to
+// 84% of the copy rate. A store is bound by instructions, 400 a warp for 256 elements of K
+// and of V: 37,000 tokens in 74 us, 30 us' worth of HBM reads and writes. (Each
+// element rounded by floor and an exact comparison took 117 us.) Small calls are launches: 12
+// us with the host's work for 512 tokens, 2 to 3 in a graph.
 //
 // The code is the exact rounding of the quotient: see codes_of.
 #include "launch_memo.h"

@@ -1,5 +1,32 @@
 // Kernel of the attention over a 4-bit cache (see the comment at the top of
-// q4_attention.cu) and its parameters, shared with the host side.
+// window_attention.cu).
+//
+// A block has eight warps, one for each kv head of a unit (or for 16 or 32 of a head's
+// rows; where there are fewer, splits of warps take the tiles in turns). A tile is 16 whole
+// token rows of K and of V, contiguous in a page, so that two bulk copies bring it for all
+// heads: 16-byte copies by the warps took 120 of 650 instructions for 32 keys, and tensor
+// copies, which go by rows, 8.6 cycles for each of 64 bytes. From there every warp works
+// alone, without a barrier inside the block but the ring's:
+//
+//   scores   mma m16n8k16, rows x 8 keys, the codes as fp16: c in the low bits of a half is
+//            the subnormal c 2^-24, so that one mask makes two operands out of a word.
+//            Queries are fp16 times a power of two of the row, bf16 ones exactly.
+//   softmax  in the accumulators' lanes; s and m of a tile are spread by shared memory
+//   product  rows x 8 head dims, the weights times s as fp16, codes of V by ldmatrix
+//
+// mma.sync instead of tcgen05: operands of the latter have to pass through tensor or shared
+// memory, unpacked, and every step between unpacking, MMAs and softmax is a barrier that
+// warps wait at. A kernel of that kind (K as e4m3 against queries in parts, V transposed by
+// ldmatrix, unpacked into tensor memory, two softmax streams) took 228 us on 32 sequences of
+// 16384 tokens, 8 kv heads of 128, 16 rows, where this one takes 167; 755 us with 64 rows
+// over 655,000 tokens, here 650 to 700; 225 us for 4 heads of 256 and 24 rows, here 235.
+//
+// What bounds it: 372 instructions for 16 keys, a head and 16 rows (33 of them mma), 71% of
+// the issue slots used: 84 us' worth of HBM reads in 167. With 32 rows or head dim 256 the
+// accumulators leave room for eight warps an SM, which wait for one another's results 1.7
+// of 5.1 cycles an instruction. Interleaving the next tile's scores with this one's product
+// was slower (174 us for 167), as were 16 rows a warp for 64 (778 for 700). 17 to 32 rows
+// go two MMA tiles to a warp, which unpack once for both (374 us for 411 in two units).
 #pragma once
 
 #include <type_traits>
@@ -44,7 +71,8 @@ struct Smem {
   static constexpr int MISC = PAR + C::kWarps * 256;    // [64]
   static constexpr int TASK = MISC + 256;
   static constexpr int PARAMS = TASK + 64;
-  static constexpr int QC = PARAMS + (sizeof(Params) + 15) / 16 * 16;                  // [pairs][2][ROWS] factors of the scores; then the queries
+  // [pairs][2][ROWS] factors of the scores; then the queries, and the plan
+  static constexpr int QC = PARAMS + (sizeof(Params) + 15) / 16 * 16;
   static_assert(sizeof(Task) <= 64, "");
   __host__ __device__ static int q(int pairs) { return (QC + pairs * 2 * C::ROWS * 4 + 127) & ~127; }
   __host__ __device__ static int prefix(int pairs) { return q(pairs) + pairs * C::Q_BYTES; }
@@ -205,7 +233,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
 
   // the queries are on their way to L2 while the plan is made
   {
-    const int64_t bytes = (int64_t)p.batch * p.rows * p.heads * D * 2;
+    const int64_t all = (int64_t)p.batch * p.rows * p.heads * D * 2, bytes = all < 32 << 20 ? all : 32 << 20;
     for (int64_t at = ((int64_t)me * C::kThreads + tid) * 128; at < bytes; at += (int64_t)grid * C::kThreads * 128)
       asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.q + at));
   }
@@ -261,14 +289,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
     k.tiles = uniform(k.tiles), k.ctx = uniform(k.ctx), k.span.ns = uniform(k.span.ns), k.span.wp = uniform(k.span.wp);
     k.span.pages = uniform(k.span.pages);
     const int head0 = k.g * p.unit_heads, kv_head = head0 + head;
-    // keys of the unit's page list, and the tokens that it leaves out behind the first extra
+    // keys of the unit's page list, and the tokens that it leaves out behind the first ones
     const int entries = k.span.pages << p.page_shift, first_keys = k.span.ns << p.page_shift;
     const int skipped = (k.span.wp - k.span.ns) << p.page_shift, key0 = k.tile0 * C::KEYS;
     const int tiles = (min(k.tiles * C::KEYS, entries - key0) + TK - 1) / TK;
     const int32_t* table = p.block_table + (int64_t)k.b * p.max_blocks;
 
-    // ---- copies. Tile i is the business of the splits' warps in turns, whole token rows of a page at once where the unit
-    // has all heads.
+    // ---- copies: whole token rows, or where a unit has some of the heads, their codes, and their s and m, of each row
     int ids = -1, win = -64;  // entries of the page list from `win` on, one a lane
     auto pages_at = [&](int l) {  // page l of the list is in the window
       if (l < win || l >= win + 32) {
@@ -396,12 +423,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
           if (lane >= 16) x.y = fmaf(8.f, x.x, x.y);  // the codes of V are taken from 8
           if (lane >= 24) x.x = -x.x;                 // and the last 8 keys' weights are negative (see the product)
           float* to_par = par + ((lane & 15) >> 1) * 8 + (lane >> 4) * 4 + (lane & 1);
-          __syncwarp();  // the last extra have been read
+          __syncwarp();  // the last ones have been read
           to_par[0] = x.x;
           to_par[2] = x.y;
           __syncwarp();
         }
-        // ---- scores: 16 rows x 8 keys a tile. Lane 4 g + t has the codes of key g from word t on: a code c in the low bits
+        // ---- scores: 16 rows x 8 keys an MMA tile. Lane 4 g + t has the codes of key g from word t on: a code c in the low bits
         // of a 16-bit half is the fp16 number c 2^-24, four bits higher c 2^-20, so that a mask makes the operands of two
         // steps out of a word.
         float s[MT][NB][4];
@@ -632,8 +659,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
                   o[mt][x / 4][x % 4] = o[mt][x / 4][x % 4] * a + from[(mt * (C::TILES * 4 + 6) + x) * 32] * b;
             }
         }
-        fence_proxy_async_smem();  // copies write here again
       }
+      fence_proxy_async_smem();  // copies write here again
     }
     // ---- results: a lane has 8 neighbouring head dims of its rows
     if (split == 0) {
@@ -649,7 +676,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             b += __shfl_xor_sync(0xffffffffu, b, x);
           }
           if (r >= nr) continue;
-          const float inv = a == 0.f ? 0.f : 1.f / a;
+          const float inv = k.pieces > 1 && a == 0.f ? 0.f : 1.f / a;
           if (k.pieces == 1) {
             uint4* dst = reinterpret_cast<uint4*>(p.out) + wattn::out_row(p, k.b, kv_head, r0 + r) * (D / 8) + t4;
 #pragma unroll

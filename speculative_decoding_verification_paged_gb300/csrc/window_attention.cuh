@@ -1,5 +1,18 @@
 // Kernel of the attention over a window of a 16-bit paged cache (see the comment
 // at the top of window_attention.cu).
+//
+// Keys on the M side of the MMAs (tiles of 128), packed query rows on N, which may be as
+// few as 16: S^T = K Q^T and O^T = V^T P^T, accumulators in tensor memory. One block an SM,
+// a warp or more for each role: tensor copies of K and V (rings of their own, so that a
+// barrier's phases are all waited for by one warp, in turn), the scores' MMAs, the
+// products' MMAs, softmax (a thread for a key, 8 or 16 of the rows), queries in and results
+// out. Nothing waits for a result that it does not need: a tile's scores are computed while
+// the last one's weights are made.
+//
+// What bounds it: HBM for long units; for 24 rows of head dim 256 (a tile in two parts, 64
+// KB) the ring holds a tile and a half ahead, which is 69 to 76% of the copy rate. Hot loops
+// of all roles together have to fit the SM's instruction cache: unrolled by hand and in
+// full, they were three times slower.
 #pragma once
 
 #include <cuda.h>
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
         if (et < k.nr) {
           const float* x = reinterpret_cast<const float*>(fixed + S::STAT + ob * S::STAT_BYTES) + et;
           const float sum = (x[0] + x[64]) + (x[128] + x[192]);
-          e_fac[et] = bad || sum == 0.f ? 0.f : 1.f / sum;
+          e_fac[et] = bad || (sum == 0.f && k.pieces > 1) ? 0.f : 1.f / sum;
           e_row[et] = out_row(p, k.b, k.g, k.r0 + et) * D;
           // a piece without a visible key has weight 0
           if (k.pieces > 1)

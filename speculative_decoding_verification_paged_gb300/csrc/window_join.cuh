@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
   for (int o = 1; o < GROUP; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (!there) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = top == INFINITY ? 0.f : 1.f / sum;  // NaN where all scores of a row are -inf, as in one piece
   a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
   reinterpret_cast<uint2*>(p.out)[out_row(p, u.b, g, R) * L + c] =
       p.fp16 ? make_uint2(q4::pack2<true>(a.x, a.y), q4::pack2<true>(a.z, a.w))

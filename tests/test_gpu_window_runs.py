@@ -101,6 +101,21 @@ def test_serving_run(sv, dtype, D, window):
             assert torch.equal(got[w][b, n - lens[b]:].cpu(), want) and not got[w][b, : n - lens[b]].any()
 
 
+def test_rows_whose_scores_are_all_minus_infinity(sv):
+    """NaN, in one piece and in many; the other kv head's rows are as ever."""
+    for ctx in (40, 9000):
+        c = make(np.random.default_rng(ctx), (ctx, 300), 2, 4, 2, 64, 64, BF, 0, 0, False)
+        q, k, v, _, table, _ = c["host"]
+        q[..., 3] = np.abs(q[..., 3]) + 0.5
+        k[table[0, : -(-ctx // 64)], :, 1, 3] = -np.inf
+        c["q"], c["k"] = torch.from_numpy(q).to(BF).to(DEV), torch.from_numpy(k).to(BF).to(DEV)
+        out, err = call(sv, c)
+        assert err == 0 and out[0, :, 2:].isnan().all()
+        good = dict(c, q=c["q"][:, :, :2].contiguous(), k=c["k"][:, :, :1].contiguous(), v=c["v"][:, :, :1].contiguous(), K=1,
+                    host=(q[:, :, :2], k[:, :, :1], v[:, :, :1], None, table, c["host"][5]))
+        check(good, out[:, :, :2])
+
+
 # q4 head counts that do not fit a block's eight warps: more than eight, and parts of eight at the end; one and two
 @pytest.mark.parametrize("H,K,D,R,bs", [(10, 10, 128, 3, 16), (24, 12, 64, 1, 32), (34, 17, 128, 20, 64), (32, 32, 256, 1, 64),
                                         (8, 1, 64, 1, 16), (2, 1, 256, 5, 128), (20, 5, 128, 9, 32)])
