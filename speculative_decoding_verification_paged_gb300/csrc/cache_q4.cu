@@ -46,30 +46,30 @@ struct Params {
   const int32_t* block_table;
   const int32_t* ctx_lens;
   int32_t* dev_err;
-  int64_t num_blocks, row;  // pages; bytes of a token's row
+  uint32_t num_blocks, row;  // pages; bytes of a token's row
   uint32_t chunks;          // 8-element chunks of all tokens
   Quotient per_token;       // chunks of a token: Hkv * D / 8
   Quotient rows;
   uint32_t tokens;
-  int page_shift, max_blocks;
+  int page_shift, max_blocks, max_tokens;
 };
 
 // The cache slot of token row n of the call: -1 for padding, -2 for what has an error.
-__device__ __forceinline__ int64_t slot_of(const Params& p, uint32_t n, int32_t* err) {
+__device__ __forceinline__ int slot_of(const Params& p, uint32_t n, int32_t* err) {
   const uint32_t b = p.rows.of(n);
   const int ctx = __ldg(p.ctx_lens + b);
-  if (ctx < 0 || (int64_t)ctx > ((int64_t)p.max_blocks << p.page_shift)) {
+  if (ctx < 0 || ctx > p.max_tokens) {
     *err = SPEC_DEVERR_CTX_LEN;
     return -2;
   }
-  const int64_t t = (int64_t)ctx - p.rows.d + (n - b * p.rows.d);
+  const int t = ctx - (int)p.rows.d + (int)(n - b * p.rows.d);
   if (t < 0) return -1;
   const int page = __ldg(p.block_table + (int64_t)b * p.max_blocks + (t >> p.page_shift));
-  if (page < 0 || page >= p.num_blocks) {
+  if ((uint32_t)page >= p.num_blocks) {
     *err = SPEC_DEVERR_BLOCK_ID;
     return -2;
   }
-  return ((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+  return (page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
 }
 
 // The code of x, given m, s and 1 / s (all times a power of two of the head where its range is close to fp32's ends). y =
@@ -156,7 +156,7 @@ template <int D, bool FP16>
 __global__ void __launch_bounds__(kThreads) cache_store_q4_kernel(const Params p) {
   constexpr int L = D / 8;  // lanes of a head
   const uint32_t c = blockIdx.x * kThreads + threadIdx.x, n = p.per_token.of(c), at = c - n * p.per_token.d;
-  int64_t slot = -1;
+  int slot = -1;
   if (n < p.tokens) {
     int32_t err = 0;
     slot = slot_of(p, n, &err);
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) cache_store_q4_kernel(const Params p
       code = codes_of(x, lo, s16, range);
     }
     if (slot >= 0) {
-      uint32_t* row = reinterpret_cast<uint32_t*>(p.dst[w] + slot * p.row);
+      uint32_t* row = reinterpret_cast<uint32_t*>(p.dst[w] + (uint64_t)(uint32_t)slot * p.row);
       row[at] = code;
       if (at % L == 0) row[p.per_token.d + at / L] = par;
     }
@@ -219,12 +219,12 @@ __global__ void __launch_bounds__(kThreads) cache_load_q4_kernel(const Params p,
     const uint32_t n = n0 + t * groups;
     if (T > 1 && n >= p.tokens) break;
     int32_t err = 0;
-    const int64_t slot = slot_of(p, n, &err);
+    const int slot = slot_of(p, n, &err);
     if (err != 0 && at == 0) raise_error(p.dev_err, err);
     if (slot >= 0) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t* row = reinterpret_cast<const uint32_t*>(p.src[w] + slot * p.row);
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(p.src[w] + (uint64_t)(uint32_t)slot * p.row);
         code[t][w] = __ldcs(row + at);
         par[t][w] = __ldg(row + p.per_token.d + at / L);
       }
@@ -234,16 +234,23 @@ __global__ void __launch_bounds__(kThreads) cache_load_q4_kernel(const Params p,
   for (int t = 0; t < T; ++t) {
     const uint32_t n = n0 + t * groups;
     if (T > 1 && n >= p.tokens) break;
-    const int64_t chunk = (int64_t)n * p.per_token.d + at;
+    const uint32_t chunk = n * p.per_token.d + at;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const float2 sm = unpack2<FP16>(par[t][w]);
+      const uint64_t s = pack_f2(sm.x, sm.x), m = pack_f2(sm.y, sm.y), base = pack_f2(-8388608.f, -8388608.f);
+      const uint32_t even = code[t][w] & 0x0f0f0f0fu, odd = code[t][w] >> 4 & 0x0f0f0f0fu;
       float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)  // 2^23 + n, as a float
-        x[i] = fmaf(__uint_as_float(((code[t][w] >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f, sm.x, sm.y);
+      for (int i = 0; i < 4; ++i) {  // a byte n behind 0x4b0000 is the float 2^23 + n
+        const uint64_t n2 = pack_f2(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7440 | i)),
+                                    __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7440 | i)));
+        const float2 f = unpack_f2(fma_f2(add_f2(n2, base), s, m));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
       if constexpr (F32) {
-        float4* out = reinterpret_cast<float4*>(p.dst[w]) + chunk * 2;
+        float4* out = reinterpret_cast<float4*>(p.dst[w]) + (int64_t)chunk * 2;
         __stcs(out, make_float4(x[0], x[1], x[2], x[3]));
         __stcs(out + 1, make_float4(x[4], x[5], x[6], x[7]));
       } else {
@@ -273,13 +280,14 @@ static int params_for(Params& p, const int32_t* block_table, const int32_t* ctx_
   p.block_table = block_table;
   p.ctx_lens = ctx_lens;
   p.dev_err = dev_err;
-  p.num_blocks = d->num_blocks;
-  p.row = row_bytes(d->num_kv_heads, D);
+  p.num_blocks = (uint32_t)d->num_blocks;
+  p.row = (uint32_t)row_bytes(d->num_kv_heads, D);
   p.per_token = quotient_by((uint32_t)per_token);
   p.chunks = (uint32_t)(tokens * per_token);
   p.rows = quotient_by((uint32_t)num_rows);
   p.tokens = (uint32_t)tokens;
   p.max_blocks = d->max_blocks_per_seq;
+  p.max_tokens = d->max_blocks_per_seq * bs;
   for (p.page_shift = 0; (1 << p.page_shift) < bs;) ++p.page_shift;
   return SPEC_OK;
 }
