@@ -391,6 +391,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
       }
     }
     const int low_pos = k.ctx - p.rows + r0 / p.gqa, high_pos = k.ctx - p.rows + (r0 + nr - 1) / p.gqa;
+    // tiles that all rows see whole begin at `early` at most, or from `near` to `late`
+    int early = low_pos - 15, near = INT32_MAX, late = 0;
+    if (p.window != 0) {
+      early = min(min(first_keys - 16, p.sinks - 16), early);
+      near = max(first_keys, high_pos - p.window + 1 - skipped);
+      late = low_pos - 15 - skipped;
+    }
     const uint32_t mine = smem_u32(queries) + pair * C::Q_BYTES + lane * 16;
     const int ahead = p.ahead * p.splits;
     bool fresh = true;
@@ -410,12 +417,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
         auto sees = [&](int position, int tok) {
           return tok <= position && (p.window == 0 || tok < p.sinks || tok > position - p.window);
         };
-        const int from = where + (where < first_keys ? 0 : skipped), to = from + 15;  // of one page
-        const bool whole = to <= low_pos && (p.window == 0 || to < p.sinks || from > high_pos - p.window);
+        const bool whole = where <= early || (where >= near && where <= late);
         // ---- s and m to fp32
         {
           const uint32_t a = lds32(at + par_of);
-          float2 x = p.fp16 ? q4::unpack2<true>(a) : q4::unpack2<false>(a);
+          float2 x;
+          if (p.fp16) x = q4::unpack2<true>(a);
+          else x = q4::unpack2<false>(a);
           if (!whole) {  // what no row sees may hold anything
             const int tok = token(lane & 15);
             if (!(tok <= high_pos && (p.window == 0 || tok < p.sinks || tok > low_pos - p.window))) x = make_float2(0.f, 0.f);
