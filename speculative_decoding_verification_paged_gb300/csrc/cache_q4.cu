@@ -8,11 +8,12 @@
 // every access of a warp is a run of consecutive bytes; the D / 8 lanes of a head find
 // its range by shuffles, least and negated greatest in the halves of one word.
 //
-// A load is bound by HBM: 65,536 tokens of 8 heads of 128 in 60 to 66 us, 340 MB, 76 to
-// 84% of the copy rate. A store is bound by instructions, 400 a warp for 256 elements of K
-// and of V: 37,000 tokens in 74 us, 30 us' worth of HBM reads and writes. (Each
-// element rounded by floor and an exact comparison took 117 us.) Small calls are launches: 12
-// us with the host's work for 512 tokens, 2 to 3 in a graph.
+// A load comes to 81 to 90% of the copy rate: 65,536 tokens of 8 heads of 128 in 56 to 62 us,
+// 340 MB. A store is bound by instructions, 450 a warp before the last step for 256 elements
+// of K and of V (73% of the issue slots used, 26% of the HBM rate): 65,536 tokens in 115 us,
+// 53 us' worth of reads and writes. Each element rounded by floor and an exact comparison took
+// 1.6 times as long. Small calls are launches: 10 us with the host's work for 512 tokens,
+// 2 to 3 in a graph.
 //
 // The code is the exact rounding of the quotient: see codes_of.
 #include "launch_memo.h"
@@ -29,7 +30,8 @@ struct Quotient {
   uint32_t mul, shift, d;  // mul 0: d is 1
   __device__ __forceinline__ uint32_t of(uint32_t x) const { return mul == 0 ? x : __umulhi(x, mul) >> shift; }
 };
-// 2^(31 + s) / d rounded up, 2^s >= d: x times it is less than 2^(31 + s) above x 2^(31 + s) / d in units of 1 / d.
+// mul = floor(2^(31 + s) / d) + 1 with 2^s >= d: mul d is above 2^(31 + s) by 2^s at most, so that for x < 2^31 the product
+// x mul / 2^(31 + s) is above x / d by less than 1 / d.
 static Quotient quotient_by(uint32_t d) {
   Quotient q = {0, 0, d};
   if (d == 1) return q;
