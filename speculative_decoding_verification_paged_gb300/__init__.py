@@ -258,8 +258,8 @@ def spec_verify_attention_plan(q: torch.Tensor, k_cache: torch.Tensor, block_tab
 
 
 def new_attention_workspace(nbytes: int, device) -> torch.Tensor:
-    """A workspace for spec_verify_attention and spec_tree_attention: its counters zeroed once (on the current stream),
-    the rest left as it is; reusable on one stream by later calls of both, of any shape that it is large enough for."""
+    """A workspace for the attention calls: its counters zeroed once (on the current stream), the rest left as it is;
+    reusable on one stream by later calls of all of them, of any shape that it is large enough for."""
     ws = torch.empty(max(int(nbytes), ATTN_COUNTER_BYTES), dtype=torch.uint8, device=device)
     if ws.is_cuda and ws.get_device() == torch.cuda.current_device():
         _check("spec_attention_workspace_init",
