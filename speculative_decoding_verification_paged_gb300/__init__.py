@@ -726,10 +726,12 @@ def _need_q4_caches(k_cache, v_cache, kv_heads: int, head_dim: int, dev: int):
     """Two 4-bit caches of one layer: (pages, page size)."""
     _need_dims(k_cache, "k_cache", torch.uint8, 4, dev)
     row = q4_row_bytes(kv_heads, head_dim)
-    if k_cache.shape[2:] != (1, row):
-        raise ValueError(f"k_cache must be [num_blocks, block_size, 1, {row}], got {tuple(k_cache.shape)}")
-    _need_shape(v_cache, "v_cache", torch.uint8, k_cache.shape, dev)
-    return k_cache.shape[0], k_cache.shape[1]
+    shape = k_cache.shape
+    pages, page, one, size = shape
+    if one != 1 or size != row:
+        raise ValueError(f"k_cache must be [num_blocks, block_size, 1, {row}], got {tuple(shape)}")
+    _need_shape(v_cache, "v_cache", torch.uint8, shape, dev)
+    return pages, page
 
 
 def spec_q4_attention(q, k_cache, v_cache, block_table, ctx_lens, kv_heads: int, out, window: int = 0, sinks: int = 0,
