@@ -9,44 +9,52 @@ namespace wattn {
 constexpr int kJoinThreads = 128;
 
 // out = sum of 2^lse_w opart_w over the pieces w of a unit, in their order, over the sum of 2^lse_w; zeros if a piece has no
-// result. A piece without a visible key (lse -inf) holds zeros. A block joins some rows of a unit, four head dims a thread.
+// result. A piece without a visible key (lse -inf) holds zeros. D / 4 threads for a row, four head dims each; a block joins
+// some rows, or (`split`) one, whose pieces its groups of threads take in turns.
 //
 // A kernel of its own: the block that happens to finish a unit's last piece would have to read 2.5 to 8 us' worth of
 // partial results at the latency of L2 by itself, on code that it meets for the first time (15 us measured for 64 pieces of
 // 32 rows); here all SMs share in it.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
-  constexpr int L = D / 4, GROUP = L < 32 ? L : 32, ROWS = kJoinThreads / L, AT_ONCE = 8;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p, int split) {
+  constexpr int L = D / 4, GROUP = L < 32 ? L : 32, GROUPS = kJoinThreads / L, AT_ONCE = 8;
+  __shared__ float4 s_part[kJoinThreads];
+  __shared__ float s_sum[GROUPS];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if ((int)blockIdx.x >= __ldcg(&p.cut_units[0].b)) return;
   const CutUnit u = p.cut_units[1 + blockIdx.x];
-  const int c = threadIdx.x % L, r = (int)blockIdx.y * ROWS + threadIdx.x / L, rows = p.pairs * p.sub, lane = threadIdx.x % GROUP;
+  const int c = threadIdx.x % L, group = threadIdx.x / L, rows = p.pairs * p.sub, lane = threadIdx.x % GROUP;
+  const int r = split ? (int)blockIdx.y : (int)blockIdx.y * GROUPS + group, part = split ? group : 0, parts = split ? GROUPS : 1;
   const int of_pair = r * p.by_sub >> 16, h = of_pair * p.by_parts >> 8, R = u.r0 - h * p.per + r, g = u.g * p.unit_heads + h;
   const bool there = r < rows && R < u.r0 + u.nr && g < p.kv_heads;
+  if (split && !there) return;
   const int first = there ? r : 0;  // the threads of a row that is not there go along
   const float* lse = p.lse + (int64_t)u.first * rows + first;
   const float4* src = reinterpret_cast<const float4*>(p.opart) + ((int64_t)u.first * rows + first) * L + c;
   const int64_t step = (int64_t)rows * L;
   float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll 4
   for (int w = lane; w < u.pieces; w += GROUP) top = fmaxf(top, __ldcg(lse + (int64_t)w * rows));
 #pragma unroll
   for (int o = 1; o < GROUP; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // this group's are the pieces part, part + parts, ...; the groups of a warp take as many steps, the last with weight 0
+  const int steps = (u.pieces + parts - 1) / parts;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
 #pragma unroll 1
-  for (int w0 = 0; w0 < u.pieces; w0 += GROUP) {
-    const float l = w0 + lane < u.pieces ? __ldcg(lse + (int64_t)(w0 + lane) * rows) : -INFINITY;
-    const float mine = l == -INFINITY || top == INFINITY ? 0.f : exp2f(l - top);
-    sum += mine;
+  for (int w0 = 0; w0 < steps; w0 += GROUP) {
+    const int piece = part + (w0 + lane) * parts;
+    const float l = piece < u.pieces ? __ldcg(lse + (int64_t)piece * rows) : -INFINITY;
+    const float weight = l == -INFINITY || top == INFINITY ? 0.f : exp2f(l - top);
+    sum += weight;
 #pragma unroll 1
-    for (int w1 = 0; w1 < GROUP && w0 + w1 < u.pieces; w1 += AT_ONCE) {
+    for (int w1 = 0; w1 < GROUP && w0 + w1 < steps; w1 += AT_ONCE) {
       float4 y[AT_ONCE];
 #pragma unroll
-      for (int w = 0; w < AT_ONCE; ++w) y[w] = __ldcg(src + min(w0 + w1 + w, u.pieces - 1) * step);
+      for (int w = 0; w < AT_ONCE; ++w) y[w] = __ldcg(src + min(part + (w0 + w1 + w) * parts, u.pieces - 1) * step);
 #pragma unroll
       for (int w = 0; w < AT_ONCE; ++w) {
-        const float f = __shfl_sync(0xffffffffu, mine, w1 + w, GROUP);
+        const float f = __shfl_sync(0xffffffffu, weight, w1 + w, GROUP);
         a.x = fmaf(f, y[w].x, a.x);
         a.y = fmaf(f, y[w].y, a.y);
         a.z = fmaf(f, y[w].z, a.z);
@@ -56,6 +64,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
 #pragma unroll
   for (int o = 1; o < GROUP; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (split) {
+    s_part[threadIdx.x] = a;
+    if (c == 0) s_sum[group] = sum;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll 1
+    for (int x = 1; x < GROUPS; ++x) {
+      const float4 y = s_part[x * L + c];
+      a = make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w);
+      sum += s_sum[x];
+    }
+  }
   if (!there) return;
   const float inv = top == INFINITY ? 0.f : 1.f / sum;  // NaN where all scores of a row are -inf, as in one piece
   a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
@@ -68,9 +88,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 template <int D>
 static int launch_join(const Params& p, int max_pieces, cudaStream_t stream) {
   const int64_t units = (int64_t)p.batch * p.head_units * p.groups;
-  const int rows = kJoinThreads / (D / 4);
+  const int lists = (int)(units < max_pieces / 2 ? units : max_pieces / 2), rows = p.pairs * p.sub, groups = kJoinThreads / (D / 4);
+  // One row a block while all blocks fit the GPU at once (about 16 an SM): few units are cut into many pieces (one sequence of
+  // 16384 tokens, 256 pieces of 32 rows: 37 us, 29 so). Else a block has a row for each group.
+  const int split = (int64_t)lists * rows <= 2400 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units < max_pieces / 2 ? units : max_pieces / 2), (unsigned)((p.pairs * p.sub + rows - 1) / rows));
+  cfg.gridDim = dim3((unsigned)lists, (unsigned)(split ? rows : (rows + groups - 1) / groups));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -78,7 +101,7 @@ static int launch_join(const Params& p, int max_pieces, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, split) == cudaSuccess ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 }  // namespace wattn
