@@ -77,8 +77,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
   }
   if (!there) return;
-  const float inv = top == INFINITY ? 0.f : 1.f / sum;  // NaN where all scores of a row are -inf, as in one piece
+  const float inv = 1.f / sum;  // the row is NaN where all its scores are -inf, as in one piece
   a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  // Chosen, not a product with 0: what the pieces hold beside a bad page may be NaN.
+  if (top == INFINITY) a = make_float4(0.f, 0.f, 0.f, 0.f);
   reinterpret_cast<uint2*>(p.out)[out_row(p, u.b, g, R) * L + c] =
       p.fp16 ? make_uint2(q4::pack2<true>(a.x, a.y), q4::pack2<true>(a.z, a.w))
              : make_uint2(q4::pack2<false>(a.x, a.y), q4::pack2<false>(a.z, a.w));
