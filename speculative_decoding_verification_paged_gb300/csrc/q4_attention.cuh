@@ -701,8 +701,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             }
           } else {
             const int64_t row = ((int64_t)k.slot * p.pairs + pair) * p.sub + r;
-            // a piece without a visible key has weight 0
-            if (t4 == 0) __stcg(p.lse + row, bad ? INFINITY : a == 0.f ? -INFINITY : log2f(a) - nref[mt][u]);
+            if (t4 == 0) __stcg(p.stat + row, make_float2(-nref[mt][u], bad ? -1.f : a));
             float4* dst = reinterpret_cast<float4*>(p.opart) + row * (D / 4) + t4 * 2;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)

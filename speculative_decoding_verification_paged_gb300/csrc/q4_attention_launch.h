@@ -53,7 +53,7 @@ static int launch_of(const spec_attn_desc* d, Params p, cudaStream_t stream) {
   const int dev = current_device();
   if (dev < 0) return SPEC_ERR_LAUNCH;
   if (!cut_up<C>(d, p.rows, &p)) return SPEC_ERR_UNSUPPORTED;
-  p.opart = p.lse + (size_t)kMaxPieces * p.pairs * p.sub;
+  p.opart = reinterpret_cast<float*>(p.stat + (size_t)kMaxPieces * p.pairs * p.sub);
   // A block takes about 2.4 us for 32 keys of 8 pairs (2.2 to 2.7 measured at head dims 128 and 256, 16 and 32 rows)
   const float tile_us = (C::D == 64 ? 0.2f : 0.3f) * p.pairs;
   p.cuts = wattn::may_cut(p, C::KEYS, tile_us);
@@ -80,7 +80,7 @@ template <class C>
 static size_t workspace_of(const spec_attn_desc* d, int rows) {
   Params p;
   if (!cut_up<C>(d, rows, &p)) return 0;
-  return SPEC_ATTN_COUNTER_BYTES + wattn::kCutBytes + (size_t)kMaxPieces * p.pairs * p.sub * (1 + C::D) * 4;
+  return SPEC_ATTN_COUNTER_BYTES + wattn::kCutBytes + (size_t)kMaxPieces * p.pairs * p.sub * (2 + C::D) * 4;
 }
 
 // fn(configuration) for `all` packed rows of a kv head: the accumulators of 32 rows of head dim 256 do not fit the registers.

@@ -65,7 +65,7 @@ static Rows rows_for(const spec_attn_desc* d, int rows) {  // whole query rows
   return r;
 }
 static size_t workspace_16(const spec_attn_desc* d, int rows) {
-  return SPEC_ATTN_COUNTER_BYTES + kCutBytes + (size_t)kMaxPieces * rows_for(d, rows).per * (1 + d->head_dim) * 4;
+  return SPEC_ATTN_COUNTER_BYTES + kCutBytes + (size_t)kMaxPieces * rows_for(d, rows).per * (2 + d->head_dim) * 4;
 }
 static size_t workspace_q4(const spec_attn_desc* d, int rows) {
   const int all = rows * (d->num_q_heads / d->num_kv_heads);
@@ -107,8 +107,8 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   p.ctx_lens = ctx_lens;
   // the first bytes are other kernels' counters, which stay zero
   p.cut_units = reinterpret_cast<CutUnit*>(ws + SPEC_ATTN_COUNTER_BYTES);
-  p.lse = reinterpret_cast<float*>(ws + SPEC_ATTN_COUNTER_BYTES + kCutBytes);
-  p.opart = p.lse + (size_t)kMaxPieces * rows.per;
+  p.stat = reinterpret_cast<float2*>(ws + SPEC_ATTN_COUNTER_BYTES + kCutBytes);
+  p.opart = reinterpret_cast<float*>(p.stat + (size_t)kMaxPieces * rows.per);
   p.dev_err = dev_err;
   p.num_blocks = d->num_blocks;
   p.batch = d->batch;

@@ -436,9 +436,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           const float sum = (x[0] + x[64]) + (x[128] + x[192]);
           e_fac[et] = bad || (sum == 0.f && k.pieces > 1) ? 0.f : 1.f / sum;
           e_row[et] = out_row(p, k.b, k.g, k.r0 + et) * D;
-          // a piece without a visible key has weight 0
-          if (k.pieces > 1)
-            __stcg(p.lse + (int64_t)k.slot * p.sub + et, bad ? INFINITY : sum == 0.f ? -INFINITY : x[256] + log2f(sum));
+          if (k.pieces > 1) __stcg(p.stat + (int64_t)k.slot * p.sub + et, make_float2(x[256], bad ? -1.f : sum));
         }
         named_sync(kBarEpi, 128);
         const uint32_t o = tmem + C::COL_O + ob * C::O_COLS + lane_off;

@@ -8,9 +8,10 @@ namespace wattn {
 
 constexpr int kJoinThreads = 128;
 
-// out = sum of 2^lse_w opart_w over the pieces w of a unit, in their order, over the sum of 2^lse_w; zeros if a piece has no
-// result. A piece without a visible key (lse -inf) holds zeros. D / 4 threads for a row, four head dims each; a block joins
-// some rows, or (`split`) one, whose pieces its groups of threads take in turns.
+// out = sum of W_w opart_w over the pieces w of a unit, in their order, over the sum of W_w = 2^reference_w sum_w; zeros if a
+// piece has no result. References and sums come apart: next to a large reference log2 of a sum has no bits left. A piece
+// without a visible key has sum 0 and holds zeros. D / 4 threads for a row, four head dims each; a block joins some rows, or
+// (`split`) one, whose pieces its groups of threads take in turns.
 //
 // A kernel of its own: the block that happens to finish a unit's last piece would have to read 2.5 to 8 us' worth of
 // partial results at the latency of L2 by itself, on code that it meets for the first time (15 us measured for 64 pieces of
@@ -29,14 +30,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const bool there = r < rows && R < u.r0 + u.nr && g < p.kv_heads;
   if (split && !there) return;
   const int first = there ? r : 0;  // the threads of a row that is not there go along
-  const float* lse = p.lse + (int64_t)u.first * rows + first;
+  const float2* stat = p.stat + (int64_t)u.first * rows + first;
   const float4* src = reinterpret_cast<const float4*>(p.opart) + ((int64_t)u.first * rows + first) * L + c;
   const int64_t step = (int64_t)rows * L;
-  float top = -INFINITY;
+  float top = -INFINITY, least = 0.f;  // of the references, and of the sums
 #pragma unroll 4
-  for (int w = lane; w < u.pieces; w += GROUP) top = fmaxf(top, __ldcg(lse + (int64_t)w * rows));
+  for (int w = lane; w < u.pieces; w += GROUP) {
+    const float2 x = __ldcg(stat + (int64_t)w * rows);
+    top = fmaxf(top, x.x);
+    least = fminf(least, x.y);
+  }
 #pragma unroll
-  for (int o = 1; o < GROUP; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int o = 1; o < GROUP; o <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+  }
   // this group's are the pieces part, part + parts, ...; the groups of a warp take as many steps, the last with weight 0
   const int steps = (u.pieces + parts - 1) / parts;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -44,8 +52,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll 1
   for (int w0 = 0; w0 < steps; w0 += GROUP) {
     const int piece = part + (w0 + lane) * parts;
-    const float l = piece < u.pieces ? __ldcg(lse + (int64_t)piece * rows) : -INFINITY;
-    const float weight = l == -INFINITY || top == INFINITY ? 0.f : exp2f(l - top);
+    float weight = 0.f;
+    if (piece < u.pieces) {
+      const float2 x = __ldcg(stat + (int64_t)piece * rows);
+      weight = exp2f(x.x - top) * x.y;
+    }
     sum += weight;
 #pragma unroll 1
     for (int w1 = 0; w1 < GROUP && w0 + w1 < steps; w1 += AT_ONCE) {
@@ -80,7 +91,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const float inv = 1.f / sum;  // the row is NaN where all its scores are -inf, as in one piece
   a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
   // Chosen, not a product with 0: what the pieces hold beside a bad page may be NaN.
-  if (top == INFINITY) a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (least < 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);
   reinterpret_cast<uint2*>(p.out)[out_row(p, u.b, g, R) * L + c] =
       p.fp16 ? make_uint2(q4::pack2<true>(a.x, a.y), q4::pack2<true>(a.z, a.w))
              : make_uint2(q4::pack2<false>(a.x, a.y), q4::pack2<false>(a.z, a.w));

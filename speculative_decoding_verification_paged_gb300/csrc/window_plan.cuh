@@ -26,7 +26,7 @@ struct Params {
   const int32_t* block_table;
   const int32_t* ctx_lens;
   CutUnit* cut_units;  // [1 + kMaxPieces / 2]
-  float* lse;          // [pieces][pairs][sub], log2 units; +inf: no result
+  float2* stat;        // [pieces][pairs][sub]: reference of a row's weights (log2 units) and their sum; below 0: no result
   float* opart;        // [pieces][pairs][sub][D], normalised
   int32_t* dev_err;
   int64_t num_blocks, row;  // pages; bytes of a 4-bit token row

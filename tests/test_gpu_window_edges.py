@@ -1,11 +1,14 @@
-"""Windowed and 4-bit attention at the edges of what the header allows: bad pages beside values that are no numbers.
+"""Windowed and 4-bit attention at the edges of what the header allows: bad pages beside values that are no numbers, scores
+far past fp32's resolution of a power of two.
 
 Tolerances are those of test_gpu_window where no other is derived."""
 
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_window import BF, call, check, make
+import window_oracle as wo
+from test_gpu_window import BF, DEV, FP, call, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -30,4 +33,51 @@ def test_bad_pages_beside_nan_are_zeros(sv, q4, D, n):
     assert err == 1
     assert not out[0].isnan().any() and not out[0].any()
     c["host"] = (*c["host"][:5], [0, 300])
+    check(c, out)
+
+
+# The scores of a row are c 2^e with a whole number c for each token, exact in fp32 until the factor log2(e) / sqrt(D) meets
+# them: equal ones have equal weights, and others are 2^20 apart at least, so that the definition's result is the mean of V
+# over the visible tokens with the largest c.
+def exact_scores(rng, D, dtype, q4, level, n, v_scale=1.0):
+    bs, R, H, K = 64, 2, 4, 2
+    c = make(rng, (n, 300), R, H, K, D, bs, dtype, 0, 0, q4)
+    q, k, v, spread, table, ctx = c["host"]
+    sign = np.where(rng.permutation(D) % 2 == 0, 1.0, -1.0)
+    up = level // 2                                                                       # powers of two of q and of K
+    q[...] = sign * 2.0 ** up
+    q[:, :, 1::2] *= -1                                                                   # every other head: the least c
+    count = rng.integers(1, 16, k.shape[:3])
+    unit = 2.0 ** (level - up)
+    c["q"] = torch.from_numpy(q).to(dtype).to(DEV)
+    if q4:
+        codes = np.broadcast_to(np.where(sign > 0, 15, 0), k.shape).astype(int)
+        s = count * unit / 8
+        rows = wo.pack(codes, s, -7.5 * s, dtype)                                         # +-7.5 s, m of 8 bits at most
+        k = wo.unpack(rows, K, D, dtype)[0]
+        assert np.array_equal(np.abs(k), np.broadcast_to(7.5 * s[..., None], k.shape))
+        c["k"] = torch.from_numpy(rows)[:, :, None, :].contiguous().to(DEV)
+        if v_scale != 1.0:
+            rows = c["v"][:, :, 0].cpu().numpy()
+            codes = np.stack([rows[..., : D] % 16, rows[..., : D] // 16], -1).reshape(*rows.shape[:2], K, D).astype(int)
+            _, s, m = wo.unpack(rows, K, D, dtype)
+            rows = wo.pack(codes, wo.round16(s * v_scale, dtype), wo.round16(m * v_scale, dtype), dtype)
+            v, spread, _ = wo.unpack(rows, K, D, dtype)
+            c["v"] = torch.from_numpy(rows)[:, :, None, :].contiguous().to(DEV)
+    else:
+        k = count[..., None] * unit * sign
+        c["k"] = torch.from_numpy(k).to(dtype).to(DEV)
+        assert np.array_equal(c["k"].double().cpu().numpy(), k)
+    c["host"] = (q, k, v, spread, table, ctx)
+    return c
+
+
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+@pytest.mark.parametrize("D,dtype,level", [(64, FP, 16), (128, FP, 16), (128, BF, 16), (256, BF, 15)])
+@pytest.mark.parametrize("n", [9000])
+def test_equal_scores_in_pieces(sv, q4, D, dtype, level, n):
+    """Scores of 2^24 in log2 units, many of them equal: their tokens share the weight equally, in whichever pieces they lie."""
+    c = exact_scores(np.random.default_rng(level + n), D, dtype, q4, level, n)
+    out, err = call(sv, c)
+    assert err == 0
     check(c, out)
