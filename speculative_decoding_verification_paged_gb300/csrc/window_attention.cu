@@ -131,6 +131,7 @@ static int call(bool q4, const void* q, const void* k_cache, const void* v_cache
   p.slots = 0;
   p.fp16 = fp16;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+  p.ref_unit = q4 ? 1.f : p.scale_log2;
   c.stream = reinterpret_cast<cudaStream_t>(stream_);
 
   if (q4) {

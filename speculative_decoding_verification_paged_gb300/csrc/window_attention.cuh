@@ -81,7 +81,7 @@ struct Smem {
   static constexpr int Q = 0;
   static constexpr int P = Q + C::QB * C::Q_BYTES;
   static constexpr int BARS = P + C::NP * C::BANDS * C::P_BYTES;  // 96 mbarriers
-  static constexpr int REF = BARS + 96 * 8;                       // [64] minus the reference of each row
+  static constexpr int REF = BARS + 96 * 8;                       // [64] minus the reference of each row, a score before its scaling
   static constexpr int ALPHA = REF + 256;                         // [64]
   static constexpr int RED = ALPHA + 256;                         // [4][64]
   static constexpr int STAT = RED + 1024;                         // [OB]: [4][64] sums, [64] reference
@@ -535,8 +535,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
 #pragma unroll
             for (int e = 0; e < CW; e += 4) {
               const float4 ref = *reinterpret_cast<const float4*>(s_ref + c0 + e);  // minus the reference
-              const uint64_t z[2] = {fma_f2(pack_f2(x[e], x[e + 1]), scale2, pack_f2(ref.x, ref.y)),
-                                     fma_f2(pack_f2(x[e + 2], x[e + 3]), scale2, pack_f2(ref.z, ref.w))};
+              // subtracted before it is scaled: the rounding of a scaled score is as large as weights are far apart
+              const uint64_t z[2] = {mul_f2(add_f2(pack_f2(x[e], x[e + 1]), pack_f2(ref.x, ref.y)), scale2),
+                                     mul_f2(add_f2(pack_f2(x[e + 2], x[e + 3]), pack_f2(ref.z, ref.w)), scale2)};
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const float2 f = unpack_f2(z[u]);
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             tmem_load_cols<8>(t_s + c, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float m = warp_max(sees(c + e) ? x[e] * p.scale_log2 : -INFINITY);
+              const float m = warp_max(sees(c + e) ? x[e] : -INFINITY);
               if (lane == 0) s_red[q4 * 64 + c0 + c + e] = m;
             }
           }
@@ -573,9 +574,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
           if (gt < CW) {
             const int r = c0 + gt;
             const float m = fmaxf(fmaxf(s_red[r], s_red[64 + r]), fmaxf(s_red[128 + r], s_red[192 + r]));
-            const float old = j == 0 ? kUnseen : -s_ref[r], now = fmaxf(old, m - C::SHIFT);
+            const float old = j == 0 ? kUnseen : -s_ref[r], now = fmaxf(old, m - C::SHIFT / p.scale_log2);
             s_ref[r] = -now;
-            s_alpha[r] = fast_exp2(old - now);
+            s_alpha[r] = fast_exp2((old - now) * p.scale_log2);
           }
           named_sync(bar_group, 128);
           if (j > 0) {

@@ -8,7 +8,7 @@ namespace wattn {
 
 constexpr int kJoinThreads = 128;
 
-// out = sum of W_w opart_w over the pieces w of a unit, in their order, over the sum of W_w = 2^reference_w sum_w; zeros if a
+// out = sum of W_w opart_w over the pieces w of a unit, in their order, over the sum of W_w = 2^(reference_w unit) sum_w; zeros if a
 // piece has no result. References and sums come apart: next to a large reference log2 of a sum has no bits left. A piece
 // without a visible key has sum 0 and holds zeros. D / 4 threads for a row, four head dims each; a block joins some rows, or
 // (`split`) one, whose pieces its groups of threads take in turns.
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     float weight = 0.f;
     if (piece < u.pieces) {
       const float2 x = __ldcg(stat + (int64_t)piece * rows);
-      weight = exp2f(x.x - top) * x.y;
+      weight = exp2f((x.x - top) * p.ref_unit) * x.y;
     }
     sum += weight;
 #pragma unroll 1

@@ -26,7 +26,7 @@ struct Params {
   const int32_t* block_table;
   const int32_t* ctx_lens;
   CutUnit* cut_units;  // [1 + kMaxPieces / 2]
-  float2* stat;        // [pieces][pairs][sub]: reference of a row's weights (log2 units) and their sum; below 0: no result
+  float2* stat;        // [pieces][pairs][sub]: reference of a row's weights and their sum; below 0: no result
   float* opart;        // [pieces][pairs][sub][D], normalised
   int32_t* dev_err;
   int64_t num_blocks, row;  // pages; bytes of a 4-bit token row
@@ -46,6 +46,7 @@ struct Params {
   float task_cost, join_cost, piece_cost;  // what a task's start and end, a join, and a piece of it cost, in tiles
   int fp16;   // type of q and out (4-bit: and of s and m)
   float scale_log2;
+  float ref_unit;  // of the references in stat, in log2 units
 };
 
 // Barriers by their shared-memory address.

@@ -81,3 +81,16 @@ def test_equal_scores_in_pieces(sv, q4, D, dtype, level, n):
     out, err = call(sv, c)
     assert err == 0
     check(c, out)
+
+
+@pytest.mark.parametrize("q4", [False], ids=["16bit"])
+@pytest.mark.parametrize("D,dtype,level", [(64, FP, 18), (128, FP, 22), (256, FP, 24), (128, BF, 18), (64, BF, 22), (128, BF, 25),
+                                           (256, BF, 27), (128, BF, 60), (64, BF, 100)])
+@pytest.mark.parametrize("n", [30, 9000])
+def test_large_scores(sv, q4, D, dtype, level, n):
+    """Scores of 2^22 to 2^110 in log2 units, whole and cut, many of them equal: a finite score, however large, is no NaN,
+    and tokens of equal scores share the weight equally wherever they lie."""
+    c = exact_scores(np.random.default_rng(level + n), D, dtype, q4, level, n)
+    out, err = call(sv, c)
+    assert err == 0
+    check(c, out)
