@@ -142,7 +142,8 @@ __device__ __noinline__ void task_call(const Params& p, const int32_t* prefix, c
 }
 // Queries: fp16 times a power of two that brings a row's largest element to [2^14, 2^15), as operand A of the
 // MMAs. Lane 4 g + t of step s holds rows g and g + 8 of the elements that meet the codes of key g that the lane has
-// (see scores); those 16-fold of odd codes are divided by 16.
+// (see scores); those 16-fold of odd codes are divided by 16. qc: what a row's scores have to be multiplied with, a power of
+// two (the codes' 2^-24 with it), and the sum of its queries divided by that.
 template <class C>
 __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8_t* queries, float* qc) {
   constexpr int D = C::D, ROWS = C::ROWS;
@@ -199,8 +200,8 @@ __device__ __noinline__ void query_call(const Params& p, const Task* task, uint8
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= e & 1 ? f2 : f1;
       if (rr < rows && c == 0) {
-        qc[of_pair * 2 * ROWS + r] = pow2(24 - e2) * p.scale_log2;
-        qc[of_pair * 2 * ROWS + ROWS + r] = sum * p.scale_log2;
+        qc[of_pair * 2 * ROWS + r] = pow2(24 - e2);
+        qc[of_pair * 2 * ROWS + ROWS + r] = sum * pow2(e2 - 24);
       }
       // word c of the row is word `at` of lane `of`'s codes, and the operands of two steps
       constexpr int WORDS = D / 32 < 4 ? D / 32 : 4;  // words of a lane in a row of up to 64 bytes
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
     // ---- state of this lane's rows: g + 8 u of tile mt
     const int r0 = k.r0 + part * p.sub, nr = kv_head < p.kv_heads ? min(p.sub, k.r0 + k.nr - r0) : 0;
     float o[MT][C::TILES][4], extra[MT][4];  // extra: what the products have too much
-    float sum[MT][2], offset[MT][2], nref[MT][2], fc[MT][2], fd[MT][2];  // nref: minus the reference; factors of the scores
+    float sum[MT][2], offset[MT][2], nref[MT][2], fc[MT][2], fd[MT][2];  // nref: minus the reference; fc, fd: see query_call
     int pos[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             const int tok = token(lane & 15);
             if (!(tok <= high_pos && (p.window == 0 || tok < p.sinks || tok > low_pos - p.window))) x = make_float2(0.f, 0.f);
           }
+          if (lane < 16) x.x *= p.scale_log2, x.y *= p.scale_log2;
           if (lane >= 16) x.y = fmaf(8.f, x.x, x.y);  // the codes of V are taken from 8
           if (lane >= 24) x.x = -x.x;                 // and the last 8 keys' weights are negative (see the product)
           float* to_par = par + ((lane & 15) >> 1) * 8 + (lane >> 4) * 4 + (lane & 1);
@@ -496,8 +498,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                uint64_t z = fma_f2(km, pack_f2(fd[mt][u], fd[mt][u]), pack_f2(nref[mt][u], nref[mt][u]));
-                z = fma_f2(ks, mul_f2(pack_f2(s[mt][n8][2 * u], s[mt][n8][2 * u + 1]), pack_f2(fc[mt][u], fc[mt][u])), z);
+                // the score, and its distance to the reference: a power of two as the factor leaves one rounding, which is
+                // zero at the score that the reference was made of
+                uint64_t z = mul_f2(km, pack_f2(fd[mt][u], fd[mt][u]));
+                z = fma_f2(ks, pack_f2(s[mt][n8][2 * u], s[mt][n8][2 * u + 1]), z);
+                z = fma_f2(z, pack_f2(fc[mt][u], fc[mt][u]), pack_f2(nref[mt][u], nref[mt][u]));
                 float2 f = unpack_f2(z), w;
                 f.x = fast_exp2(f.x);
                 f.y = fast_exp2(f.y);
@@ -538,7 +543,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
             if (settled || !__any_sync(0xffffffffu, grow)) break;
           }
           // new references: 2^SHIFT below the largest weight times s of each row, if that is higher; what was summed so far
-          // is scaled down
+          // is scaled down. A score of 2^27 or more has no bits for that: its weight is 1, times s as it is.
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -549,13 +554,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) q4_attention_kernel(c
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const float* of = par_at + n8 * 32 + e;
-                  const float z = fmaf(of[0], s[mt][n8][2 * u + e] * fc[mt][u], of[2] * fd[mt][u]) +
-                                  log2f(fmaxf(fabsf(of[4]), C::TINY));
-                  if (whole || sees(pos[mt][u], token(n8 * 8 + 2 * t4 + e))) m = fmaxf(m, z);
+                  const float z = __fmul_rn(fmaf(of[0], s[mt][n8][2 * u + e], __fmul_rn(of[2], fd[mt][u])), fc[mt][u]);
+                  const float ref = fabsf(z) < 0x1p27f ? z + (log2f(fmaxf(fabsf(of[4]), C::TINY)) - C::SHIFT) : z;
+                  if (whole || sees(pos[mt][u], token(n8 * 8 + 2 * t4 + e))) m = fmaxf(m, ref);
                 }
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-              const float old = -nref[mt][u], now = fmaxf(old, m - C::SHIFT), alpha = fast_exp2(old - now);
+              const float old = -nref[mt][u], now = fmaxf(old, m), alpha = fast_exp2(old - now);
               nref[mt][u] = -now;
               sum[mt][u] *= alpha;
               offset[mt][u] *= alpha;

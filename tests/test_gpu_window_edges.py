@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import window_oracle as wo
-from test_gpu_window import BF, DEV, FP, call, check, make
+from test_gpu_window import BF, DEV, FP, call, check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -83,7 +83,7 @@ def test_equal_scores_in_pieces(sv, q4, D, dtype, level, n):
     check(c, out)
 
 
-@pytest.mark.parametrize("q4", [False], ids=["16bit"])
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
 @pytest.mark.parametrize("D,dtype,level", [(64, FP, 18), (128, FP, 22), (256, FP, 24), (128, BF, 18), (64, BF, 22), (128, BF, 25),
                                            (256, BF, 27), (128, BF, 60), (64, BF, 100)])
 @pytest.mark.parametrize("n", [30, 9000])
@@ -94,3 +94,33 @@ def test_large_scores(sv, q4, D, dtype, level, n):
     out, err = call(sv, c)
     assert err == 0
     check(c, out)
+
+
+def test_large_scores_and_small_values(sv):
+    """V of a 4-bit cache far below 1 under scores of 2^26 to 2^33: the reference, which is a sum of the score and log2 s,
+    has no bits for the latter."""
+    for level in (18, 20, 21, 22, 23, 25):
+        c = exact_scores(np.random.default_rng(level), 128, BF, True, level, 700, 2.0 ** -10)
+        out, err = call(sv, c)
+        assert err == 0
+        check(c, out)
+
+
+def test_q4_rows_whose_scores_are_all_minus_infinity(sv):
+    """NaN, in one piece and in many, as over a 16-bit cache; the other kv head's rows are as ever."""
+    for n in (30, 9000):
+        c = make(np.random.default_rng(n), (n, 300), 2, 4, 2, 64, 64, BF, 0, 0, True)
+        q, k, v, spread, table, ctx = c["host"]
+        q[...] = np.abs(q) + 0.5
+        c["q"] = torch.from_numpy(q).to(BF).to(DEV)
+        pages = torch.as_tensor(table[0, : -(-n // 64)]).long().to(DEV)
+        low = torch.tensor([0x80, 0xff], dtype=torch.uint8, device=DEV)                   # -inf
+        c["k"][pages, :, 0, 64 + 4 + 2: 64 + 4 + 4] = low                                 # m of kv head 1
+        out, err = call(sv, c)
+        assert err == 0 and out[0, :, 2:].isnan().all()
+        got = out.double().cpu().numpy()
+        q = c["q"].double().cpu().numpy()
+        c["host"] = (q, np.nan_to_num(k), np.nan_to_num(v), spread, table, ctx)
+        for b, heads in ((0, slice(0, 2)), (1, slice(0, 4))):
+            ref, tol = reference(c, b)
+            assert np.all(np.abs(got[b] - ref)[:, heads] <= tol[:, heads])
