@@ -754,7 +754,9 @@ int spec_cache_load_q4(const void* k_cache, const void* v_cache, const int32_t* 
  * largest lose bits; a row with an element of 2^115 or more may come out as NaN), the
  * weights times s as fp16 times a power of two of the row. Where a row's largest score is
  * 2^27 or more (times log2 e), that power is set without regard to s: tokens of V with an
- * s below 2^-14 lose bits, and one above 2^15 counts as that.
+ * s below 2^-14 lose bits, and one above 2^15 counts as that. At all scores,
+ * tokens of V with an s below 2^-60 lose bits, and elements of V of 2^40 or more may come
+ * out as infinities or NaN.
  */
 int spec_q4_attention(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_table, const int32_t* ctx_lens, int32_t num_rows,

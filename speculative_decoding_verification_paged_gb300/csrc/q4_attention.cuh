@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr int Q_BYTES = MT * STEPS * 512;     // of a kv head's rows
   static constexpr int STATE = MT * (TILES * 4 + 6);   // registers of a lane that the join of splits hands over
   // Weights are 2^SHIFT at the largest of the keys that set a row's reference, TOP at most.
-  static constexpr float SHIFT = 7.f, TOP = 32768.f, TINY = 0x1p-60f;
+  static constexpr float SHIFT = 7.f, TOP = 32768.f, TINY = 0x1p-40f;
 };
 
 // Shared memory behind the ring, in order.

@@ -106,6 +106,19 @@ def test_large_scores_and_small_values(sv):
         check(c, out)
 
 
+def test_large_equal_values(sv):
+    """Tokens of which all V elements are equal (s = 0), and large: 2^60 in a 4-bit cache."""
+    for n in (30, 300, 9000):
+        c = make(np.random.default_rng(n), (n, 40), 2, 8, 2, 128, 64, BF, 0, 0, True)
+        q, k, v, spread, table, ctx = c["host"]
+        rows = wo.pack(np.zeros(v.shape, int), np.zeros(v.shape[:3]), np.full(v.shape[:3], 2.0 ** 60), BF)
+        c["v"] = torch.from_numpy(rows)[:, :, None, :].contiguous().to(DEV)
+        c["host"] = (q, k, wo.unpack(rows, 2, 128, BF)[0], np.zeros(spread.shape), table, ctx)
+        out, err = call(sv, c)
+        assert err == 0
+        check(c, out)
+
+
 def test_q4_rows_whose_scores_are_all_minus_infinity(sv):
     """NaN, in one piece and in many, as over a 16-bit cache; the other kv head's rows are as ever."""
     for n in (30, 9000):
