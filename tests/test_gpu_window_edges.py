@@ -1,5 +1,5 @@
 """Windowed and 4-bit attention at the edges of what the header allows: bad pages beside values that are no numbers, scores
-far past fp32's resolution of a power of two.
+far past fp32's resolution of a power of two, tasks in a row with single buffers.
 
 Tolerances are those of test_gpu_window where no other is derived."""
 
@@ -137,3 +137,39 @@ def test_q4_rows_whose_scores_are_all_minus_infinity(sv):
         for b, heads in ((0, slice(0, 2)), (1, slice(0, 4))):
             ref, tol = reference(c, b)
             assert np.all(np.abs(got[b] - ref)[:, heads] <= tol[:, heads])
+
+
+# head dim 256 and 33 to 64 packed rows have one buffer of queries, accumulators and weights: several tasks a block, some cut
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("R,H,K,D", [(16, 8, 2, 256), (12, 6, 2, 256), (16, 16, 4, 128), (8, 8, 2, 64)])
+def test_many_tasks_of_many_rows(sv, q4, dtype, R, H, K, D):
+    rng = np.random.default_rng(R + H + D)
+    ctx = [int(x) for x in rng.integers(R, 150, 330)]
+    ctx[3], ctx[77], ctx[200] = 0, 0, 2500
+    c = make(rng, ctx, R, H, K, D, 16, dtype, 0, 0, q4)
+    out, err = call(sv, c)
+    assert err == 0
+    assert torch.isfinite(out.float()).all() and not out[3].any() and not out[77].any()
+    pick = sorted({3, 200, 329, *range(0, 330, 11)})
+    some = dict(c, host=(c["host"][0][pick], *c["host"][1:4], c["host"][4][pick], [ctx[b] for b in pick]))
+    check(some, out[pick])
+    again, _ = call(sv, c)
+    assert torch.equal(out, again)
+    # each alone gives what it gives among the others, but for the cuts: within both tolerances
+    for b in (0, 200, 329):
+        one = dict(c, q=c["q"][b: b + 1].contiguous(), table=c["table"][b: b + 1].contiguous(), ctx=c["ctx"][b: b + 1].contiguous(),
+                   host=(c["host"][0][b: b + 1], *c["host"][1:4], c["host"][4][b: b + 1], [ctx[b]]))
+        alone, err = call(sv, one)
+        assert err == 0
+        check(one, alone)
+
+
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+def test_every_row_of_the_largest_batch(sv, q4):
+    rng = np.random.default_rng(21)
+    ctx = [int(x) for x in rng.integers(0, 20, 4096)]
+    c = make(rng, ctx, 1, 2, 1, 256, 16, BF, 5, 1, q4)
+    out, err = call(sv, c)
+    assert err == 0
+    check(c, out)
