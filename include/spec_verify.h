@@ -662,9 +662,10 @@ int spec_cache_update(int32_t* block_table, int32_t* page_refs, const int32_t* c
  *  ctx_lens    [B] int32, tokens in the cache, the rows' own included: 0 (an empty
  *              row of a padded batch: out rows of zeros, no error), or in
  *              [num_rows, max_blocks_per_seq * bs]
- *  out         [B, num_rows, Hq, D] of type `dtype`. The softmax weights are rounded
- *              once to 16 bits before they meet V (an error of up to half a step of
- *              sum p |v|, beside the output's own rounding).
+ *  out         [B, num_rows, Hq, D] of type `dtype`. Before they meet V the softmax
+ *              weights p are rounded to two 16-bit numbers each (an error of 2^-16
+ *              sum p |v| at most, beside the output's own rounding); bf16 ones at head
+ *              dim 64, or where num_rows * G > 32, to one (2^-8 sum p |v|)
  *  workspace   >= spec_window_attention_workspace(d, num_rows) bytes, 256-byte
  *              aligned, its first SPEC_ATTN_COUNTER_BYTES bytes ZERO-FILLED before
  *              its first use; one workspace serves every attention call of any

@@ -44,9 +44,12 @@ struct Cfg {
   static constexpr int NG = ROWS <= 16 ? 1 : ROWS / 16;  // softmax warpgroups, CW rows each
   static constexpr int CW = ROWS / NG;
   static constexpr int HALVES = D == 256 ? 2 : 1;  // O^T accumulators of 128 lanes
-  // An fp16 weight keeps its bits between 2^15 and 2^-14 only: two bands of weights, the lower one times 2^18, with
-  // an accumulator each, cover 2^15 to 2^-32.
-  static constexpr int BANDS = FP16 ? 2 : 1;
+  // Weights are two 16-bit numbers, the second one what the first has left, with an accumulator each: 22 bits in fp16 (down
+  // to 2^-26, times 2^12 so that it is no subnormal; 2^-37 is the least step), 16 in bf16. With bf16 only where HBM hides the
+  // second product: 32 sequences of head dim 128 with a window of 4096 tokens 103 us with one and two on 16 rows, 108 and 111
+  // on 32, but 119 and 162 on 64, and 65 and 73 on 16 rows of head dim 64; 64 ragged ones of head dim 256, 24 rows, 114 and 115.
+  static constexpr int BANDS = FP16 || (D >= 128 && ROWS <= 32) ? 2 : 1;
+  static constexpr float LOW = FP16 ? 0x1p12f : 1.f;
   static constexpr int QB = D == 256 && N == 64 ? 1 : 2;           // query buffers
   static constexpr int NP = D == 256 && N == 64 && BANDS == 2 ? 1 : 2;  // P buffers
   static constexpr int O_COLS = BANDS * HALVES * N;
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
               float low[8];
               tmem_load_cols<8>(o + (C::HALVES + hh) * N + c, low);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = fmaf(low[e], 0x1p-18f, v[e]);
+              for (int e = 0; e < 8; ++e) v[e] = fmaf(low[e], 1.f / C::LOW, v[e]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= e_fac[c + e];
@@ -620,19 +623,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
             }
           }
         }
-        // ---- sums, and the weights in 16 bits
+        // ---- sums, and the weights in 16 bits, or twice that
         uint32_t hi[CW / 2], lo[C::BANDS == 2 ? CW / 2 : 1];
 #pragma unroll
         for (int e = 0; e < CW / 2; ++e) l[e] = add_f2(l[e], y[e]);
 #pragma unroll
         for (int e = 0; e < CW / 2; ++e) {
           const float2 w = unpack_f2(y[e]);
+          hi[e] = q4::pack2<C::FP16>(w.x, w.y);
           if constexpr (C::BANDS == 2) {
-            const float a = w.x >= 0.0625f ? w.x : 0.f, b = w.y >= 0.0625f ? w.y : 0.f;
-            hi[e] = q4::pack2<true>(a, b);
-            lo[e] = q4::pack2<true>((w.x - a) * 0x1p18f, (w.y - b) * 0x1p18f);
-          } else {
-            hi[e] = q4::pack2<C::FP16>(w.x, w.y);
+            const float2 a = q4::unpack2<C::FP16>(hi[e]);
+            lo[e] = q4::pack2<C::FP16>((w.x - a.x) * C::LOW, (w.y - a.y) * C::LOW);
           }
         }
         wait(pv_done + 8 * (i % C::NP), i / C::NP - 1);  // the buffer's last product is done

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import window_oracle as wo
-from test_gpu_window import BF, DEV, FP, call, check, make, reference
+from test_gpu_window import BF, DEV, FP, HALF, call, check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +173,23 @@ def test_every_row_of_the_largest_batch(sv, q4):
     out, err = call(sv, c)
     assert err == 0
     check(c, out)
+
+
+@pytest.mark.parametrize("dtype,D,R,H,K", [(BF, 128, 4, 32, 8), (BF, 128, 8, 16, 4), (BF, 256, 4, 24, 4), (BF, 256, 1, 8, 8),
+                                           (FP, 64, 3, 8, 2), (FP, 128, 4, 32, 8), (FP, 128, 16, 16, 4), (FP, 256, 16, 8, 2)])
+def test_weights_of_two_numbers(sv, dtype, D, R, H, K):
+    """Where the weights are two 16-bit numbers they add 2^-16 of S at most, (2^-8)^2 in bf16, to the 2^-16 of fp32 scores,
+    exponentials and sums (fp16: 2^-22, and a least step of 2^-37 next to weights of 2^7 or more); the rest is the rounding of
+    the result."""
+    c = make(np.random.default_rng(D + R), (R + 20, 700, 2100), R, H, K, D, 64, dtype, 600, 4, False)
+    out, err = call(sv, c)
+    assert err == 0
+    q, k, v, _, table, ctx = c["host"]
+    got = out.double().cpu().numpy()
+    for b, n in enumerate(ctx):
+        t = np.arange(n)
+        page = np.where(wo.sees(n, R, 600, 4).any(0), table[b, t // 64], 0)
+        ref, S, _, _ = wo.attention(q[b], k[page, t % 64], v[page, t % 64], 600, 4)
+        tol = 2.0 ** -15 * S + HALF[dtype] * np.abs(ref) + torch.finfo(dtype).smallest_normal
+        bad = np.abs(got[b] - ref) > tol
+        assert not bad.any(), (b, int(bad.sum()), (np.abs(got[b] - ref) / S).max())
