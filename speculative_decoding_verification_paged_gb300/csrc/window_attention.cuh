@@ -18,7 +18,6 @@
 #include <cuda.h>
 
 #include "attention_tc.cuh"
-#include "tree_attention.cuh"
 #include "window_plan.cuh"
 
 namespace specv {
@@ -28,7 +27,6 @@ using attn::tc::reduce_cols;
 using attn::tc::reduced_col;
 using attn::tc::tmem_load_cols;
 using attn::tc::tmem_store_cols;
-using tattn::umma_commit_elect;
 
 constexpr int TK = 128;            // keys per tile (MMA M)
 constexpr int kMaxSlots = 16;      // K and V tiles in shared memory
@@ -164,9 +162,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) window_attention_kernel(const 
                                                                           const __grid_constant__ CUtensorMap tm_v) {
   constexpr int D = C::D, N = C::N, CW = C::CW;
   using S = Smem<C>;
+  // The products' MMA has 128 head dims. Of tiles with 64 it takes the other 64 lanes, which no one reads, from what lies
+  // behind the tile: the next slot, or for the last one the area behind the ring.
+  static_assert(D >= 128 || S::PREFIX >= C::SLOT, "the MMA stays inside the block's shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // 16-bit: KS slots for K, the others for V, so that a barrier's phases are all waited for by one warp, in turn (the
+  // KS slots for K, the others for V, so that a barrier's phases are all waited for by one warp, in turn (the
   // parity of a phase says nothing to a warp that has not seen the phase before)
   const int NS = p.slots, KS = NS - NS / 2;
   uint8_t* ring = smem;
