@@ -43,7 +43,7 @@ static int settings_of(int batch, Launch* l) {
 }
 template <class C>
 static int launch_of(const Launch& l, Call c) {
-  c.p.cuts = may_cut(c.p, C::KEYS, C::TILE_US);
+  c.p.cuts = may_cut(c.p, C::KEYS, C::TILE_US, 9.f);
   c.p.task_cost = C::TASK_COST;
   c.p.join_cost = C::JOIN_COST;
   c.p.piece_cost = C::PIECE_COST;

@@ -105,7 +105,7 @@ static int launch_join(const Params& p, int max_pieces, cudaStream_t stream) {
   // One row a block where few units are cut, and so into many pieces; else a block has a row for each group. Over 4 bits, 128
   // rows a unit: one sequence of 8192 tokens 29 us, 36 with a row a group; two 32 and 38, four 35 and 37, eight of 2048 tokens
   // 31 both, 16 of them 37 and 35. 16 bits, 128 rows a sequence: four of 8192 tokens 39 both, eight of 4096 tokens 41 and 39.
-  const int split = (int64_t)lists * rows <= 600 ? 1 : 0;
+  const int split = (int64_t)lists * rows <= 1000 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)lists, (unsigned)(split ? rows : (rows + groups - 1) / groups));
   cfg.blockDim = dim3(kJoinThreads);

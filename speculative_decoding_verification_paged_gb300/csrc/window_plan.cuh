@@ -150,15 +150,15 @@ __device__ __forceinline__ Task task_at(const Params& p, const int32_t* prefix, 
 }
 
 // Whether a unit can be so long, in tiles that take `tile_us`, that cutting it pays: where not, the join's launch is left out
-// with the cuts. At 9 us' worth of tiles the two are even (8 kv heads of 128, one row: one sequence of 512 tokens, 6 us, 13 us
-// whole and 16 with cuts, of 1024 tokens 17 both; 20 sequences of 768 tokens 27 and 28; over 4 bits, one of 64 tokens 15 and
-// 18, of 128 tokens 19 and 18, of 256 tokens 25 and 17).
-static inline bool may_cut(const Params& p, int keys, float tile_us) {
+// with the cuts. `even_us` of tiles are even: 9 over 16 bits (8 kv heads of 128, one row: one sequence of 512 tokens, 6 us, 13
+// us whole and 16 with cuts, of 1024 tokens 17 both; 20 sequences of 768 tokens 27 and 28), 6 over 4 bits, where tiles are
+// shorter (one of 64 tokens, 5 us, 15 and 18, of 96 tokens 19 both, of 128 tokens 19 and 18, of 256 tokens 25 and 17).
+static inline bool may_cut(const Params& p, int keys, float tile_us, float even_us) {
   const int64_t page = int64_t(1) << p.page_shift, table = (int64_t)p.max_blocks << p.page_shift;
   int64_t tokens = table;
   if (p.window != 0) tokens = (p.sinks + page - 1) / page * page + ((int64_t)p.window + p.rows + 2 * page) / page * page;
   if (tokens > table) tokens = table;
-  return (float)((tokens + keys - 1) / keys) * tile_us > 9.f;
+  return (float)((tokens + keys - 1) / keys) * tile_us > even_us;
 }
 
 // Length of the pieces. A block does ceil(tasks / blocks) tasks, one after the other; a task costs its tiles and
