@@ -8,12 +8,12 @@
 // every access of a warp is a run of consecutive bytes; the D / 8 lanes of a head find
 // its range by shuffles, least and negated greatest in the halves of one word.
 //
-// A load comes to 81 to 90% of the copy rate: 65,536 tokens of 8 heads of 128 in 56 to 62 us,
-// 340 MB. A store is bound by instructions, 450 a warp before the last step for 256 elements
-// of K and of V (73% of the issue slots used, 26% of the HBM rate): 65,536 tokens in 115 us,
-// 53 us' worth of reads and writes. Each element rounded by floor and an exact comparison took
-// 1.6 times as long. Small calls are launches: 10 us with the host's work for 512 tokens,
-// 2 to 3 in a graph.
+// A load comes to 81% of the copy rate: 65,536 tokens of 8 heads of 128, 340 MB, in 62 us (56
+// among other calls, whose starts and ends overlap). A store is bound by instructions, 423 a warp
+// for 256 elements of K and of V, 72% of the issue slots used: the same 340 MB, 50 us' worth at
+// the copy rate, in 127 us (115 among others). fp32 results are 608 MB in 136 us.
+// Each element rounded by floor and an exact comparison took 1.6 times as long. Small calls are
+// launches: 10 us with the host's work for 512 tokens, 2 to 3 in a graph.
 //
 // The code is the exact rounding of the quotient: see codes_of.
 #include "launch_memo.h"
@@ -310,8 +310,8 @@ static void launch_store(const Params& p, bool fp16, cudaStream_t stream) {
 }
 template <int D, bool FP16, bool F32>
 static void launch_load_as(const Params& p, cudaStream_t stream) {
-  // Four tokens a thread keep more loads on their way (65,536 tokens of 8 heads of 128: 66 us, 70 with one); a call too small
-  // to fill the GPU that way is better off with one.
+  // Four tokens a thread keep more loads on their way; a call too small to fill the GPU that way is better off with one. 65,536
+  // tokens of 8 heads of 128 take 62 us, 66 with one a thread; 32,768 (4 M chunks) 35 both, 24,576 29 and 27.
   const uint32_t groups = p.chunks >= 4u << 20 ? (p.tokens + 3) / 4 : p.tokens;
   if (groups < p.tokens) cache_load_q4_kernel<D, FP16, F32, 4><<<blocks_for(p, groups), kThreads, 0, stream>>>(p, groups);
   else cache_load_q4_kernel<D, FP16, F32, 1><<<blocks_for(p, groups), kThreads, 0, stream>>>(p, groups);

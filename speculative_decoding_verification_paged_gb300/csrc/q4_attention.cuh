@@ -18,17 +18,20 @@
 // memory, unpacked, and every step between unpacking, MMAs and softmax is a barrier that
 // warps wait at. A kernel of that kind (K as e4m3 against queries in parts, V transposed by
 // ldmatrix, unpacked into tensor memory, two softmax streams) took 228 us on 32 sequences of
-// 16384 tokens, 8 kv heads of 128, 16 rows, where this one takes 167; 755 us with 64 rows
-// over 655,000 tokens, here 700; 225 us for 4 heads of 256 and 24 rows, here 228.
+// 16384 tokens, 8 kv heads of 128, 16 rows, where this one takes 169; 755 us with 64 rows
+// over 655,000 tokens, here 721; 225 us for 4 heads of 256 and 24 rows, here 226: the choice
+// is won on up to 16 rows, and even on more. (All of these are single calls between events
+// with L2 flushed, on the same inputs.)
 //
-// What bounds it: 372 instructions for 16 keys, a head and 16 rows (33 of them mma), 71% of
-// the issue slots used: 84 us' worth of HBM reads in 167. With 32 rows or head dim 256 the
-// accumulators leave room for eight warps an SM, which wait for one another's results 1.7
-// of 5.1 cycles an instruction. Interleaving the next tile's scores with this one's product
-// was slower (174 us for 167), as were 16 rows a warp for 64 (778 for 709) and two warps for
-// a head's rows, which exchange weights and share the head dims (224 us for 228 at head dim
-// 256, 916 for 708 with 64 rows). 17 to 32 rows go two MMA tiles to a warp, which unpack once
-// for both (374 us for 411 in two units).
+// What bounds it: 372 instructions for 16 keys, a head and 16 rows (33 of them mma), 57% of
+// the issue slots used, start and end included: 84 us' worth of HBM reads in 169. With 32
+// rows or head dim 256 the accumulators leave room for eight warps an SM, which issue in 41%
+// of the slots and wait for their results 1.7 cycles an instruction. Each against this kernel
+// as it was then: interleaving the next tile's scores with this one's product was slower (174
+// us for 167), as were 16 rows a warp for 64 (778 for 709) and two warps for a head's rows,
+// which exchange weights and share the head dims (224 us for 228 at head dim 256, 916 for 708
+// with 64 rows). 17 to 32 rows go two MMA tiles to a warp, which unpack once for both (374 us
+// for 411 in two units).
 #pragma once
 
 #include <type_traits>

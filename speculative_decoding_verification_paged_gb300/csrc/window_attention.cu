@@ -6,12 +6,14 @@
 // A 4-bit cache holds codes n with a scale s and a minimum m for each token and
 // head: s_it = (s_t n_t . q_i + m_t sum(q_i)) / sqrt(D), and the same for V.
 //
-// A unit is one sequence, one kv head (4-bit: up to eight, whose codes share a token
-// row) and up to 64 of its packed rows (query row x head of the group): its K and V
-// are read once for all of them. Pages that no row sees are not read; pages of the
-// sinks and of the window form one list. The device plans the call from ctx_lens
-// (window_plan.cuh): units go to the blocks in turns, and are cut where that shortens
-// the longest block's work; a kernel of its own joins cut units (window_join.cuh).
+// A unit is some packed rows (query row x head of the group) of one sequence and kv
+// head, for all of which K and V are read once: over 16 bits up to 64 rows; over 4 bits
+// eight warps' worth, each with 16 or 32 rows of a head (up to eight heads, whose codes
+// share a token row). More rows are more units, which read K and V again. Pages that no
+// row sees are not read; pages of the sinks and of the window form one list. The device
+// plans the call from ctx_lens (window_plan.cuh): units go to the blocks in turns, and are
+// cut where that shortens the longest block's work; a kernel of its own joins cut units
+// (window_join.cuh).
 //
 // Softmax in one pass: a row's weights are 2^(score - reference). The reference is set
 // 2^7 below the largest weight of the first keys, and again only when a later weight
@@ -19,8 +21,8 @@
 //
 // 16 bits (window_attention.cuh): bound by HBM, K and V by tensor copies into tcgen05.
 // 32 sequences with a window of 4096 tokens, 8 kv heads of 128, 16 packed rows: 548 MB
-// in 90 to 103 us, 78 to 89% of the copy rate; 64 ragged sequences, 4 heads of 256, 24
-// rows: 539 MB in 104 to 114 us.
+// in 105 us between events with L2 flushed, 91 among other calls, 77 to 88% of the copy
+// rate; 64 ragged sequences, 4 heads of 256, 24 rows: 539 MB in 115 us, 109 among others.
 //
 // 4 bits (q4_attention.cuh): bound by instructions, since a byte holds four times the
 // work: unpacking, and mma with 16 rows a time.

@@ -10,9 +10,12 @@
 // the last one's weights are made.
 //
 // What bounds it: HBM for long units (24 rows of head dim 256 over whole contexts of 1024 to
-// 16384 tokens: 92% of the copy rate); under a window the units' starts and ends, 20 to 25 us
-// a call. Hot loops of all roles together have to fit the SM's instruction cache: unrolled by
-// hand and in full, they were three times slower.
+// 16384 tokens: 90% of the copy rate); under a window the units' starts and ends, 20 to 25 us
+// a call; with 64 packed rows the softmax and, in fp16, the second product (32 sequences with a
+// window of 4096 tokens, 8 heads of 128: bf16 121 us, fp16 162, 82 us' worth of bytes); at head
+// dim 64 the MMAs, half of whose lanes are dropped (the same with 16 rows: 65 us, 40 us' worth).
+// Hot loops of all roles together have to fit the SM's instruction cache: unrolled by hand and
+// in full, they were three times slower.
 #pragma once
 
 #include <cuda.h>

@@ -10,7 +10,7 @@ namespace specv {
 namespace wattn {
 
 constexpr int kMaxBatch = 4096;
-constexpr int kMaxRows = 64;       // packed query rows of a unit
+constexpr int kMaxRows = 64;       // packed query rows of a unit over 16 bits, and query heads of a kv head
 constexpr int kMaxPieces = 768;    // pieces of cut units in a call, at most
 constexpr int kCandidates = 32;
 constexpr int kCutBytes = (1 + kMaxPieces / 2) * 24 + 255 & ~255;  // of the list of cut units
